@@ -20,6 +20,8 @@ Functions keep the C names:
 * ``arx_ext_*``: the external-writer form -- a host thread writes each
   rank's partial into page-locked slots and raises its flag, the GPU waits
   for the flags and reduces.
+* ``arx_linear / arx_dropout_add / arx_layer_norm``, their ``_bwd`` forms and
+  ``arx_reduce_layer_norm``: the operators around a sublayer's all-reduce.
 """
 
 from __future__ import annotations
@@ -27,6 +29,8 @@ from __future__ import annotations
 import ctypes
 import os
 from typing import Sequence
+
+from . import _ops
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libarx.so")
@@ -145,6 +149,7 @@ def _load() -> ctypes.CDLL:
         "arx_ext_step": ([extp, vp, sz, vp], i32),
         "arx_ext_query": ([extp, u32p, u32p, vp], i32),
         "arx_ext_reset": ([extp, vp], i32),
+        **_ops.SIGNATURES,
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -577,6 +582,8 @@ def arx_ext_reset(x: arx_ext, stream=None) -> None:
     _check(lib.arx_ext_reset(ctypes.byref(x), _stream(stream)))
 
 
+from ._ops import *  # noqa: E402,F403
+
 __all__ = [
     "ArxError", "arx_ctx", "lib", "arx_status_string", "arx_last_error", "arx_reduce", "arx_reduce_plan",
     "arx_step_plan",
@@ -587,4 +594,5 @@ __all__ = [
     "arx_ext", "arx_ext_region_bytes", "arx_ext_words_bytes", "arx_ext_init", "arx_ext_set_timeout",
     "arx_ext_wait_free", "arx_ext_slot", "arx_ext_publish", "arx_ext_post", "arx_ext_publish_all",
     "arx_ext_step", "arx_ext_query", "arx_ext_reset",
+    *_ops.__all__,
 ]

@@ -1,0 +1,442 @@
+"""Binding of the operators around the reduce (``include/arx.h``, "The operators
+around a sublayer's all-reduce"): matrix product with its epilogue, dropout
+with bias and residual, layer norm, and the fused end of a sublayer.
+
+Every operator has two forms: a function that checks its tensors and makes one
+C call, and a plan (``arx_layer_norm_plan`` and so on) that checks them once
+and makes the same C call each time it is called, for eager callers that
+repeat it.  A plan keeps its tensors alive; their contents may change between
+calls, their storage must not.
+
+Matrices are tensors of two or more dimensions whose last one is contiguous
+and whose leading ones collapse into one row stride; vectors are contiguous.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+ARX_BF16, ARX_F16, ARX_F32 = range(3)
+ARX_ACT_NONE, ARX_ACT_RELU, ARX_ACT_GELU, ARX_ACT_GELU_TANH, ARX_ACT_SILU = range(5)
+
+_vp, _u64, _i32, _f32, _f64 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int32, ctypes.c_float, ctypes.c_double
+
+
+def _struct(name, *fields):
+    """Mirror of a struct of include/arx.h: (type, names) pairs in order."""
+    flat = [(n, t) for t, names in fields for n in names.split()]
+    return type(name, (ctypes.Structure,), {"_fields_": flat, "__doc__": f"Mirror of ``struct {name}`` in include/arx.h."})
+
+
+arx_layer_norm_args = _struct(
+    "arx_layer_norm_args", (_vp, "x weight bias y mean rstd"), (_u64, "rows cols ldx ldy"), (_f32, "eps"),
+    (_i32, "dtype wdtype reserved"))
+arx_layer_norm_bwd_args = _struct(
+    "arx_layer_norm_bwd_args", (_vp, "dy x mean rstd weight dresidual dx dweight dbias workspace"),
+    (_u64, "workspace_bytes rows cols lddy ldx lddresidual lddx"), (_i32, "dtype wdtype"))
+arx_dropout_add_args = _struct(
+    "arx_dropout_add_args", (_vp, "x bias residual out rng"), (_u64, "rows cols ldx ldresidual ldout"), (_f64, "p"),
+    (_i32, "dtype wdtype"))
+arx_dropout_add_bwd_args = _struct(
+    "arx_dropout_add_bwd_args", (_vp, "dout dx dbias rng workspace"), (_u64, "workspace_bytes rows cols lddout lddx"),
+    (_f64, "p"), (_i32, "dtype wdtype"))
+arx_reduce_layer_norm_args = _struct(
+    "arx_reduce_layer_norm_args", (_vp, "slots bias residual weight norm_bias h y mean rstd rng"), (_u64, "rows cols"),
+    (_f64, "p"), (_f32, "eps"), (_i32, "W"))
+arx_linear_args = _struct(
+    "arx_linear_args", (_vp, "x w bias residual out z status"), (_u64, "M N K ldx ldw ldresidual ldout ldz"),
+    (_i32, "act dtype wdtype reserved"))
+arx_linear_bwd_args = _struct(
+    "arx_linear_bwd_args", (_vp, "dout z x w dx dw dbias workspace"), (_u64, "workspace_bytes"), (_vp, "status"),
+    (_u64, "M N K lddout ldz ldx ldw lddx lddw"), (_i32, "act dtype wdtype reserved"))
+
+SIGNATURES = {
+    **{f"arx_{op}": ([ctypes.POINTER(t), _vp], ctypes.c_int) for op, t in (
+        ("layer_norm", arx_layer_norm_args), ("layer_norm_bwd", arx_layer_norm_bwd_args),
+        ("dropout_add", arx_dropout_add_args), ("dropout_add_bwd", arx_dropout_add_bwd_args),
+        ("reduce_layer_norm", arx_reduce_layer_norm_args), ("linear", arx_linear_args),
+        ("linear_bwd", arx_linear_bwd_args))},
+    **{f"arx_{op}_workspace_bytes": ([_u64, _u64], ctypes.c_size_t)
+       for op in ("layer_norm_bwd", "dropout_add_bwd", "linear_bwd")},
+}
+
+
+def _core():
+    import deterministic_shot_all_gb300 as core
+    return core
+
+
+_DTYPES: dict = {}
+
+
+def _dtype(t, name, allowed):
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: ARX_BF16, torch.float16: ARX_F16, torch.float32: ARX_F32})
+    code = _DTYPES.get(t.dtype)
+    if code not in allowed:
+        raise TypeError(f"{name}: {t.dtype} not supported")
+    return code
+
+
+class _Marshal:
+    """Fills an argument struct from tensors, checking each against the others."""
+
+    def __init__(self, args, first, name, types):
+        self.a = args
+        self.refs = []
+        self.dtype = first.dtype
+        self.device = None  # the current device, looked up once a tensor is on a GPU
+        if types is not None:
+            args.dtype = _dtype(first, name, types)
+        self.wdtype = None
+
+    def _on_device(self, t, name):
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+        if self.device is None:
+            import torch
+            self.device = torch.cuda.current_device()
+        if t.device.index != self.device:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{self.device}")
+
+    def matrix(self, t, name, rows=None, cols=None, ld=None):
+        """Sets field ``name`` (and ``ld<name>``) to the matrix and returns (rows, cols)."""
+        if t is None:
+            return None
+        if t.dtype is not self.dtype:
+            raise TypeError(f"{name}: expected {self.dtype}, got {t.dtype}")
+        if t.dim() < 2:
+            raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimension(s)")
+        n = t.shape[-1]
+        r = 1
+        for s in t.shape[:-1]:
+            r *= s
+        if (rows is not None and r != rows) or (cols is not None and n != cols):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs [{rows}, {cols}]")
+        stride = t.stride(-2) if t.shape[-2] > 1 else n
+        if r * n > 0:
+            if n > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{name}: the last dimension must be contiguous")
+            # The leading dimensions have to be one run of equally spaced rows.
+            step, last = None, None
+            for s, d in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+                if s == 1:
+                    continue
+                if step is None:
+                    step = d
+                elif d != last:
+                    raise ValueError(f"{name}: rows are not equally spaced (shape {tuple(t.shape)}, "
+                                     f"strides {tuple(t.stride())})")
+                last = d * s
+            stride = n if step is None else step
+            if step is not None and step < n:
+                raise ValueError(f"{name}: rows overlap (stride {step} below {n} columns)")
+        self._on_device(t, name)
+        setattr(self.a, name, t.data_ptr())
+        setattr(self.a, ld or "ld" + name, stride)
+        self.refs.append(t)
+        return r, n
+
+    def contiguous(self, t, name, rows, cols):
+        """A matrix without a leading dimension in the struct; returns its address."""
+        if t is None:
+            return None
+        if t.dtype is not self.dtype:
+            raise TypeError(f"{name}: expected {self.dtype}, got {t.dtype}")
+        if t.dim() < 2 or t.shape[-1] != cols or t.numel() != rows * cols:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs [{rows}, {cols}]")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        self._on_device(t, name)
+        self.refs.append(t)
+        return t.data_ptr()
+
+    def vector(self, t, name, n, dtype=None):
+        """``dtype`` None: a parameter, of the matrices' type or 32 bits, all of a call alike."""
+        if t is None:
+            return
+        import torch
+        if dtype is None:
+            if t.dtype is not self.dtype and t.dtype is not torch.float32:
+                raise TypeError(f"{name}: expected {self.dtype} or torch.float32, got {t.dtype}")
+            if self.wdtype is not None and t.dtype is not self.wdtype:
+                raise TypeError(f"{name}: {t.dtype}, but another parameter is {self.wdtype}")
+            self.wdtype = t.dtype
+        elif t.dtype is not dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.dim() != 1 or t.shape[0] != n:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs [{n}]")
+        if n > 1 and t.stride(0) != 1:
+            raise ValueError(f"{name}: must be contiguous")
+        self._on_device(t, name)
+        setattr(self.a, name, t.data_ptr())
+        self.refs.append(t)
+
+    def rng(self, p, rng):
+        import torch
+        self.a.p = p
+        if rng is None:
+            return
+        if rng.dtype not in (torch.int64, getattr(torch, "uint64", torch.int64)) or rng.numel() != 2:
+            raise TypeError("rng: expected two 64-bit integers (seed, offset)")
+        if not rng.is_contiguous():
+            raise ValueError("rng: must be contiguous")
+        self._on_device(rng, "rng")
+        self.a.rng = rng.data_ptr()
+        self.refs.append(rng)
+
+    def status(self, t):
+        if t is None:
+            return
+        import torch
+        if t.dtype not in (torch.int32, getattr(torch, "uint32", torch.int32)) or t.numel() < 1:
+            raise TypeError("status: expected one 32-bit integer")
+        self._on_device(t, "status")
+        self.a.status = t.data_ptr()
+        self.refs.append(t)
+
+    def workspace(self, t):
+        if t is None:
+            return
+        if not t.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
+        self._on_device(t, "workspace")
+        self.a.workspace = t.data_ptr() or None
+        self.a.workspace_bytes = t.numel() * t.element_size()
+        self.refs.append(t)
+
+    def done(self):
+        if hasattr(self.a, "wdtype"):
+            self.a.wdtype = self.a.dtype if self.wdtype in (None, self.dtype) else ARX_F32
+        return self.a, self.refs
+
+
+_ROW_TYPES = (ARX_BF16, ARX_F16, ARX_F32)
+_PRODUCT_TYPES = (ARX_BF16, ARX_F16)
+
+
+def _layer_norm(x, y, weight=None, bias=None, mean=None, rstd=None, eps=1e-5):
+    import torch
+    m = _Marshal(arx_layer_norm_args(eps=eps), x, "x", _ROW_TYPES)
+    rows, cols = m.matrix(x, "x")
+    m.matrix(y, "y", rows, cols)
+    m.vector(weight, "weight", cols)
+    m.vector(bias, "bias", cols)
+    m.vector(mean, "mean", rows, torch.float32)
+    m.vector(rstd, "rstd", rows, torch.float32)
+    m.a.rows, m.a.cols = rows, cols
+    return m.done()
+
+
+def _layer_norm_bwd(dy, x, mean, rstd, dx=None, weight=None, dresidual=None, dweight=None, dbias=None,
+                    workspace=None):
+    import torch
+    m = _Marshal(arx_layer_norm_bwd_args(), x, "x", _ROW_TYPES)
+    rows, cols = m.matrix(x, "x")
+    m.matrix(dy, "dy", rows, cols)
+    m.matrix(dresidual, "dresidual", rows, cols)
+    m.matrix(dx, "dx", rows, cols)
+    m.vector(mean, "mean", rows, torch.float32)
+    m.vector(rstd, "rstd", rows, torch.float32)
+    for t, name in ((weight, "weight"), (dweight, "dweight"), (dbias, "dbias")):
+        m.vector(t, name, cols)
+    m.workspace(workspace)
+    m.a.rows, m.a.cols = rows, cols
+    return m.done()
+
+
+def _dropout_add(x, out, p, rng=None, bias=None, residual=None):
+    m = _Marshal(arx_dropout_add_args(), x, "x", _ROW_TYPES)
+    rows, cols = m.matrix(x, "x")
+    m.matrix(residual, "residual", rows, cols)
+    m.matrix(out, "out", rows, cols)
+    m.vector(bias, "bias", cols)
+    m.rng(p, rng)
+    m.a.rows, m.a.cols = rows, cols
+    return m.done()
+
+
+def _dropout_add_bwd(dout, dx, p, rng=None, dbias=None, workspace=None):
+    m = _Marshal(arx_dropout_add_bwd_args(), dout, "dout", _ROW_TYPES)
+    rows, cols = m.matrix(dout, "dout")
+    m.matrix(dx, "dx", rows, cols)
+    m.vector(dbias, "dbias", cols)
+    m.rng(p, rng)
+    m.workspace(workspace)
+    m.a.rows, m.a.cols = rows, cols
+    return m.done()
+
+
+def _reduce_layer_norm(slots, h, y, bias=None, residual=None, weight=None, norm_bias=None, mean=None, rstd=None,
+                       eps=1e-5, p=0.0, rng=None):
+    import torch
+    a = arx_reduce_layer_norm_args(eps=eps)
+    if y.dtype is not torch.bfloat16:
+        raise TypeError(f"y: expected torch.bfloat16, got {y.dtype}")
+    if y.dim() < 2:
+        raise ValueError(f"y: expected a matrix, got {y.dim()} dimension(s)")
+    a.cols = cols = y.shape[-1]
+    a.rows = rows = y.numel() // cols if cols else 0
+    m = _Marshal(a, y, "y", None)
+    a.W = len(slots)
+    arr = (ctypes.c_void_p * max(1, len(slots)))(*[m.contiguous(s, f"slots[{i}]", rows, cols)
+                                                   for i, s in enumerate(slots)])
+    a.slots = ctypes.cast(arr, _vp)
+    m.refs.append(arr)
+    a.residual = m.contiguous(residual, "residual", rows, cols)
+    a.h = m.contiguous(h, "h", rows, cols)
+    a.y = m.contiguous(y, "y", rows, cols)
+    for t, name in ((bias, "bias"), (weight, "weight"), (norm_bias, "norm_bias")):
+        m.vector(t, name, cols, torch.bfloat16)
+    m.vector(mean, "mean", rows, torch.float32)
+    m.vector(rstd, "rstd", rows, torch.float32)
+    m.rng(p, rng)
+    return m.done()
+
+
+def _linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, status=None):
+    m = _Marshal(arx_linear_args(act=act), x, "x", _PRODUCT_TYPES)
+    M, K = m.matrix(x, "x")
+    N, _ = m.matrix(w, "w", None, K)
+    m.matrix(residual, "residual", M, N)
+    m.matrix(out, "out", M, N)
+    m.matrix(z, "z", M, N)
+    m.vector(bias, "bias", N)
+    m.status(status)
+    m.a.M, m.a.N, m.a.K = M, N, K
+    return m.done()
+
+
+def _linear_bwd(dout, x, w, dx=None, dw=None, dbias=None, z=None, act=ARX_ACT_NONE, workspace=None, status=None):
+    m = _Marshal(arx_linear_bwd_args(act=act), dout, "dout", _PRODUCT_TYPES)
+    M, N = m.matrix(dout, "dout")
+    K = next((t.shape[-1] for t in (x, w) if t is not None), 0)
+    m.matrix(z, "z", M, N)
+    m.matrix(x, "x", M, K)
+    m.matrix(w, "w", N, K)
+    m.matrix(dx, "dx", M, K)
+    m.matrix(dw, "dw", N, K)
+    m.vector(dbias, "dbias", N)
+    m.workspace(workspace)
+    m.status(status)
+    m.a.M, m.a.N, m.a.K = M, N, K
+    return m.done()
+
+
+class _Plan:
+    """A checked call: one C call with the stored arguments each time it is called."""
+
+    _marshal = _name = None
+
+    def __init__(self, *args, stream=None, **kwargs):
+        core = _core()
+        self._args, self._refs = type(self)._marshal(*args, **kwargs)
+        self._ref = ctypes.byref(self._args)
+        self._stream = core._stream(stream)
+        self._fn = getattr(core.lib, self._name)
+
+    def __call__(self) -> None:
+        st = self._fn(self._ref, self._stream)
+        if st:
+            _core()._check(st)
+
+
+def _function(name, marshal, doc):
+    def call(*args, stream=None, check=True, **kwargs):
+        core = _core()
+        a, _ = marshal(*args, **kwargs)
+        st = getattr(core.lib, name)(ctypes.byref(a), core._stream(stream))
+        if check:
+            core._check(st)
+        return st
+    call.__name__ = call.__qualname__ = name
+    call.__doc__ = doc
+    plan = type(name + "_plan", (_Plan,), {"_marshal": staticmethod(marshal), "_name": name,
+                                           "__doc__": f"A prepared ``{name}``: the same arguments, checked once."})
+    plan.__module__ = call.__module__ = "deterministic_shot_all_gb300"
+    return call, plan
+
+
+arx_layer_norm, arx_layer_norm_plan = _function("arx_layer_norm", _layer_norm, """\
+Enqueue y = (x - mean) * rstd * weight + bias over the rows of ``x``.
+
+    ``arx_layer_norm(x, y, weight=None, bias=None, mean=None, rstd=None, eps=1e-5, stream=None, check=True)``
+
+    bf16, fp16 or fp32; weight and bias of the same type or fp32.  ``y`` may be ``x``.
+    ``mean`` and ``rstd``: fp32 [rows] outputs for the backward pass.
+    """)
+arx_layer_norm_bwd, arx_layer_norm_bwd_plan = _function("arx_layer_norm_bwd", _layer_norm_bwd, """\
+Enqueue the gradients of ``arx_layer_norm``.
+
+    ``arx_layer_norm_bwd(dy, x, mean, rstd, dx=None, weight=None, dresidual=None, dweight=None, dbias=None,
+    workspace=None, stream=None, check=True)``
+
+    ``dresidual`` is added to dx; dx may be dy, x or dresidual.  ``workspace``: a device
+    tensor of ``arx_layer_norm_bwd_workspace_bytes(rows, cols)`` bytes when dweight or
+    dbias is asked for.
+    """)
+arx_dropout_add, arx_dropout_add_plan = _function("arx_dropout_add", _dropout_add, """\
+Enqueue out = residual + keep(x + bias) / (1 - p), the mask from a counter-based generator.
+
+    ``arx_dropout_add(x, out, p, rng=None, bias=None, residual=None, stream=None, check=True)``
+
+    ``rng``: a device tensor of two int64, seed and offset, read when the kernel runs.
+    ``out`` may be ``x`` or ``residual``.
+    """)
+arx_dropout_add_bwd, arx_dropout_add_bwd_plan = _function("arx_dropout_add_bwd", _dropout_add_bwd, """\
+Enqueue dx = keep(dout) / (1 - p) with the forward's mask, and dbias, its sum over rows.
+
+    ``arx_dropout_add_bwd(dout, dx, p, rng=None, dbias=None, workspace=None, stream=None, check=True)``
+
+    dx may be dout or None; ``workspace`` of ``arx_dropout_add_bwd_workspace_bytes(rows,
+    cols)`` bytes when dbias is asked for.
+    """)
+arx_reduce_layer_norm, arx_reduce_layer_norm_plan = _function("arx_reduce_layer_norm", _reduce_layer_norm, """\
+Enqueue h = residual + keep(rank-order sum of slots + bias) / (1 - p), y = layer norm of h.
+
+    ``arx_reduce_layer_norm(slots, h, y, bias=None, residual=None, weight=None, norm_bias=None, mean=None,
+    rstd=None, eps=1e-5, p=0.0, rng=None, stream=None, check=True)``
+
+    bf16, contiguous; ``h`` (may be None) and ``y`` may each be a slot or the residual.
+    """)
+arx_linear, arx_linear_plan = _function("arx_linear", _linear, """\
+Enqueue out = act(x w^T + bias) + residual on the tensor cores.
+
+    ``arx_linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, status=None, stream=None,
+    check=True)``
+
+    bf16 or fp16; x [M, K], w [N, K]; bias of the same type or fp32.  ``z`` receives
+    x w^T + bias for the backward pass.  ``out`` may be ``residual``.
+    """)
+arx_linear_bwd, arx_linear_bwd_plan = _function("arx_linear_bwd", _linear_bwd, """\
+Enqueue dz = dout * act'(z), dx = dz w, dw = dz^T x, dbias = sum over rows of dz.
+
+    ``arx_linear_bwd(dout, x, w, dx=None, dw=None, dbias=None, z=None, act=ARX_ACT_NONE, workspace=None,
+    status=None, stream=None, check=True)``
+
+    ``workspace`` of ``arx_linear_bwd_workspace_bytes(M, N)`` bytes, unless there is no
+    activation and no dbias.
+    """)
+
+
+def arx_layer_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_core().lib.arx_layer_norm_bwd_workspace_bytes(rows, cols))
+
+
+def arx_dropout_add_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_core().lib.arx_dropout_add_bwd_workspace_bytes(rows, cols))
+
+
+def arx_linear_bwd_workspace_bytes(M: int, N: int) -> int:
+    return int(_core().lib.arx_linear_bwd_workspace_bytes(M, N))
+
+
+__all__ = [
+    "ARX_BF16", "ARX_F16", "ARX_F32", "ARX_ACT_NONE", "ARX_ACT_RELU", "ARX_ACT_GELU", "ARX_ACT_GELU_TANH",
+    "ARX_ACT_SILU",
+    *(f"arx_{op}{suffix}" for op in ("layer_norm", "layer_norm_bwd", "dropout_add", "dropout_add_bwd",
+                                     "reduce_layer_norm", "linear", "linear_bwd")
+      for suffix in ("", "_plan", "_args")),
+    "arx_layer_norm_bwd_workspace_bytes", "arx_dropout_add_bwd_workspace_bytes", "arx_linear_bwd_workspace_bytes",
+]

@@ -530,6 +530,245 @@ arx_status arx_ext_reset(arx_ext* x, void* stream);
 arx_status arx_step_noalloc(const void* const* inputs, int W, void* out, size_t n,
                             uint32_t* dev_status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around a sublayer's all-reduce.
+ *
+ * A rank of a tensor-parallel block computes a matrix product (arx_linear),
+ * the ranks' partials are summed in rank order, and the sum goes through
+ * bias, dropout and the residual add into a layer norm
+ * (arx_reduce_layer_norm, or arx_reduce, arx_dropout_add and arx_layer_norm
+ * one after the other); the *_bwd calls are their backward passes.
+ *
+ * Conventions, beside those at the top:
+ *  - Matrices are row-major: element (i, j) of x is x[i * ldx + j], ldx in
+ *    elements, at least the column count (ignored when there is one row).
+ *    Vectors are contiguous.
+ *  - `dtype` is the type of the matrices, `wdtype` that of the weight, bias
+ *    and their gradients: the same type, or ARX_F32.
+ *  - Every element is widened to fp32, computed and summed in fp32 and rounded
+ *    once (nearest even) where it is stored, except where a call says so.
+ *    Infinities and NaN follow the formulas.
+ *  - The same call on the same values gives the same bits on every run: sums
+ *    are taken in an order that depends on the sizes alone (no atomics).
+ *  - An output may be exactly one of the inputs that a call names (same
+ *    address, same leading dimension: each element is read before it is
+ *    written); any other overlap of an output with an input, another output
+ *    or the workspace is ARX_EOVERLAP.  Views of one buffer whose rows
+ *    interleave without sharing elements do not overlap.
+ *  - Every call launches kernels only, returns without waiting and can be
+ *    captured into a CUDA graph.  Argument errors return ARX_EINVAL before
+ *    anything is enqueued.  Rows, columns, M, N and K are below 2^31.
+ *  - A workspace is the caller's device buffer, 16-byte aligned, of at least
+ *    the bytes that the *_workspace_bytes call gives; its contents need no
+ *    initialisation and mean nothing afterwards.  Calls that share one must
+ *    be serialised.
+ * ------------------------------------------------------------------------- */
+#define ARX_BF16 0
+#define ARX_F16 1
+#define ARX_F32 2
+
+/* Layer norm of each row:
+ *   mean = sum(x) / cols, var = sum((x - mean)^2) / cols, rstd = 1 / sqrt(var + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ *   x      [rows, cols] of `dtype`
+ *   weight, bias  [cols] of `wdtype`, or NULL for 1 and 0
+ *   y      [rows, cols]; may be exactly x
+ *   mean, rstd    fp32 [rows], or NULL (both or neither need not be given) */
+typedef struct arx_layer_norm_args {
+  const void* x;
+  const void* weight;
+  const void* bias;
+  void* y;
+  float* mean;
+  float* rstd;
+  uint64_t rows, cols, ldx, ldy;
+  float eps;
+  int32_t dtype, wdtype;
+  int32_t reserved;
+} arx_layer_norm_args;
+
+arx_status arx_layer_norm(const arx_layer_norm_args* a, void* stream);
+
+/* Its backward pass, from the forward's x, mean and rstd:
+ *   q = dy * weight, xh = (x - mean) * rstd,
+ *   dx = rstd * (q - sum(q) / cols - xh * sum(q * xh) / cols) + dresidual,
+ *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy.
+ *   dy, x, dresidual  [rows, cols]; dresidual (the gradient that reaches x past
+ *                     the norm) may be NULL
+ *   dx                [rows, cols]; may be exactly dy, x or dresidual; NULL skips it
+ *   dweight, dbias    [cols] of `wdtype`; either may be NULL.  With rows == 0
+ *                     they are set to zero.
+ *   workspace         arx_layer_norm_bwd_workspace_bytes(rows, cols) bytes;
+ *                     may be NULL when dweight and dbias are */
+typedef struct arx_layer_norm_bwd_args {
+  const void* dy;
+  const void* x;
+  const float* mean;
+  const float* rstd;
+  const void* weight;
+  const void* dresidual;
+  void* dx;
+  void* dweight;
+  void* dbias;
+  void* workspace;
+  uint64_t workspace_bytes;
+  uint64_t rows, cols, lddy, ldx, lddresidual, lddx;
+  int32_t dtype, wdtype;
+} arx_layer_norm_bwd_args;
+
+size_t arx_layer_norm_bwd_workspace_bytes(uint64_t rows, uint64_t cols);
+arx_status arx_layer_norm_bwd(const arx_layer_norm_bwd_args* a, void* stream);
+
+/* Dropout with the bias before it and the residual after it:
+ *   out = residual + keep(x + bias) * 65536 / (65536 - T),  T = round(65536 p),
+ * where an element that is not kept contributes 0 whatever its value.
+ *
+ * The mask is never stored: element (row, col) is kept when its 16-bit value
+ * is at least T.  The values are Philox4x32-10 (Salmon et al., "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011) of the counter (col / 8, row,
+ * offset low half, offset high half) under the key (seed low half, seed high
+ * half): the four words of a counter are, low halves first, the values of
+ * columns 8 (col / 8) ... + 7.  A backward pass with the same rng regenerates
+ * the same mask; another layer or step takes another seed or offset.  The
+ * probability is p to within 2^-17, and the scale is exact for the T used.
+ *   x         [rows, cols] of `dtype`
+ *   bias      [cols] of `wdtype`, or NULL;  residual [rows, cols], or NULL
+ *   out       [rows, cols]; may be exactly x or residual
+ *   p         0 <= p <= 1 (1 drops everything)
+ *   rng       DEVICE pointer to two uint64, seed and offset, 8-byte aligned: read
+ *             when the kernel runs, so a captured graph takes new values from
+ *             memory at every replay.  May be NULL when p == 0. */
+typedef struct arx_dropout_add_args {
+  const void* x;
+  const void* bias;
+  const void* residual;
+  void* out;
+  const uint64_t* rng;
+  uint64_t rows, cols, ldx, ldresidual, ldout;
+  double p;
+  int32_t dtype, wdtype;
+} arx_dropout_add_args;
+
+arx_status arx_dropout_add(const arx_dropout_add_args* a, void* stream);
+
+/* Its backward pass: dx = keep(dout) * 65536 / (65536 - T), dbias = sum over
+ * rows of dx (before it is rounded).  The residual's gradient is dout itself.
+ *   dx      [rows, cols]; may be exactly dout; NULL skips it
+ *   dbias   [cols] of `wdtype`, or NULL; zero when rows == 0
+ *   workspace  arx_dropout_add_bwd_workspace_bytes(rows, cols) bytes; may be NULL
+ *           when dbias is */
+typedef struct arx_dropout_add_bwd_args {
+  const void* dout;
+  void* dx;
+  void* dbias;
+  const uint64_t* rng;
+  void* workspace;
+  uint64_t workspace_bytes;
+  uint64_t rows, cols, lddout, lddx;
+  double p;
+  int32_t dtype, wdtype;
+} arx_dropout_add_bwd_args;
+
+size_t arx_dropout_add_bwd_workspace_bytes(uint64_t rows, uint64_t cols);
+arx_status arx_dropout_add_bwd(const arx_dropout_add_bwd_args* a, void* stream);
+
+/* The end of a sublayer in one kernel, for bf16 partials:
+ *   s = ((+0 + slot[0]) + slot[1]) + ... in rank order (as arx_reduce, not rounded),
+ *   h = residual + keep(s + bias) * 65536 / (65536 - T),
+ *   y = layer_norm(h) with weight and norm_bias,
+ * the norm taken of h before its rounding (mean, rstd likewise).
+ *   slots     HOST array of W device pointers, each to a contiguous bf16 [rows, cols];
+ *             read during the call only; slots may repeat or overlap each other
+ *   bias      bf16 [cols] or NULL;  residual  contiguous bf16 [rows, cols] or NULL
+ *   weight, norm_bias  bf16 [cols] or NULL
+ *   h, y      contiguous bf16 [rows, cols]; each may be exactly a slot or the
+ *             residual, but not each other; h may be NULL
+ *   mean, rstd   fp32 [rows] or NULL
+ *   p, rng    as in arx_dropout_add */
+typedef struct arx_reduce_layer_norm_args {
+  const void* const* slots;
+  const void* bias;
+  const void* residual;
+  const void* weight;
+  const void* norm_bias;
+  void* h;
+  void* y;
+  float* mean;
+  float* rstd;
+  const uint64_t* rng;
+  uint64_t rows, cols;
+  double p;
+  float eps;
+  int32_t W;
+} arx_reduce_layer_norm_args;
+
+arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stream);
+
+/* Matrix product with bias, activation and residual in its epilogue:
+ *   z = x w^T + bias,  out = act(z) + residual.
+ *   x     [M, K], w [N, K] (output feature by input feature), of `dtype`
+ *         (ARX_BF16 or ARX_F16), products summed in fp32 on the tensor cores
+ *   bias  [N] of `wdtype`, or NULL;  residual  [M, N], or NULL
+ *   out   [M, N]; may be exactly the residual
+ *   z     [M, N], or NULL: the product with its bias, for arx_linear_bwd
+ *   act   ARX_ACT_*: none, relu, gelu (z Phi(z)), gelu_tanh (its tanh form),
+ *         silu (z / (1 + exp(-z)))
+ *   status  optional DEVICE uint32, zero before the call: set to a nonzero
+ *         device error word (ARX_ETIMEOUT in the low byte) if a wait of the
+ *         kernel for its own copies or products ran out; the outputs are then
+ *         unspecified.  No input causes it.
+ * Rows whose address or leading dimension is not a multiple of 16 bytes are
+ * loaded by threads instead of by the copy engine, at a lower rate. */
+#define ARX_ACT_NONE 0
+#define ARX_ACT_RELU 1
+#define ARX_ACT_GELU 2
+#define ARX_ACT_GELU_TANH 3
+#define ARX_ACT_SILU 4
+
+typedef struct arx_linear_args {
+  const void* x;
+  const void* w;
+  const void* bias;
+  const void* residual;
+  void* out;
+  void* z;
+  uint32_t* status;
+  uint64_t M, N, K, ldx, ldw, ldresidual, ldout, ldz;
+  int32_t act, dtype, wdtype;
+  int32_t reserved;
+} arx_linear_args;
+
+arx_status arx_linear(const arx_linear_args* a, void* stream);
+
+/* Its backward pass:
+ *   dz = dout * act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum over rows of dz.
+ * dz is an operand of two products and so rounded to `dtype`; dbias sums it
+ * unrounded.  (The residual's gradient is dout itself.)
+ *   dout    [M, N];  z [M, N] from the forward, needed unless act is ARX_ACT_NONE
+ *   x, w    as in the forward; x may be NULL without dw, w without dx
+ *   dx      [M, K], dw [N, K], dbias [N] of `wdtype`; any may be NULL.
+ *           M == 0 sets dw and dbias to zero.
+ *   workspace  arx_linear_bwd_workspace_bytes(M, N) bytes (dz and partial sums);
+ *           may be NULL when act is ARX_ACT_NONE and dbias is NULL */
+typedef struct arx_linear_bwd_args {
+  const void* dout;
+  const void* z;
+  const void* x;
+  const void* w;
+  void* dx;
+  void* dw;
+  void* dbias;
+  void* workspace;
+  uint64_t workspace_bytes;
+  uint32_t* status;
+  uint64_t M, N, K, lddout, ldz, ldx, ldw, lddx, lddw;
+  int32_t act, dtype, wdtype;
+  int32_t reserved;
+} arx_linear_bwd_args;
+
+size_t arx_linear_bwd_workspace_bytes(uint64_t M, uint64_t N);
+arx_status arx_linear_bwd(const arx_linear_bwd_args* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
