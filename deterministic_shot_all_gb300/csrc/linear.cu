@@ -10,10 +10,12 @@
 // Roles (warps): one copies, one issues the matrix instructions, four read
 // the accumulators and run the epilogue; operands pass through a ring of
 // stages guarded by mbarriers.  Matrices that the copy engine cannot address
-// (rows off 16 bytes) are loaded by 128 more threads into the same swizzled
+// (rows off 16 bytes) are loaded by 512 more threads into the same swizzled
 // stages.
 //
-// Two forms:
+// Three forms:
+//  vector one to four rows (decode): dot products on the CUDA cores, see
+//         dot_kernel; the tensor cores' set-up would cost more than the work.
 //  wide   persistent blocks over tiles of 128 x 256, two accumulators in tensor
 //         memory, so a tile's epilogue runs under the next tile's products;
 //  split  for few tiles (decode, small matrices): the output's columns take
@@ -41,7 +43,7 @@ constexpr uint32_t kStep = 64;               // contraction elements in a stage
 constexpr uint32_t kPBytes = kLanes * 128;   // P's part of a stage
 constexpr uint32_t kMaxStages = 12;
 constexpr uint32_t kStageBudget = 200 * 1024;  // also keeps one block on an SM: tensor memory is never contended
-constexpr uint32_t kLoaders = 128;
+constexpr uint32_t kLoaders = 512;
 
 struct GemmArgs {
   const uint16_t *p, *q;
@@ -90,31 +92,118 @@ __device__ __forceinline__ void copy_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 
-// The copy engine's box in plain loads: `rows` rows of 64 elements at
-// (row0, col0) of a [nrows, ncols] matrix, zeros outside it, swizzled as the
-// copy engine does (16-byte unit u of row r at u ^ (r mod 8)).
-__device__ __forceinline__ void load_box(uint8_t* dst, const uint16_t* src, uint64_t ld, uint32_t nrows, uint32_t ncols,
-                                         uint32_t row0, uint32_t col0, uint32_t rows, uint32_t tid) {
-  for (uint32_t i = tid; i < rows * 8; i += kLoaders) {
-    const uint32_t r = i >> 3, u = i & 7u, row = row0 + r, col = col0 + u * 8;
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (row < nrows) {
-      const uint16_t* p = src + row * ld + col;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (col + k < ncols) w[k >> 1] |= uint32_t(p[k]) << (16 * (k & 1));
-    }
-    *reinterpret_cast<uint4*>(dst + r * 128 + ((u ^ (r & 7u)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+// ---- filling a stage with plain loads -------------------------------------------------
+//
+// A stage is (128 + bn) rows of eight 16-byte units; a unit's 8 elements may
+// start at any even address.  Aligned 16-byte loads cover it: a thread loads
+// the aligned unit at or below its address, takes the next one from its
+// neighbour in the row (the last of a row loads it), and shifts the 8
+// elements out of the pair.  Nothing outside [lo, hi), the matrix's first and
+// last byte, is touched: units whose aligned loads would cross them go element
+// by element.
+
+struct Operand {
+  const uint16_t* p;
+  uint64_t ld;
+  uint32_t nrows, ncols;  // as stored
+  uint32_t mn, row0;      // the tile's first matrix row
+  uintptr_t lo, hi;
+};
+
+__device__ __forceinline__ Operand operand(const uint16_t* p, uint64_t ld, uint32_t mn, uint32_t rows, uint32_t k,
+                                           uint32_t row0) {
+  Operand o{p, ld, mn ? k : rows, mn ? rows : k, mn, row0, 0, 0};
+  o.lo = reinterpret_cast<uintptr_t>(p);
+  o.hi = o.lo + ((o.nrows - 1) * ld + o.ncols) * 2;
+  return o;
+}
+
+// In flight: one unit of a thread.
+struct Unit {
+  uint4 a, b;
+  uintptr_t at;    // address of the unit's first element
+  int n;           // its elements inside the matrix, at most 8 (0 or less: none)
+  uint32_t flags;  // 1: `a` was loaded, 2: `b` was loaded
+};
+
+__device__ __forceinline__ void unit_load(Unit& t, const Operand& o, uint32_t id, uint32_t k0) {
+  const uint32_t line = id >> 3, u = id & 7u;
+  const uint32_t row = o.mn ? k0 + (line & 63u) : o.row0 + line;
+  const uint32_t col = (o.mn ? o.row0 + (line >> 6) * 64 : k0) + u * 8;
+  t.a = t.b = make_uint4(0, 0, 0, 0);
+  t.n = row < o.nrows ? int(o.ncols) - int(col) : -8;
+  t.at = reinterpret_cast<uintptr_t>(o.p + row * o.ld + col);
+  t.flags = 0;
+  const uintptr_t q = t.at & ~uintptr_t(15);
+  // Also loaded when only the unit before needs it.
+  if (t.n > -8 && q >= o.lo && q + 16 <= o.hi) {
+    t.a = *reinterpret_cast<const uint4*>(q);
+    t.flags = 1;
+  }
+  if (u == 7 && t.n > 0 && (t.at & 15) != 0 && q + 32 <= o.hi) {
+    t.b = *reinterpret_cast<const uint4*>(q + 16);
+    t.flags |= 2;
   }
 }
 
-__device__ __forceinline__ void load_operand(uint8_t* dst, const uint16_t* src, uint64_t ld, bool mn, uint32_t nrows,
-                                             uint32_t nk, uint32_t row0, uint32_t k0, uint32_t rows, uint32_t tid) {
-  if (!mn) {
-    load_box(dst, src, ld, nrows, nk, row0, k0, rows, tid);
-  } else {
-    for (uint32_t r = 0; r < rows; r += 64) load_box(dst + r * 128, src, ld, nk, nrows, k0, row0 + r, 64, tid);
+__device__ __forceinline__ void unit_store(Unit& t, uint32_t id, uint8_t* dst) {
+  const uint32_t u = id & 7u;
+  uint4 nb;
+  nb.x = __shfl_down_sync(0xFFFFFFFFu, t.a.x, 1);
+  nb.y = __shfl_down_sync(0xFFFFFFFFu, t.a.y, 1);
+  nb.z = __shfl_down_sync(0xFFFFFFFFu, t.a.z, 1);
+  nb.w = __shfl_down_sync(0xFFFFFFFFu, t.a.w, 1);
+  const uint32_t nf = __shfl_down_sync(0xFFFFFFFFu, t.flags, 1);
+  if (u != 7) {
+    t.b = nb;
+    if (nf & 1) t.flags |= 2;
   }
+  const uint32_t mis = uint32_t(t.at & 15);
+  const int n = t.n > 8 ? 8 : t.n;
+  uint32_t w[4] = {0, 0, 0, 0};
+  if (n > 0) {
+    if ((t.flags & 1) && (mis + 2 * n <= 16 || (t.flags & 2))) {
+      uint32_t s[8] = {t.a.x, t.a.y, t.a.z, t.a.w, t.b.x, t.b.y, t.b.z, t.b.w};
+      if (mis & 8)
+#pragma unroll
+        for (int i = 0; i < 6; ++i) s[i] = s[i + 2];
+      if (mis & 4)
+#pragma unroll
+        for (int i = 0; i < 5; ++i) s[i] = s[i + 1];
+      const uint32_t shift = (mis & 2) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(s[i], s[i + 1], shift);
+      if (n < 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] &= n >= 2 * i + 2 ? 0xFFFFFFFFu : (n == 2 * i + 1 ? 0xFFFFu : 0u);
+    } else {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(t.at);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+    }
+  }
+  const uint32_t line = id >> 3;
+  *reinterpret_cast<uint4*>(dst + line * 128 + ((u ^ (line & 7u)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// kN units of a thread at once: their loads are in flight together.
+template <int kN>
+__device__ __forceinline__ void load_units(const Operand& o, uint8_t* dst, uint32_t first, uint32_t k0) {
+  Unit t[kN];
+#pragma unroll
+  for (int j = 0; j < kN; ++j) unit_load(t[j], o, first + j * kLoaders, k0);
+#pragma unroll
+  for (int j = 0; j < kN; ++j) unit_store(t[j], first + j * kLoaders, dst);
+}
+
+__device__ __forceinline__ void load_stage(const Operand& p, const Operand& q, uint8_t* dst, uint32_t bn, uint32_t k0,
+                                           uint32_t tid) {
+  load_units<kLanes * 8 / kLoaders>(p, dst, tid, k0);
+  const uint32_t units = bn * 8;
+  uint32_t i = tid;
+  for (; i + kLoaders < units; i += 2 * kLoaders) load_units<2>(q, dst + kPBytes, i, k0);
+  if (i < units) load_units<1>(q, dst + kPBytes, i, k0);  // whole warps: units and kLoaders are multiples of 32
 }
 
 // ---- the roles, for one tile -------------------------------------------------------
@@ -125,8 +214,15 @@ template <bool kTma>
 __device__ __forceinline__ bool fill_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
                                           uint8_t* stages, Ring& ring, uint32_t p0, uint32_t q0, uint32_t first,
                                           uint32_t last, uint32_t tid) {
+  Operand op, oq;
+  if constexpr (!kTma) {
+    op = operand(a.p, a.ldp, a.p_mn, a.P, a.K, p0);
+    oq = operand(a.q, a.ldq, a.q_mn, a.Q, a.K, q0);
+  }
   for (uint32_t i = first; i < last; ++i) {
-    if (!mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort)) return false;
+    bool ok = mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort);
+    if constexpr (!kTma) ok = __all_sync(0xFFFFFFFFu, ok);
+    if (!ok) return false;
     uint8_t* dst = stages + ring.slot * a.stage_bytes;
     const uint32_t bar = addr_of(&s.full[ring.slot]);
     if constexpr (kTma) {
@@ -134,8 +230,7 @@ __device__ __forceinline__ bool fill_tile(const GemmArgs& a, const CUtensorMap* 
       copy_operand(addr_of(dst), mp, a.p_mn, p0, i * kStep, kLanes, bar);
       copy_operand(addr_of(dst) + kPBytes, mq, a.q_mn, q0, i * kStep, a.bn, bar);
     } else {
-      load_operand(dst, a.p, a.ldp, a.p_mn, a.P, a.K, p0, i * kStep, kLanes, tid);
-      load_operand(dst + kPBytes, a.q, a.ldq, a.q_mn, a.Q, a.K, q0, i * kStep, a.bn, tid);
+      load_stage(op, oq, dst, a.bn, i * kStep, tid);
       fence_async_shared();
       mbar_arrive(bar);
     }
@@ -420,6 +515,80 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
   finish_block(a, s, warp, lane, kTma, ring, last - first);
 }
 
+// ---- one to four rows ------------------------------------------------------------------
+//
+// out[m][j] = sum_k x[m][k] w[j][k]: w is read once, which bounds the kernel,
+// at 2 M operations to an element.  A warp (or `split` warps of a block) takes
+// a feature j; its lanes take 16-byte units of the row, kBatch of them in
+// flight, and x comes from L1.  The lanes' sums meet in a butterfly and the
+// split warps' in warp order.  kV = 1: rows off 16 bytes, element by element.
+
+constexpr uint32_t kDotRows = 4;
+constexpr uint32_t kDotThreads = 256;
+constexpr int kDotBatch = 8;
+
+template <int D, int kM, int kV>
+__global__ void __launch_bounds__(kDotThreads) dot_kernel(const __grid_constant__ GemmArgs a) {
+  __shared__ float part[kDotThreads / 32][kM];
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const uint32_t per = kDotThreads / 32 / a.split;             // features of a block
+  const uint32_t j = blockIdx.x * per + warp / a.split, share = warp % a.split;
+  // A hint only (as in the reduce kernels): the weights' way to L2 starts
+  // while the stream's previous kernel, whose output x may be, still runs.
+  if (kV == 8 && share == 0 && lane == 0 && j < a.Q && a.K > 0) prefetch_l2_bulk(a.q + j * a.ldq, a.K * 2);
+  dependent_launch_prologue();
+  float acc[kM] = {};
+  if (j < a.Q) {
+    const uint16_t* w = a.q + j * a.ldq;
+    const uint32_t units = a.K / kV, step = 32 * a.split;
+    for (uint32_t u0 = share * 32 + lane; u0 < units; u0 += kDotBatch * step) {
+      Pack<D, kV> wv[kDotBatch];
+#pragma unroll
+      for (int b = 0; b < kDotBatch; ++b)
+        if (u0 + b * step < units)
+          wv[b].load(w + size_t(u0 + b * step) * kV);
+        else
+          wv[b].zero();
+#pragma unroll
+      for (int b = 0; b < kDotBatch; ++b) {
+        if (u0 + b * step >= units) break;
+        float f[kV];
+        wv[b].get(f);
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+          float x[kV];
+          load_params<kV>(a.p + m * a.ldp, D, size_t(u0 + b * step) * kV, x);
+#pragma unroll
+          for (int k = 0; k < kV; ++k) acc[m] = fmaf(f[k], x[k], acc[m]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < kM; ++m) acc[m] = warp_sum(acc[m]);
+  if (a.split > 1) {
+    if (lane == 0)
+#pragma unroll
+      for (int m = 0; m < kM; ++m) part[warp][m] = acc[m];
+    __syncthreads();
+    if (share == 0)
+      for (uint32_t r = 1; r < a.split; ++r)
+#pragma unroll
+        for (int m = 0; m < kM; ++m) acc[m] += part[warp + r][m];
+  }
+  if (share != 0 || j >= a.Q) return;
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+    if (lane == uint32_t(m)) {
+      float f[1] = {acc[m]};
+      if (a.bias) f[0] += load_param(a.bias, a.wdtype, j);
+      if (a.z) a.z[m * a.ldz + j] = Elem<D>::round(f[0]);
+      activate<1>(f, a.act);
+      if (a.residual) f[0] += Elem<D>::widen(a.residual[m * a.ldresidual + j]);
+      a.out[m * a.ldout + j] = Elem<D>::round(f[0]);
+    }
+}
+
 // ---- host side ---------------------------------------------------------------------
 
 // cuTensorMapEncodeTiled, looked up once through the runtime (the library
@@ -505,6 +674,17 @@ cudaError_t launch_split(const GemmArgs& a, const CUtensorMap& mp, const CUtenso
 
 uint32_t ceil_div(uint64_t a, uint64_t b) { return uint32_t((a + b - 1) / b); }
 
+template <int D, int kV>
+cudaError_t launch_dot(const GemmArgs& a, cudaStream_t st) {
+  const dim3 grid(ceil_div(a.Q, kDotThreads / 32 / a.split));
+  switch (a.P) {
+    case 1: return launch_op(dot_kernel<D, 1, kV>, grid, kDotThreads, 0, st, a);
+    case 2: return launch_op(dot_kernel<D, 2, kV>, grid, kDotThreads, 0, st, a);
+    case 3: return launch_op(dot_kernel<D, 3, kV>, grid, kDotThreads, 0, st, a);
+    default: return launch_op(dot_kernel<D, 4, kV>, grid, kDotThreads, 0, st, a);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
@@ -526,6 +706,19 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
     return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0);
   };
   a.vec = aligned(a.out, a.ldout) && aligned(a.z, a.ldz) && aligned(a.residual, a.ldresidual) && aligned(a.bias, 8);
+
+  const bool bf16 = c.dtype == ARX_BF16;
+  if (c.rows <= kDotRows && !c.p_mn && !c.q_mn) {
+    a.p = static_cast<const uint16_t*>(c.p), a.q = static_cast<const uint16_t*>(c.q);
+    a.ldp = c.ldp, a.ldq = c.ldq;
+    a.P = uint32_t(c.rows), a.Q = uint32_t(c.cols);
+    const bool units = a.K % 8 == 0 && copyable(a.p, a.ldp, a.P) && copyable(a.q, a.ldq, a.Q);
+    // Warps for about 16 to an SM, while each keeps 256 elements or more.
+    a.split = 1;
+    while (a.split < 8 && uint64_t(a.Q) * a.split < 2432 && a.K / a.split > 512) a.split *= 2;
+    if (bf16) return units ? launch_dot<ARX_BF16, 8>(a, st) : launch_dot<ARX_BF16, 1>(a, st);
+    return units ? launch_dot<ARX_F16, 8>(a, st) : launch_dot<ARX_F16, 1>(a, st);
+  }
 
   // Wide tiles when they occupy most of the SMs, else the split form.
   const bool wide = uint64_t(ceil_div(c.rows, kLanes)) * ceil_div(c.cols, 256) >= 100;
@@ -556,7 +749,6 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   const uint64_t p_rows = a.p_mn ? a.K : a.P, q_rows = a.q_mn ? a.K : a.Q;
   const bool tma = a.K > 0 && copyable(a.p, a.ldp, p_rows) && copyable(a.q, a.ldq, q_rows);
   CUtensorMap mp{}, mq{};
-  const bool bf16 = c.dtype == ARX_BF16;
   if (tma) {
     err = encode(&mp, a.p, a.ldp, p_rows, a.p_mn ? a.P : a.K, a.p_mn ? 64 : kLanes, bf16);
     if (err != cudaSuccess) return err;
