@@ -16,8 +16,11 @@
 // Three forms:
 //  vector one to four rows (decode): dot products on the CUDA cores, see
 //         dot_kernel; the tensor cores' set-up would cost more than the work.
-//  wide   persistent blocks over tiles of 128 x 256, two accumulators in tensor
-//         memory, so a tile's epilogue runs under the next tile's products;
+//  wide   persistent pairs of blocks over tiles of 256 x 256 (one instruction
+//         spans both SMs, each holding half of either operand: a single SM
+//         at 128 x 256 would need 96 bytes a cycle from L2, against the 64
+//         it can take; the pair needs 64), two accumulators in tensor memory,
+//         so a tile's epilogue runs under the next tile's products;
 //  split  for few tiles (decode, small matrices): the output's columns take
 //         the 128 accumulator lanes, its few rows the instruction's N, and a
 //         cluster of up to 8 blocks splits the contraction; the partials
@@ -56,7 +59,7 @@ struct GemmArgs {
   uint64_t ldout, ldz, ldresidual;
   uint32_t* status;
   int act, wdtype;
-  uint32_t bn;         // rows of Q in a tile
+  uint32_t bn, bq;     // rows of Q in a tile, and in a block's stage
   uint32_t stages, stage_bytes;
   uint32_t steps;      // stages' worth of contraction: ceil(K / 64)
   uint32_t split;      // blocks of a cluster that share a tile's contraction
@@ -83,12 +86,21 @@ __device__ __forceinline__ uint32_t addr_of(const void* p) { return shared_addre
 
 // ---- filling a stage -----------------------------------------------------------
 
+template <bool kPair>
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, uint32_t x, uint32_t y, uint32_t bar) {
+  if constexpr (kPair)
+    tma_load_2d_pair(dst, map, x, y, bar);
+  else
+    tma_load_2d(dst, map, x, y, bar);
+}
+
+template <bool kPair>
 __device__ __forceinline__ void copy_operand(uint32_t dst, const CUtensorMap* map, bool mn, uint32_t row0, uint32_t k0,
                                              uint32_t rows, uint32_t bar) {
   if (!mn) {
-    tma_load_2d(dst, map, k0, row0, bar);
+    copy_box<kPair>(dst, map, k0, row0, bar);
   } else {
-    for (uint32_t r = 0; r < rows; r += 64) tma_load_2d(dst + r * 128, map, row0 + r, k0, bar);
+    for (uint32_t r = 0; r < rows; r += 64) copy_box<kPair>(dst + r * 128, map, row0 + r, k0, bar);
   }
 }
 
@@ -208,12 +220,13 @@ __device__ __forceinline__ void load_stage(const Operand& p, const Operand& q, u
 
 // ---- the roles, for one tile -------------------------------------------------------
 
-// One thread (the copy engine) or kLoaders threads.  Returns false after a
-// wait ran out.
-template <bool kTma>
+// One thread (the copy engine) or kLoaders threads.  In a pair each block
+// fills its own half of the stage; both halves count on the first block's
+// barrier.  Returns false after a wait ran out.
+template <bool kTma, bool kPair>
 __device__ __forceinline__ bool fill_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
                                           uint8_t* stages, Ring& ring, uint32_t p0, uint32_t q0, uint32_t first,
-                                          uint32_t last, uint32_t tid) {
+                                          uint32_t last, uint32_t tid, uint32_t rank) {
   Operand op, oq;
   if constexpr (!kTma) {
     op = operand(a.p, a.ldp, a.p_mn, a.P, a.K, p0);
@@ -224,22 +237,30 @@ __device__ __forceinline__ bool fill_tile(const GemmArgs& a, const CUtensorMap* 
     if constexpr (!kTma) ok = __all_sync(0xFFFFFFFFu, ok);
     if (!ok) return false;
     uint8_t* dst = stages + ring.slot * a.stage_bytes;
-    const uint32_t bar = addr_of(&s.full[ring.slot]);
+    uint32_t bar = addr_of(&s.full[ring.slot]);
     if constexpr (kTma) {
-      mbar_arrive_expect(bar, a.stage_bytes);
-      copy_operand(addr_of(dst), mp, a.p_mn, p0, i * kStep, kLanes, bar);
-      copy_operand(addr_of(dst) + kPBytes, mq, a.q_mn, q0, i * kStep, a.bn, bar);
+      if (!kPair || rank == 0) mbar_arrive_expect(bar, kPair ? 2 * a.stage_bytes : a.stage_bytes);
+      if (kPair) bar = cluster_peer_address(bar, 0);
+      copy_operand<kPair>(addr_of(dst), mp, a.p_mn, p0, i * kStep, kLanes, bar);
+      copy_operand<kPair>(addr_of(dst) + kPBytes, mq, a.q_mn, q0, i * kStep, a.bq, bar);
     } else {
-      load_stage(op, oq, dst, a.bn, i * kStep, tid);
+      load_stage(op, oq, dst, a.bq, i * kStep, tid);
       fence_async_shared();
-      mbar_arrive(bar);
+      __syncwarp();
+      if (tid % 32 == 0) {
+        if (kPair)
+          mbar_arrive_cluster(cluster_peer_address(bar, 0));
+        else
+          mbar_arrive(bar);
+      }
     }
     ring.next(a.stages);
   }
   return true;
 }
 
-// One thread issues the tile's products into `tmem`.
+// One thread (of a pair's first block) issues the tile's products into `tmem`.
+template <bool kPair>
 __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint32_t stages, Ring& ring, uint32_t tmem,
                                               uint32_t first, uint32_t last) {
   // A contraction step of 16 is 32 bytes along a K-major row, 16 rows of an
@@ -252,8 +273,8 @@ __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint
     const uint64_t dp = operand_descriptor(base, kStep * 128), dq = operand_descriptor(base + kPBytes, kStep * 128);
 #pragma unroll
     for (uint32_t k = 0; k < kStep / 16; ++k)
-      mma_f16(tmem, dp + k * adv_p, dq + k * adv_q, a.idesc, i != first || k != 0);
-    mma_commit(addr_of(&s.empty[ring.slot]));
+      mma_f16<kPair>(tmem, dp + k * adv_p, dq + k * adv_q, a.idesc, i != first || k != 0);
+    mma_commit<kPair>(addr_of(&s.empty[ring.slot]));
     ring.next(a.stages);
   }
   return true;
@@ -317,58 +338,109 @@ __device__ __forceinline__ void finish16(const GemmArgs& a, float (&v)[16], uint
     }
 }
 
+template <bool kTma, bool kPair>
 __device__ __forceinline__ void setup(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
-                                      bool tma, uint32_t warp) {
+                                      uint32_t warp) {
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < a.stages; ++i) {
-      mbar_init(addr_of(&s.full[i]), tma ? 1 : kLoaders);
+      mbar_init(addr_of(&s.full[i]), kTma ? 1 : (kPair ? 2 : 1) * (kLoaders / 32));
       mbar_init(addr_of(&s.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(addr_of(&s.acc_full[i]), 1);
-      mbar_init(addr_of(&s.acc_empty[i]), 128);
+      mbar_init(addr_of(&s.acc_empty[i]), 8);  // the epilogue warps of a pair
     }
     mbar_init(addr_of(&s.drain), 1);
     s.abort = 0;
     mbar_init_fence();
-    if (tma) prefetch_tensor_map(mp), prefetch_tensor_map(mq);
+    if (kTma) prefetch_tensor_map(mp), prefetch_tensor_map(mq);
   }
-  if (warp == 1) tmem_alloc(addr_of(&s.tmem), a.tmem_columns);
+  if (warp == 1) tmem_alloc<kPair>(addr_of(&s.tmem), a.tmem_columns);
   tmem_fence_before();
   __syncthreads();
+  if (kPair) {  // the peer's barriers are ready before a copy counts on them
+    cluster_arrive_release();
+    cluster_wait();
+  }
   tmem_fence_after();
 }
 
-// Every thread, after its role.  When a wait ran out, the copies and the
-// matrix instructions still in flight are waited for, again with a bound,
-// before the block's memory is given up.  `ring`, `issued`: the copying
-// thread's next stage and an upper bound of the stages it filled.
-__device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint32_t warp, uint32_t lane, bool tma,
+// Every thread, after its role; kCluster: the cluster's blocks read or signal
+// each other's memory, so none leaves before all are done.  When a wait ran
+// out in any of them, the copies and the matrix instructions still in flight
+// are waited for, again with a bound, before the memory is given up.  `ring`,
+// `issued`: the copying thread's next stage and an upper bound of the stages
+// it filled.
+template <bool kTma, bool kPair>
+__device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint32_t warp, uint32_t lane, uint32_t rank,
                                              Ring ring, uint32_t issued) {
   tmem_fence_before();
   __syncthreads();
+  cluster_arrive_release();
+  cluster_wait();
   tmem_fence_after();
-  if (s.abort) {
+  uint32_t gave_up = s.abort;
+  if (kPair) gave_up |= ld_cluster_u32(cluster_peer_address(addr_of(const_cast<uint32_t*>(&s.abort)), rank ^ 1));
+  if (gave_up) {
     volatile uint32_t own = 0;
-    if (tma && threadIdx.x == 0) {
+    if (kTma && threadIdx.x == 0 && (!kPair || rank == 0)) {
       for (uint32_t i = 0; i < issued && i < a.stages; ++i) {
         if (ring.slot == 0) ring.slot = a.stages, ring.phase ^= 1;
         --ring.slot;
         mbar_wait(addr_of(&s.full[ring.slot]), ring.phase, &own);
       }
     }
-    if (warp == 1 && lane == 0) {
-      mma_commit(addr_of(&s.drain));
+    if (warp == 1 && lane == 0 && (!kPair || rank == 0)) {
+      mma_commit<kPair>(addr_of(&s.drain));
       mbar_wait(addr_of(&s.drain), 0, &own);
     }
     if (threadIdx.x == 0 && a.status) *a.status = uint32_t(ARX_ETIMEOUT) | (12u << 8);
+  }
+  if (kPair) {  // after the peer's abort word was read, and any drain
+    __syncwarp();
+    cluster_arrive_release();
+    cluster_wait();
+  } else {
     __syncthreads();
   }
-  if (warp == 1) tmem_free(s.tmem, a.tmem_columns);
+  if (warp == 1) tmem_free<kPair>(s.tmem, a.tmem_columns);
 }
 
 template <bool kTma>
 constexpr uint32_t kGemmThreads = kTma ? 192 : 192 + kLoaders;
+
+// The same of 4 consecutive columns.
+template <int D>
+__device__ __forceinline__ void finish4(const GemmArgs& a, float (&v)[4], uint32_t row, uint32_t col) {
+  uint16_t* out = a.out + row * a.ldout + col;
+  const uint32_t n = col < a.P ? a.P - col : 0;
+  const bool whole = a.vec && n >= 4;
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k)
+    if (a.bias && k < n) v[k] += load_param(a.bias, a.wdtype, col + k);
+  if (a.z) {
+    uint16_t* z = a.z + row * a.ldz + col;
+    if (whole) {
+      st_global(reinterpret_cast<uint2*>(z), make_uint2(Elem<D>::round2(v[0], v[1]), Elem<D>::round2(v[2], v[3])));
+    } else {
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)
+        if (k < n) z[k] = Elem<D>::round(v[k]);
+    }
+  }
+  activate<4>(v, a.act);
+  if (a.residual)
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k)
+      if (k < n) v[k] += Elem<D>::widen(a.residual[row * a.ldresidual + col + k]);
+  if (whole) {
+    st_global(reinterpret_cast<uint2*>(out), make_uint2(Elem<D>::round2(v[0], v[1]), Elem<D>::round2(v[2], v[3])));
+  } else {
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k)
+      if (k < n) out[k] = Elem<D>::round(v[k]);
+  }
+}
 
 // Tile order: bands of 8 row tiles, down the band first, so that the blocks
 // at work at one time share operands in L2.
@@ -386,35 +458,35 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
   uint8_t* stages = smem_raw + ((1024u - (addr_of(smem_raw) & 1023u)) & 1023u);
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  setup(a, &mp, &mq, s, kTma, warp);
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31, rank = cluster_ctarank();
+  setup<kTma, true>(a, &mp, &mq, s, warp);
   dependent_launch_prologue();
-  const uint32_t tiles = a.tiles_p * a.tiles_q;
+  const uint32_t tiles = a.tiles_p * a.tiles_q, first_tile = blockIdx.x / 2, step = gridDim.x / 2;
 
   Ring ring;
   uint32_t issued = 0;
   if (kTma ? threadIdx.x == 0 : warp >= 6) {
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    for (uint32_t t = first_tile; t < tiles; t += step) {
       uint32_t tp, tq;
       tile_at(a, t, tp, tq);
       issued = a.stages;
-      if (!fill_tile<kTma>(a, &mp, &mq, s, stages, ring, tp * kLanes, tq * a.bn, 0, a.steps,
-                           threadIdx.x - (kTma ? 0 : 192)))
+      if (!fill_tile<kTma, true>(a, &mp, &mq, s, stages, ring, (2 * tp + rank) * kLanes, tq * a.bn + rank * a.bq, 0,
+                                 a.steps, threadIdx.x - (kTma ? 0 : 192), rank))
         break;
     }
-  } else if (warp == 1 && lane == 0 && a.steps > 0) {
+  } else if (warp == 1 && lane == 0 && rank == 0 && a.steps > 0) {
     uint32_t n = 0;
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
+    for (uint32_t t = first_tile; t < tiles; t += step, ++n) {
       const uint32_t b = n & 1, use = n >> 1;
       if (!mbar_wait(addr_of(&s.acc_empty[b]), (use & 1) ^ 1, &s.abort)) break;
       tmem_fence_after();
-      if (!multiply_tile(a, s, addr_of(stages), ring, s.tmem + b * 256, 0, a.steps)) break;
-      mma_commit(addr_of(&s.acc_full[b]));
+      if (!multiply_tile<true>(a, s, addr_of(stages), ring, s.tmem + b * 256, 0, a.steps)) break;
+      mma_commit<true>(addr_of(&s.acc_full[b]));
     }
   } else if (warp >= 2 && warp < 6) {
     const uint32_t quarter = warp & 3;  // the accumulator lanes this warp may read
     uint32_t n = 0;
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
+    for (uint32_t t = first_tile; t < tiles; t += step, ++n) {
       uint32_t tp, tq;
       tile_at(a, t, tp, tq);
       const uint32_t b = n & 1, use = n >> 1;
@@ -422,7 +494,7 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.abort))) break;
         tmem_fence_after();
       }
-      const uint32_t row = tp * kLanes + quarter * 32 + lane, col0 = tq * a.bn;
+      const uint32_t row = (2 * tp + rank) * kLanes + quarter * 32 + lane, col0 = tq * a.bn;
       for (uint32_t c = 0; c < a.bn && col0 + c < a.Q; c += 16) {
         float v[16];
         if (a.steps > 0)
@@ -434,11 +506,12 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
         __syncwarp();
       }
       tmem_fence_before();
-      mbar_arrive(addr_of(&s.acc_empty[b]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_peer_address(addr_of(&s.acc_empty[b]), 0));
     }
   }
   __syncwarp();
-  finish_block(a, s, warp, lane, kTma, ring, issued);
+  finish_block<kTma, true>(a, s, warp, lane, rank, ring, issued);
 }
 
 // One tile per cluster; block r of the cluster takes the r-th share of the
@@ -451,7 +524,7 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
   __shared__ Shared s;
   uint8_t* stages = smem_raw + ((1024u - (addr_of(smem_raw) & 1023u)) & 1023u);
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  setup(a, &mp, &mq, s, kTma, warp);
+  setup<kTma, false>(a, &mp, &mq, s, warp);
   dependent_launch_prologue();
   const uint32_t rank = blockIdx.x % a.split, tile = blockIdx.x / a.split;
   const uint32_t tp = tile % a.tiles_p, tq = tile / a.tiles_p;
@@ -463,9 +536,10 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
 
   Ring ring;
   if (kTma ? threadIdx.x == 0 : warp >= 6) {
-    fill_tile<kTma>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, threadIdx.x - (kTma ? 0 : 192));
+    fill_tile<kTma, false>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, threadIdx.x - (kTma ? 0 : 192), 0);
   } else if (warp == 1 && lane == 0 && first < last) {
-    if (multiply_tile(a, s, addr_of(stages), ring, s.tmem, first, last)) mma_commit(addr_of(&s.acc_full[0]));
+    if (multiply_tile<false>(a, s, addr_of(stages), ring, s.tmem, first, last))
+      mma_commit<false>(addr_of(&s.acc_full[0]));
   } else if (warp >= 2 && warp < 6) {
     const uint32_t quarter = warp & 3;
     bool ok = true;
@@ -490,29 +564,26 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
   cluster_wait();
 
   // The tile's elements (column of the output = lane, row = Q's row) are
-  // shared out over the cluster's blocks; each is the sum of the partials in
-  // block order.
+  // shared out over the cluster's blocks in groups of four lanes; each is the
+  // sum of the partials in block order.
   const uint32_t nq = a.Q - q0 < a.bn ? a.Q - q0 : a.bn;
-  const uint32_t total = nq * kLanes;
-  const uint32_t per = ((total + a.split - 1) / a.split + 31) & ~31u;
-  const uint32_t end = (rank + 1) * per < total ? (rank + 1) * per : total;
+  const uint32_t groups = nq * (kLanes / 4);
+  const uint32_t per = (groups + a.split - 1) / a.split;
+  const uint32_t end = (rank + 1) * per < groups ? (rank + 1) * per : groups;
   const uint32_t at = addr_of(part);
   for (uint32_t i = rank * per + threadIdx.x; i < end; i += kGemmThreads<kTma>) {
-    const uint32_t j = p0 + (i & (kLanes - 1)), row = q0 + i / kLanes;
-    float v = 0.0f;
-    for (uint32_t r = 0; r < a.split; ++r) v += ld_cluster_f32(cluster_peer_address(at + i * 4, r));
-    if (j >= a.P) continue;
-    if (a.bias) v += load_param(a.bias, a.wdtype, j);
-    if (a.z) a.z[row * a.ldz + j] = Elem<D>::round(v);
-    float f[1] = {v};
-    activate<1>(f, a.act);
-    if (a.residual) f[0] += Elem<D>::widen(a.residual[row * a.ldresidual + j]);
-    a.out[row * a.ldout + j] = Elem<D>::round(f[0]);
+    const uint32_t j = p0 + (i * 4 & (kLanes - 1)), row = q0 + i / (kLanes / 4);
+    float4 in[8];
+#pragma unroll
+    for (uint32_t r = 0; r < 8; ++r)
+      if (r < a.split) in[r] = ld_cluster_f32x4(cluster_peer_address(at + i * 16, r));
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t r = 0; r < 8; ++r)
+      if (r < a.split) v[0] += in[r].x, v[1] += in[r].y, v[2] += in[r].z, v[3] += in[r].w;
+    finish4<D>(a, v, row, j);
   }
-  __syncwarp();
-  cluster_arrive_release();  // no block leaves while a peer reads its partials
-  cluster_wait();
-  finish_block(a, s, warp, lane, kTma, ring, last - first);
+  finish_block<kTma, false>(a, s, warp, lane, rank, ring, last - first);
 }
 
 // ---- one to four rows ------------------------------------------------------------------
@@ -642,34 +713,42 @@ cudaError_t allow_smem() {
   return e;
 }
 
-template <int D, bool kTma>
-cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, int sms, cudaStream_t st) {
-  cudaError_t e = allow_smem<gemm_wide_kernel<D, kTma>>();
-  if (e != cudaSuccess) return e;
-  const uint32_t tiles = a.tiles_p * a.tiles_q;
-  return launch_op(gemm_wide_kernel<D, kTma>, dim3(tiles < uint32_t(sms) ? tiles : uint32_t(sms)),
-                   kGemmThreads<kTma>, kStageBudget + 1024, st, a, mp, mq);
-}
-
-template <int D, bool kTma>
-cudaError_t launch_split(const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t st) {
-  cudaError_t e = allow_smem<gemm_split_kernel<D, kTma>>();
+// Launch with clusters of `cluster` blocks.
+template <auto kKernel>
+cudaError_t launch_cluster(uint32_t blocks, uint32_t threads, uint32_t cluster, uint32_t smem, cudaStream_t st,
+                           const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq) {
+  cudaError_t e = allow_smem<kKernel>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.tiles_p * a.tiles_q * a.split);
-  cfg.blockDim = dim3(kGemmThreads<kTma>);
-  cfg.dynamicSmemBytes = kStageBudget + 1024;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, gemm_split_kernel<D, kTma>, a, mp, mq);
+  e = cudaLaunchKernelEx(&cfg, kKernel, a, mp, mq);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// A persistent grid: as many pairs as the device holds at once (two blocks to
+// a pair, one block to an SM), or fewer tiles.
+template <int D, bool kTma>
+cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, int sms, cudaStream_t st) {
+  const uint32_t tiles = a.tiles_p * a.tiles_q, pairs = uint32_t(sms) / 2;
+  return launch_cluster<gemm_wide_kernel<D, kTma>>(2 * (tiles < pairs ? tiles : pairs), kGemmThreads<kTma>, 2,
+                                                   kStageBudget + 1024, st, a, mp, mq);
+}
+
+template <int D, bool kTma>
+cudaError_t launch_split(const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t st) {
+  return launch_cluster<gemm_split_kernel<D, kTma>>(a.tiles_p * a.tiles_q * a.split, kGemmThreads<kTma>, a.split,
+                                                    kStageBudget + 1024, st, a, mp, mq);
 }
 
 uint32_t ceil_div(uint64_t a, uint64_t b) { return uint32_t((a + b - 1) / b); }
@@ -727,6 +806,7 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
     a.p = cp, a.q = cq, a.ldp = c.ldp, a.ldq = c.ldq, a.p_mn = c.p_mn, a.q_mn = c.q_mn;
     a.P = uint32_t(c.rows), a.Q = uint32_t(c.cols);
     a.bn = 256;
+    a.bq = a.bn / 2;
     a.split = 1;
     a.tmem_columns = 512;
   } else {
@@ -734,17 +814,19 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
     a.P = uint32_t(c.cols), a.Q = uint32_t(c.rows);
     a.bn = a.q_mn ? 64 : 16;
     while (a.bn < a.Q && a.bn < 256) a.bn *= 2;
+    a.bq = a.bn;
     a.tmem_columns = a.bn < 32 ? 32 : a.bn;
     const uint32_t tiles = ceil_div(a.P, kLanes) * ceil_div(a.Q, a.bn);
     a.split = 1;
     while (a.split < 8 && 2 * a.split * tiles <= uint32_t(sms) && 2 * a.split <= a.steps) a.split *= 2;
   }
-  a.tiles_p = ceil_div(a.P, kLanes);
+  const uint32_t lanes = wide ? 2 * kLanes : kLanes;
+  a.tiles_p = ceil_div(a.P, lanes);
   a.tiles_q = ceil_div(a.Q, a.bn);
-  a.stage_bytes = kPBytes + a.bn * 128;
+  a.stage_bytes = kPBytes + a.bq * 128;
   a.stages = kStageBudget / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
-  a.idesc = mma_descriptor(c.dtype == ARX_BF16, a.p_mn, a.q_mn, kLanes, a.bn);
+  a.idesc = mma_descriptor(c.dtype == ARX_BF16, a.p_mn, a.q_mn, lanes, a.bn);
 
   const uint64_t p_rows = a.p_mn ? a.K : a.P, q_rows = a.q_mn ? a.K : a.Q;
   const bool tma = a.K > 0 && copyable(a.p, a.ldp, p_rows) && copyable(a.q, a.ldq, q_rows);
@@ -752,7 +834,7 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   if (tma) {
     err = encode(&mp, a.p, a.ldp, p_rows, a.p_mn ? a.P : a.K, a.p_mn ? 64 : kLanes, bf16);
     if (err != cudaSuccess) return err;
-    err = encode(&mq, a.q, a.ldq, q_rows, a.q_mn ? a.Q : a.K, a.q_mn ? 64 : a.bn, bf16);
+    err = encode(&mq, a.q, a.ldq, q_rows, a.q_mn ? a.Q : a.K, a.q_mn ? 64 : a.bq, bf16);
     if (err != cudaSuccess) return err;
   }
   if (wide) {
