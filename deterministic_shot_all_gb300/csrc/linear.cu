@@ -31,6 +31,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "arx_internal.h"
@@ -45,7 +46,12 @@ constexpr uint32_t kLanes = 128;             // rows of P in a tile (accumulator
 constexpr uint32_t kStep = 64;               // contraction elements in a stage
 constexpr uint32_t kPBytes = kLanes * 128;   // P's part of a stage
 constexpr uint32_t kMaxStages = 12;
-constexpr uint32_t kStageBudget = 200 * 1024;  // also keeps one block on an SM: tensor memory is never contended
+// Shared memory of a block's stages.  One wide block, or two split blocks of
+// up to 128 accumulator columns, fit an SM at a time, so the blocks on an SM
+// never want more tensor memory than it has (a block that waited for columns
+// while its cluster waited for it could wait forever).
+constexpr uint32_t kStageBudget = 196608, kSplitBudget = 98304;
+constexpr uint32_t kEpilogueBytes = 8 * 32 * 33 * 4;  // the wide form's epilogue warps
 constexpr uint32_t kLoaders = 512;
 
 struct GemmArgs {
@@ -65,7 +71,7 @@ struct GemmArgs {
   uint32_t split;      // blocks of a cluster that share a tile's contraction
   uint32_t tiles_p, tiles_q;
   uint32_t idesc, tmem_columns;
-  uint32_t vec;        // out, z, residual and bias allow 16-byte accesses
+  uint32_t quads, octets;  // out, z and residual allow accesses of 4 elements, of 8 (bias too)
 };
 
 struct Shared {
@@ -104,15 +110,19 @@ __device__ __forceinline__ void copy_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 
-// ---- filling a stage with plain loads -------------------------------------------------
+// ---- filling a stage by threads ---------------------------------------------------------
 //
-// A stage is (128 + bn) rows of eight 16-byte units; a unit's 8 elements may
-// start at any even address.  Aligned 16-byte loads cover it: a thread loads
-// the aligned unit at or below its address, takes the next one from its
-// neighbour in the row (the last of a row loads it), and shifts the 8
-// elements out of the pair.  Nothing outside [lo, hi), the matrix's first and
-// last byte, is touched: units whose aligned loads would cross them go element
-// by element.
+// A stage is (128 + bq) rows of eight 16-byte units; a unit's 8 elements may
+// start at any even address, and end outside the matrix (zeros are filled in).
+// A thread reads its units in words that every row of both operands is aligned
+// to -- kWord = 8 bytes, 4, or 2: the five 4-byte words around the unit,
+// shifted by half a word where it lies between words.  The addresses advance
+// by a constant from stage to stage, so that a unit costs about ten
+// instructions (with its address and bounds worked out anew it cost 70, which
+// took the issue slots: 1.3 us a stage of 32 KB).  The first and the last
+// stage of a contraction, and units that the matrix's edge cuts, take the
+// general path: nothing outside [lo, hi), the matrix's first and last byte,
+// is read.
 
 struct Operand {
   const uint16_t* p;
@@ -130,131 +140,166 @@ __device__ __forceinline__ Operand operand(const uint16_t* p, uint64_t ld, uint3
   return o;
 }
 
-// In flight: one unit of a thread.
+// A unit on its way: four words, or, where its address lies between words,
+// five that are to be shifted by half a word.
 struct Unit {
-  uint4 a, b;
-  uintptr_t at;    // address of the unit's first element
-  int n;           // its elements inside the matrix, at most 8 (0 or less: none)
-  uint32_t flags;  // 1: `a` was loaded, 2: `b` was loaded
+  uint32_t w[5];
 };
 
-__device__ __forceinline__ void unit_load(Unit& t, const Operand& o, uint32_t id, uint32_t k0) {
-  const uint32_t line = id >> 3, u = id & 7u;
-  const uint32_t row = o.mn ? k0 + (line & 63u) : o.row0 + line;
-  const uint32_t col = (o.mn ? o.row0 + (line >> 6) * 64 : k0) + u * 8;
-  t.a = t.b = make_uint4(0, 0, 0, 0);
-  t.n = row < o.nrows ? int(o.ncols) - int(col) : -8;
-  t.at = reinterpret_cast<uintptr_t>(o.p + row * o.ld + col);
-  t.flags = 0;
-  const uintptr_t q = t.at & ~uintptr_t(15);
-  // Also loaded when only the unit before needs it.
-  if (t.n > -8 && q >= o.lo && q + 16 <= o.hi) {
-    t.a = *reinterpret_cast<const uint4*>(q);
-    t.flags = 1;
+// Row and column of a unit in the matrix as stored, k0 the stage's first
+// contraction element.
+__device__ __forceinline__ uint32_t unit_row(const Operand& o, uint32_t id, uint32_t k0) {
+  return o.mn ? k0 + (id >> 3 & 63u) : o.row0 + (id >> 3);
+}
+__device__ __forceinline__ uint32_t unit_col(const Operand& o, uint32_t id, uint32_t k0) {
+  return (o.mn ? o.row0 + (id >> 9) * 64 : k0) + (id & 7u) * 8;
+}
+
+// General path: element by element.
+__device__ __noinline__ Unit unit_edge(const uint16_t* p, int n) {
+  Unit t = {};
+  const uint32_t skip = uint32_t(reinterpret_cast<uintptr_t>(p) & 2) >> 1;
+  for (int i = 0; i < 8 && i < n; ++i) {
+    const uint32_t v = uint32_t(p[i]) << (16 * ((i + skip) & 1));
+    const uint32_t at = (i + skip) >> 1;
+#pragma unroll
+    for (uint32_t k = 0; k < 5; ++k)
+      if (k == at) t.w[k] |= v;
   }
-  if (u == 7 && t.n > 0 && (t.at & 15) != 0 && q + 32 <= o.hi) {
-    t.b = *reinterpret_cast<const uint4*>(q + 16);
-    t.flags |= 2;
+  return t;
+}
+
+template <int kWord>
+__device__ __forceinline__ void unit_fast(Unit& t, const uint8_t* p, bool shifted) {
+  if constexpr (kWord == 8) {
+    const uint2 a = reinterpret_cast<const uint2*>(p)[0], b = reinterpret_cast<const uint2*>(p)[1];
+    t.w[0] = a.x, t.w[1] = a.y, t.w[2] = b.x, t.w[3] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    if (kWord == 2 && shifted) t.w[4] = reinterpret_cast<const uint32_t*>(p)[4];
   }
 }
 
-__device__ __forceinline__ void unit_store(Unit& t, uint32_t id, uint8_t* dst) {
-  const uint32_t u = id & 7u;
-  uint4 nb;
-  nb.x = __shfl_down_sync(0xFFFFFFFFu, t.a.x, 1);
-  nb.y = __shfl_down_sync(0xFFFFFFFFu, t.a.y, 1);
-  nb.z = __shfl_down_sync(0xFFFFFFFFu, t.a.z, 1);
-  nb.w = __shfl_down_sync(0xFFFFFFFFu, t.a.w, 1);
-  const uint32_t nf = __shfl_down_sync(0xFFFFFFFFu, t.flags, 1);
-  if (u != 7) {
-    t.b = nb;
-    if (nf & 1) t.flags |= 2;
-  }
-  const uint32_t mis = uint32_t(t.at & 15);
-  const int n = t.n > 8 ? 8 : t.n;
-  uint32_t w[4] = {0, 0, 0, 0};
-  if (n > 0) {
-    if ((t.flags & 1) && (mis + 2 * n <= 16 || (t.flags & 2))) {
-      uint32_t s[8] = {t.a.x, t.a.y, t.a.z, t.a.w, t.b.x, t.b.y, t.b.z, t.b.w};
-      if (mis & 8)
-#pragma unroll
-        for (int i = 0; i < 6; ++i) s[i] = s[i + 2];
-      if (mis & 4)
-#pragma unroll
-        for (int i = 0; i < 5; ++i) s[i] = s[i + 1];
-      const uint32_t shift = (mis & 2) * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(s[i], s[i + 1], shift);
-      if (n < 8)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] &= n >= 2 * i + 2 ? 0xFFFFFFFFu : (n == 2 * i + 1 ? 0xFFFFu : 0u);
-    } else {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(t.at);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
-    }
-  }
-  const uint32_t line = id >> 3;
-  *reinterpret_cast<uint4*>(dst + line * 128 + ((u ^ (line & 7u)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+// One of a thread's places in the stages of a tile.
+struct Place {
+  const uint8_t* at;  // the unit's first word in the next stage to fetch
+  uint64_t step;      // from stage to stage
+  uint32_t id;
+  bool on, fast, shifted;
+};
+
+template <int kWord>
+__device__ __forceinline__ Place place(const Operand& o, uint32_t id, uint32_t units, uint32_t first) {
+  Place c;
+  c.id = id;
+  c.on = id < units;
+  const uint32_t row = unit_row(o, id, first * kStep), col = unit_col(o, id, first * kStep);
+  // Past the matrix's last row (MN-major: column) a unit feeds results that
+  // are not stored: whole ones read another row instead, cut ones take the
+  // general path.
+  const uint32_t safe = o.mn ? row : (row < o.nrows ? row : 0);
+  c.fast = o.mn ? col + 8 <= o.ncols : true;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(o.p + safe * o.ld + col);
+  c.shifted = kWord == 2 && (a & 2) != 0;
+  c.at = reinterpret_cast<const uint8_t*>(kWord == 2 ? a & ~uintptr_t(3) : a);
+  c.step = o.mn ? kStep * o.ld * 2 : kStep * 2;
+  return c;
 }
 
-// kN units of a thread at once: their loads are in flight together.
-template <int kN>
-__device__ __forceinline__ void load_units(const Operand& o, uint8_t* dst, uint32_t first, uint32_t k0) {
-  Unit t[kN];
-#pragma unroll
-  for (int j = 0; j < kN; ++j) unit_load(t[j], o, first + j * kLoaders, k0);
-#pragma unroll
-  for (int j = 0; j < kN; ++j) unit_store(t[j], first + j * kLoaders, dst);
+template <int kWord>
+__device__ __forceinline__ void fetch(Unit& t, Place& c, const Operand& o, uint32_t stage, bool edge) {
+  if (!c.on) return;
+  if (!edge && c.fast) {
+    unit_fast<kWord>(t, c.at, c.shifted);
+  } else {
+    const uint32_t row = unit_row(o, c.id, stage * kStep), col = unit_col(o, c.id, stage * kStep);
+    const int n = row < o.nrows ? int(o.ncols) - int(col) : 0;
+    const uint16_t* p = o.p + row * o.ld + col;
+    t = unit_edge(p, n);
+    // The row of a stage's unit past the matrix may differ from the safe one
+    // in its place between words; its zeros are the same either way.
+  }
+  c.at += c.step;
 }
 
-__device__ __forceinline__ void load_stage(const Operand& p, const Operand& q, uint8_t* dst, uint32_t bn, uint32_t k0,
-                                           uint32_t tid) {
-  load_units<kLanes * 8 / kLoaders>(p, dst, tid, k0);
-  const uint32_t units = bn * 8;
-  uint32_t i = tid;
-  for (; i + kLoaders < units; i += 2 * kLoaders) load_units<2>(q, dst + kPBytes, i, k0);
-  if (i < units) load_units<1>(q, dst + kPBytes, i, k0);  // whole warps: units and kLoaders are multiples of 32
+template <int kWord>
+__device__ __forceinline__ void put(const Unit& t, const Place& c, uint8_t* dst) {
+  if (!c.on) return;
+  const uint32_t line = c.id >> 3, u = c.id & 7u;
+  uint4 v = make_uint4(t.w[0], t.w[1], t.w[2], t.w[3]);
+  if (kWord == 2) {
+    const uint32_t s = c.shifted ? 16 : 0;
+    v = make_uint4(__funnelshift_r(t.w[0], t.w[1], s), __funnelshift_r(t.w[1], t.w[2], s),
+                   __funnelshift_r(t.w[2], t.w[3], s), __funnelshift_r(t.w[3], t.w[4], s));
+  }
+  *reinterpret_cast<uint4*>(dst + line * 128 + ((u ^ (line & 7u)) << 4)) = v;  // the copy engine's swizzle
 }
 
 // ---- the roles, for one tile -------------------------------------------------------
 
-// One thread (the copy engine) or kLoaders threads.  In a pair each block
-// fills its own half of the stage; both halves count on the first block's
-// barrier.  Returns false after a wait ran out.
-template <bool kTma, bool kPair>
-__device__ __forceinline__ bool fill_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
+// One thread.  In a pair each block fills its own half of the stage; both
+// halves count on the first block's barrier.  Returns false after a wait ran
+// out.
+template <bool kPair>
+__device__ __forceinline__ bool copy_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
                                           uint8_t* stages, Ring& ring, uint32_t p0, uint32_t q0, uint32_t first,
-                                          uint32_t last, uint32_t tid, uint32_t rank) {
-  Operand op, oq;
-  if constexpr (!kTma) {
-    op = operand(a.p, a.ldp, a.p_mn, a.P, a.K, p0);
-    oq = operand(a.q, a.ldq, a.q_mn, a.Q, a.K, q0);
-  }
+                                          uint32_t last, uint32_t rank) {
   for (uint32_t i = first; i < last; ++i) {
-    bool ok = mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort);
-    if constexpr (!kTma) ok = __all_sync(0xFFFFFFFFu, ok);
-    if (!ok) return false;
+    if (!mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort)) return false;
     uint8_t* dst = stages + ring.slot * a.stage_bytes;
     uint32_t bar = addr_of(&s.full[ring.slot]);
-    if constexpr (kTma) {
-      if (!kPair || rank == 0) mbar_arrive_expect(bar, kPair ? 2 * a.stage_bytes : a.stage_bytes);
-      if (kPair) bar = cluster_peer_address(bar, 0);
-      copy_operand<kPair>(addr_of(dst), mp, a.p_mn, p0, i * kStep, kLanes, bar);
-      copy_operand<kPair>(addr_of(dst) + kPBytes, mq, a.q_mn, q0, i * kStep, a.bq, bar);
-    } else {
-      load_stage(op, oq, dst, a.bq, i * kStep, tid);
+    if (!kPair || rank == 0) mbar_arrive_expect(bar, kPair ? 2 * a.stage_bytes : a.stage_bytes);
+    if (kPair) bar = cluster_peer_address(bar, 0);
+    copy_operand<kPair>(addr_of(dst), mp, a.p_mn, p0, i * kStep, kLanes, bar);
+    copy_operand<kPair>(addr_of(dst) + kPBytes, mq, a.q_mn, q0, i * kStep, a.bq, bar);
+    ring.next(a.stages);
+  }
+  return true;
+}
+
+// kLoaders threads: the same as copy_tile where rows are off 16 bytes (bq <=
+// 128: two units of P and up to two of Q to a thread).  The words of the next
+// stages (two; one of the five-word kind) are in flight while a stage is stored.
+template <int kWord, bool kPair>
+__device__ __forceinline__ bool load_tile(const GemmArgs& a, Shared& s, uint8_t* stages, Ring& ring, uint32_t p0,
+                                          uint32_t q0, uint32_t first, uint32_t last, uint32_t tid) {
+  constexpr int kBuffers = kWord == 2 ? 2 : 3;
+  const Operand op = operand(a.p, a.ldp, a.p_mn, a.P, a.K, p0), oq = operand(a.q, a.ldq, a.q_mn, a.Q, a.K, q0);
+  Place c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    c[j] = j < 2 ? place<kWord>(op, tid + j * kLoaders, kLanes * 8, first)
+                 : place<kWord>(oq, tid + (j - 2) * kLoaders, a.bq * 8, first);
+  Unit t[kBuffers][4];
+  const auto fetch_stage = [&](Unit(&u)[4], uint32_t i) {
+    const bool edge = i == 0 || i + 1 == a.steps;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fetch<kWord>(u[j], c[j], j < 2 ? op : oq, i, edge);
+  };
+#pragma unroll
+  for (int b = 0; b + 1 < kBuffers; ++b)
+    if (first + b < last) fetch_stage(t[b], first + b);
+  for (uint32_t i = first; i < last; i += kBuffers) {
+#pragma unroll
+    for (int b = 0; b < kBuffers; ++b) {
+      if (i + b >= last) break;
+      if (i + b + kBuffers - 1 < last) fetch_stage(t[(b + kBuffers - 1) % kBuffers], i + b + kBuffers - 1);
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort))) return false;
+      uint8_t* dst = stages + ring.slot * a.stage_bytes;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) put<kWord>(t[b][j], c[j], j < 2 ? dst : dst + kPBytes);
       fence_async_shared();
       __syncwarp();
+      const uint32_t bar = addr_of(&s.full[ring.slot]);
       if (tid % 32 == 0) {
         if (kPair)
           mbar_arrive_cluster(cluster_peer_address(bar, 0));
         else
           mbar_arrive(bar);
       }
+      ring.next(a.stages);
     }
-    ring.next(a.stages);
   }
   return true;
 }
@@ -280,63 +325,76 @@ __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint
   return true;
 }
 
-// Bias, z, activation, residual of 16 consecutive columns of a row.
+// Epilogue of 16 consecutive columns of a row, from registers: rows and
+// parameters on 16-byte boundaries, whole groups.
 template <int D>
 __device__ __forceinline__ void finish16(const GemmArgs& a, float (&v)[16], uint32_t row, uint32_t col) {
-  uint16_t* out = a.out + row * a.ldout + col;
-  const uint32_t n = a.Q - col;
-  if (a.vec && n >= 16) {
-    if (a.bias) {
-      float b[8];
+  if (a.bias) {
+    float b[8];
 #pragma unroll
-      for (int h = 0; h < 16; h += 8) {
-        load_params<8>(a.bias, a.wdtype, col + h, b);
+    for (int h = 0; h < 16; h += 8) {
+      load_params<8>(a.bias, a.wdtype, col + h, b);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[h + k] += b[k];
-      }
+      for (int k = 0; k < 8; ++k) v[h + k] += b[k];
     }
-    Pack<D, 8> o;
-    if (a.z) {
-#pragma unroll
-      for (int h = 0; h < 16; h += 8) {
-        o.set(reinterpret_cast<const float(&)[8]>(v[h]));
-        o.store(a.z + row * a.ldz + col + h);
-      }
-    }
-    activate<16>(v, a.act);
-    if (a.residual) {
-      float r[8];
-#pragma unroll
-      for (int h = 0; h < 16; h += 8) {
-        o.load(a.residual + row * a.ldresidual + col + h);
-        o.get(r);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[h + k] += r[k];
-      }
-    }
+  }
+  Pack<D, 8> o;
+  if (a.z) {
 #pragma unroll
     for (int h = 0; h < 16; h += 8) {
       o.set(reinterpret_cast<const float(&)[8]>(v[h]));
-      o.store(out + h);
+      o.store(a.z + row * a.ldz + col + h);
     }
-    return;
   }
-  if (a.bias)
-#pragma unroll
-    for (uint32_t k = 0; k < 16; ++k)
-      if (k < n) v[k] += load_param(a.bias, a.wdtype, col + k);
-  if (a.z)
-#pragma unroll
-    for (uint32_t k = 0; k < 16; ++k)
-      if (k < n) a.z[row * a.ldz + col + k] = Elem<D>::round(v[k]);
   activate<16>(v, a.act);
+  if (a.residual) {
+    float r[8];
 #pragma unroll
-  for (uint32_t k = 0; k < 16; ++k)
-    if (k < n) {
-      if (a.residual) v[k] += Elem<D>::widen(a.residual[row * a.ldresidual + col + k]);
-      out[k] = Elem<D>::round(v[k]);
+    for (int h = 0; h < 16; h += 8) {
+      o.load(a.residual + row * a.ldresidual + col + h);
+      o.get(r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[h + k] += r[k];
     }
+  }
+#pragma unroll
+  for (int h = 0; h < 16; h += 8) {
+    o.set(reinterpret_cast<const float(&)[8]>(v[h]));
+    o.store(a.out + row * a.ldout + col + h);
+  }
 }
+
+// Any other alignment: a warp's 32 rows by 32 columns, staged in shared memory
+// as [row][33].  A lane takes a column and walks down the rows, so that the
+// warp accesses a row's line at a time; each lane on its own row, element by
+// element, would touch 32 lines with every access.
+template <int D>
+__device__ __forceinline__ void finish_staged(const GemmArgs& a, const float* staged, uint32_t row0, uint32_t col,
+                                              uint32_t lane) {
+  const uint32_t rows = row0 < a.P ? (a.P - row0 < 32 ? a.P - row0 : 32) : 0;
+  if (col >= a.Q) return;
+  const float bias = a.bias ? load_param(a.bias, a.wdtype, col) : 0.0f;
+#pragma unroll 8
+  for (uint32_t r = 0; r < rows; ++r) {
+    const uint64_t row = row0 + r;
+    float v[1] = {staged[r * 33 + lane] + bias};
+    float res = 0.0f;
+    if (a.residual) res = Elem<D>::widen(a.residual[row * a.ldresidual + col]);
+    if (a.z) a.z[row * a.ldz + col] = Elem<D>::round(v[0]);
+    activate<1>(v, a.act);
+    a.out[row * a.ldout + col] = Elem<D>::round(v[0] + res);
+  }
+}
+
+// Warps: the copying one, the multiplying one, the epilogue's -- eight (two to
+// a quarter of the lanes, halving the columns), four beside loading threads --
+// and the loading threads.
+template <bool kTma>
+constexpr uint32_t kEpilogueWarps = kTma ? 8 : 4;
+template <bool kTma>
+constexpr uint32_t kFirstLoader = (2 + kEpilogueWarps<kTma>) * 32;
+template <bool kTma>
+constexpr uint32_t kGemmThreads = kFirstLoader<kTma> + (kTma ? 0 : kLoaders);
 
 template <bool kTma, bool kPair>
 __device__ __forceinline__ void setup(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
@@ -348,7 +406,7 @@ __device__ __forceinline__ void setup(const GemmArgs& a, const CUtensorMap* mp, 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(addr_of(&s.acc_full[i]), 1);
-      mbar_init(addr_of(&s.acc_empty[i]), 8);  // the epilogue warps of a pair
+      mbar_init(addr_of(&s.acc_empty[i]), 2 * kEpilogueWarps<kTma>);  // of a pair
     }
     mbar_init(addr_of(&s.drain), 1);
     s.abort = 0;
@@ -406,15 +464,12 @@ __device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint3
   if (warp == 1) tmem_free<kPair>(s.tmem, a.tmem_columns);
 }
 
-template <bool kTma>
-constexpr uint32_t kGemmThreads = kTma ? 192 : 192 + kLoaders;
-
 // The same of 4 consecutive columns.
 template <int D>
 __device__ __forceinline__ void finish4(const GemmArgs& a, float (&v)[4], uint32_t row, uint32_t col) {
   uint16_t* out = a.out + row * a.ldout + col;
   const uint32_t n = col < a.P ? a.P - col : 0;
-  const bool whole = a.vec && n >= 4;
+  const bool whole = a.quads && n >= 4;
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k)
     if (a.bias && k < n) v[k] += load_param(a.bias, a.wdtype, col + k);
@@ -451,10 +506,11 @@ __device__ __forceinline__ void tile_at(const GemmArgs& a, uint32_t t, uint32_t&
   tp = 8u * b + (in - tq * rows);
 }
 
-template <int D, bool kTma>
-__global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
+template <int D, int kWord>
+__global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     gemm_wide_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap mp,
                      const __grid_constant__ CUtensorMap mq) {
+  constexpr bool kTma = kWord == 16;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
   uint8_t* stages = smem_raw + ((1024u - (addr_of(smem_raw) & 1023u)) & 1023u);
@@ -465,14 +521,18 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
 
   Ring ring;
   uint32_t issued = 0;
-  if (kTma ? threadIdx.x == 0 : warp >= 6) {
+  if (kTma ? threadIdx.x == 0 : threadIdx.x >= kFirstLoader<kTma>) {
     for (uint32_t t = first_tile; t < tiles; t += step) {
       uint32_t tp, tq;
       tile_at(a, t, tp, tq);
+      const uint32_t p0 = (2 * tp + rank) * kLanes, q0 = tq * a.bn + rank * a.bq;
       issued = a.stages;
-      if (!fill_tile<kTma, true>(a, &mp, &mq, s, stages, ring, (2 * tp + rank) * kLanes, tq * a.bn + rank * a.bq, 0,
-                                 a.steps, threadIdx.x - (kTma ? 0 : 192), rank))
-        break;
+      bool ok;
+      if constexpr (kTma)
+        ok = copy_tile<true>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
+      else
+        ok = load_tile<kWord, true>(a, s, stages, ring, p0, q0, 0, a.steps, threadIdx.x - kFirstLoader<kTma>);
+      if (!ok) break;
     }
   } else if (warp == 1 && lane == 0 && rank == 0 && a.steps > 0) {
     uint32_t n = 0;
@@ -483,7 +543,7 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
       if (!multiply_tile<true>(a, s, addr_of(stages), ring, s.tmem + b * 256, 0, a.steps)) break;
       mma_commit<true>(addr_of(&s.acc_full[b]));
     }
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp >= 2 && warp < 2 + kEpilogueWarps<kTma>) {
     const uint32_t quarter = warp & 3;  // the accumulator lanes this warp may read
     uint32_t n = 0;
     for (uint32_t t = first_tile; t < tiles; t += step, ++n) {
@@ -494,16 +554,31 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.abort))) break;
         tmem_fence_after();
       }
-      const uint32_t row = (2 * tp + rank) * kLanes + quarter * 32 + lane, col0 = tq * a.bn;
-      for (uint32_t c = 0; c < a.bn && col0 + c < a.Q; c += 16) {
-        float v[16];
-        if (a.steps > 0)
-          tmem_load16(s.tmem + b * 256 + c + (quarter * 32 << 16), v);
-        else
+      const uint32_t row0 = (2 * tp + rank) * kLanes + quarter * 32, col0 = tq * a.bn;
+      float* staged = reinterpret_cast<float*>(stages + kStageBudget) + (warp - 2) * 32 * 33;
+      const bool whole = a.octets && col0 + a.bn <= a.Q;
+      const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
+      for (uint32_t c = c0; c < c0 + half && col0 + c < a.Q; c += 32) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-        if (row < a.P) finish16<D>(a, v, row, col0 + c);
-        __syncwarp();
+        for (uint32_t h = 0; h < 32; h += 16) {
+          float v[16];
+          if (a.steps > 0)
+            tmem_load16(s.tmem + b * 256 + c + h + (quarter * 32 << 16), v);
+          else
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+          if (whole) {
+            if (row0 + lane < a.P) finish16<D>(a, v, row0 + lane, col0 + c + h);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) staged[lane * 33 + h + k] = v[k];
+          }
+          __syncwarp();
+        }
+        if (!whole) {
+          finish_staged<D>(a, staged, row0, col0 + c + lane, lane);
+          __syncwarp();
+        }
       }
       tmem_fence_before();
       __syncwarp();
@@ -516,10 +591,11 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
 
 // One tile per cluster; block r of the cluster takes the r-th share of the
 // contraction.  P's rows are the output's columns here, Q's rows its rows.
-template <int D, bool kTma>
-__global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
+template <int D, int kWord>
+__global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     gemm_split_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap mp,
                       const __grid_constant__ CUtensorMap mq) {
+  constexpr bool kTma = kWord == 16;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
   uint8_t* stages = smem_raw + ((1024u - (addr_of(smem_raw) & 1023u)) & 1023u);
@@ -535,12 +611,15 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
   float* part = reinterpret_cast<float*>(stages);  // [bn][128 lanes], once the stages are done with
 
   Ring ring;
-  if (kTma ? threadIdx.x == 0 : warp >= 6) {
-    fill_tile<kTma, false>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, threadIdx.x - (kTma ? 0 : 192), 0);
+  if (kTma ? threadIdx.x == 0 : threadIdx.x >= kFirstLoader<kTma>) {
+    if constexpr (kTma)
+      copy_tile<false>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, 0);
+    else
+      load_tile<kWord, false>(a, s, stages, ring, p0, q0, first, last, threadIdx.x - kFirstLoader<kTma>);
   } else if (warp == 1 && lane == 0 && first < last) {
     if (multiply_tile<false>(a, s, addr_of(stages), ring, s.tmem, first, last))
       mma_commit<false>(addr_of(&s.acc_full[0]));
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp >= 2 && warp < 2 + kEpilogueWarps<kTma>) {
     const uint32_t quarter = warp & 3;
     bool ok = true;
     if (first < last) {
@@ -548,7 +627,7 @@ __global__ void __launch_bounds__(kGemmThreads<kTma>, 1)
       tmem_fence_after();
     }
     if (ok)
-      for (uint32_t c = 0; c < a.bn; c += 16) {
+      for (uint32_t c = (warp - 2) / 4 * 16; c < a.bn; c += kEpilogueWarps<kTma> * 4) {
         float v[16];
         if (first < last)
           tmem_load16(s.tmem + c + (quarter * 32 << 16), v);
@@ -708,7 +787,7 @@ cudaError_t allow_smem() {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kStageBudget + 1024));
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kStageBudget + 1024 + kEpilogueBytes));
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
   return e;
 }
@@ -736,22 +815,64 @@ cudaError_t launch_cluster(uint32_t blocks, uint32_t threads, uint32_t cluster, 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+uint32_t split_budget(uint32_t bn) { return bn <= 128 ? kSplitBudget : kStageBudget; }
+
 // A persistent grid: as many pairs as the device holds at once (two blocks to
 // a pair, one block to an SM), or fewer tiles.
-template <int D, bool kTma>
+template <int D, int kWord>
 cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, int sms, cudaStream_t st) {
   const uint32_t tiles = a.tiles_p * a.tiles_q, pairs = uint32_t(sms) / 2;
-  return launch_cluster<gemm_wide_kernel<D, kTma>>(2 * (tiles < pairs ? tiles : pairs), kGemmThreads<kTma>, 2,
-                                                   kStageBudget + 1024, st, a, mp, mq);
+  return launch_cluster<gemm_wide_kernel<D, kWord>>(2 * (tiles < pairs ? tiles : pairs), kGemmThreads<kWord == 16>, 2,
+                                                   kStageBudget + 1024 + kEpilogueBytes, st, a, mp, mq);
 }
 
-template <int D, bool kTma>
+template <int D, int kWord>
 cudaError_t launch_split(const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t st) {
-  return launch_cluster<gemm_split_kernel<D, kTma>>(a.tiles_p * a.tiles_q * a.split, kGemmThreads<kTma>, a.split,
-                                                    kStageBudget + 1024, st, a, mp, mq);
+  return launch_cluster<gemm_split_kernel<D, kWord>>(a.tiles_p * a.tiles_q * a.split, kGemmThreads<kWord == 16>, a.split,
+                                                    split_budget(a.bn) + 1024, st, a, mp, mq);
 }
 
 uint32_t ceil_div(uint64_t a, uint64_t b) { return uint32_t((a + b - 1) / b); }
+
+// Which form, with how many rows of Q to a tile and how many blocks to a
+// tile's contraction: the one with the least estimated time, in SM cycles.
+struct Form {
+  bool wide;
+  uint32_t bn, split;
+};
+
+Form choose_form(const GemmCall& c, uint32_t steps, uint32_t word, uint32_t sms) {
+  Form best{};
+  double least = 0;
+  const auto consider = [&](const Form& f, double cycles) {
+    if (best.bn == 0 || cycles < least) best = f, least = cycles;
+  };
+  // A stage costs its copies or its products, whichever is longer.  Measured:
+  // an SM takes in 50 bytes a cycle in pairs, 36 for one split block and 44
+  // for two; loading threads 17 (words of 8 bytes) or 12, 10 in pairs; the
+  // products take 2.5 cycles a row of Q.
+  const auto stage = [&](uint32_t bn, uint32_t bq, double rate) {
+    const double copies = (kPBytes + bq * 128.0) / rate, products = 2.5 * bn;
+    return copies > products ? copies : products;
+  };
+  for (uint32_t bn = 256; bn >= 128; bn /= 2) {
+    const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, bn);
+    const double waves = ceil_div(tiles, sms / 2);
+    consider(Form{true, bn, 1}, waves * steps * stage(bn, bn / 2, word == 16 ? 50 : 10) + 6000 + 40 * bn);
+  }
+  // Joining and storing a tile takes about 25 cycles a row of Q, 45 through
+  // the cluster.
+  for (uint32_t bn = c.p_mn ? 64 : 16; bn <= (word == 16 ? 256 : 128); bn *= 2) {
+    const uint32_t tiles = ceil_div(c.cols, kLanes) * ceil_div(c.rows, bn);
+    for (uint32_t split = 1; split <= 8 && (split == 1 || split <= steps); split *= 2) {
+      const double on_sm = ceil_div(uint64_t(tiles) * split, sms), rate = word == 16 ? (bn <= 128 && on_sm > 1 ? 44 : 36) : word == 8 ? 17 : 12;
+      consider(Form{false, bn, split},
+               on_sm * (ceil_div(steps, split) * stage(bn, bn, rate) + (split > 1 ? 45 : 25) * bn) + 6000);
+    }
+    if (bn >= c.rows) break;
+  }
+  return best;
+}
 
 template <int D, int kV>
 cudaError_t launch_dot(const GemmArgs& a, cudaStream_t st) {
@@ -781,10 +902,14 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   a.K = uint32_t(c.k);
   a.steps = ceil_div(c.k, kStep);
 
-  const auto aligned = [](const void* p, uint64_t ld) {
-    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0);
+  const auto aligned = [](const void* p, uint64_t ld, unsigned elements) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % (2 * elements) == 0 && ld % elements == 0);
   };
-  a.vec = aligned(a.out, a.ldout) && aligned(a.z, a.ldz) && aligned(a.residual, a.ldresidual) && aligned(a.bias, 8);
+  const auto out_aligned = [&](unsigned n) {
+    return aligned(a.out, a.ldout, n) && aligned(a.z, a.ldz, n) && aligned(a.residual, a.ldresidual, n);
+  };
+  a.quads = out_aligned(4);
+  a.octets = out_aligned(8) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
 
   const bool bf16 = c.dtype == ARX_BF16;
   if (c.rows <= kDotRows && !c.p_mn && !c.q_mn) {
@@ -799,50 +924,58 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
     return units ? launch_dot<ARX_F16, 8>(a, st) : launch_dot<ARX_F16, 1>(a, st);
   }
 
-  // Wide tiles when they occupy most of the SMs, else the split form.
-  const bool wide = uint64_t(ceil_div(c.rows, kLanes)) * ceil_div(c.cols, 256) >= 100;
   const auto *cp = static_cast<const uint16_t*>(c.p), *cq = static_cast<const uint16_t*>(c.q);
+  // How the operands are brought in: 16, by the copy engine; else by threads,
+  // in the widest words that every row of both is aligned to (8, 4 or 2 bytes).
+  const uint64_t cp_rows = c.p_mn ? a.K : c.rows, cq_rows = c.q_mn ? a.K : c.cols;
+  uint64_t bits = reinterpret_cast<uintptr_t>(cp) | reinterpret_cast<uintptr_t>(cq);
+  if (cp_rows > 1) bits |= c.ldp * 2;
+  if (cq_rows > 1) bits |= c.ldq * 2;
+  uint32_t word = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
+  if (word == 16 && a.K == 0) word = 8;  // an empty matrix has no map
+  const Form form = choose_form(c, a.steps, word, uint32_t(sms));
+  const bool wide = form.wide;
+  a.bn = form.bn;
+  a.split = form.split;
   if (wide) {
     a.p = cp, a.q = cq, a.ldp = c.ldp, a.ldq = c.ldq, a.p_mn = c.p_mn, a.q_mn = c.q_mn;
     a.P = uint32_t(c.rows), a.Q = uint32_t(c.cols);
-    a.bn = 256;
     a.bq = a.bn / 2;
-    a.split = 1;
     a.tmem_columns = 512;
   } else {
     a.p = cq, a.q = cp, a.ldp = c.ldq, a.ldq = c.ldp, a.p_mn = c.q_mn, a.q_mn = c.p_mn;
     a.P = uint32_t(c.cols), a.Q = uint32_t(c.rows);
-    a.bn = a.q_mn ? 64 : 16;
-    while (a.bn < a.Q && a.bn < 256) a.bn *= 2;
     a.bq = a.bn;
     a.tmem_columns = a.bn < 32 ? 32 : a.bn;
-    const uint32_t tiles = ceil_div(a.P, kLanes) * ceil_div(a.Q, a.bn);
-    a.split = 1;
-    while (a.split < 8 && 2 * a.split * tiles <= uint32_t(sms) && 2 * a.split <= a.steps) a.split *= 2;
   }
   const uint32_t lanes = wide ? 2 * kLanes : kLanes;
   a.tiles_p = ceil_div(a.P, lanes);
   a.tiles_q = ceil_div(a.Q, a.bn);
   a.stage_bytes = kPBytes + a.bq * 128;
-  a.stages = kStageBudget / a.stage_bytes;
+  a.stages = (wide ? kStageBudget : split_budget(a.bn)) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   a.idesc = mma_descriptor(c.dtype == ARX_BF16, a.p_mn, a.q_mn, lanes, a.bn);
 
   const uint64_t p_rows = a.p_mn ? a.K : a.P, q_rows = a.q_mn ? a.K : a.Q;
-  const bool tma = a.K > 0 && copyable(a.p, a.ldp, p_rows) && copyable(a.q, a.ldq, q_rows);
   CUtensorMap mp{}, mq{};
-  if (tma) {
+  if (word == 16) {
     err = encode(&mp, a.p, a.ldp, p_rows, a.p_mn ? a.P : a.K, a.p_mn ? 64 : kLanes, bf16);
     if (err != cudaSuccess) return err;
     err = encode(&mq, a.q, a.ldq, q_rows, a.q_mn ? a.Q : a.K, a.q_mn ? 64 : a.bq, bf16);
     if (err != cudaSuccess) return err;
   }
-  if (wide) {
-    if (bf16) return tma ? launch_wide<ARX_BF16, true>(a, mp, mq, sms, st) : launch_wide<ARX_BF16, false>(a, mp, mq, sms, st);
-    return tma ? launch_wide<ARX_F16, true>(a, mp, mq, sms, st) : launch_wide<ARX_F16, false>(a, mp, mq, sms, st);
+  const auto run = [&](auto w) {
+    constexpr int kWord = decltype(w)::value;
+    if (wide)
+      return bf16 ? launch_wide<ARX_BF16, kWord>(a, mp, mq, sms, st) : launch_wide<ARX_F16, kWord>(a, mp, mq, sms, st);
+    return bf16 ? launch_split<ARX_BF16, kWord>(a, mp, mq, st) : launch_split<ARX_F16, kWord>(a, mp, mq, st);
+  };
+  switch (word) {
+    case 16: return run(std::integral_constant<int, 16>{});
+    case 8: return run(std::integral_constant<int, 8>{});
+    case 4: return run(std::integral_constant<int, 4>{});
+    default: return run(std::integral_constant<int, 2>{});
   }
-  if (bf16) return tma ? launch_split<ARX_BF16, true>(a, mp, mq, st) : launch_split<ARX_BF16, false>(a, mp, mq, st);
-  return tma ? launch_split<ARX_F16, true>(a, mp, mq, st) : launch_split<ARX_F16, false>(a, mp, mq, st);
 }
 
 }  // namespace arx
