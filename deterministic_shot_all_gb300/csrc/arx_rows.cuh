@@ -180,21 +180,61 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the TPR threads of a row (whole warps; all of the block's threads
-// call it).  `buf`: TPR / 32 floats of shared memory per row group, a fresh
-// buffer for every call between two block barriers.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* buf) {
-  v = warp_sum(v);
-  if constexpr (TPR > 32) {
-    constexpr int kWarps = TPR / 32;
-    if ((threadIdx.x & 31) == 0) buf[(threadIdx.x % TPR) / 32] = v;
+// Barrier of a row's T threads; RPC rows to a block (a hardware barrier of
+// its own for each where there are several).
+template <int T, int RPC>
+__device__ __forceinline__ void row_barrier() {
+  if constexpr (T == 32)
+    __syncwarp();
+  else if constexpr (RPC == 1)
     __syncthreads();
-    v = buf[0];
+  else
+    asm volatile("bar.sync %0, %1;" :: "r"(1 + threadIdx.x / T), "n"(T) : "memory");
+}
+
+// Sums of N values over the T threads of a row, by one barrier.  `buf`:
+// N * T / 32 floats of shared memory of the row, not those of the row's last
+// call.
+template <int T, int RPC, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* buf) {
+  constexpr int kWarps = T / 32;
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) v += buf[i];
+  for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
+  if constexpr (T > 32) {
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int n = 0; n < N; ++n) buf[n * kWarps + (threadIdx.x % T) / 32] = v[n];
+    row_barrier<T, RPC>();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      v[n] = buf[n * kWarps];
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) v[n] += buf[n * kWarps + i];
+    }
   }
-  return v;
+}
+
+template <int T, int RPC>
+__device__ __forceinline__ float row_sum(float v, float* buf) {
+  float a[1] = {v};
+  row_sums<T, RPC, 1>(a, buf);
+  return a[0];
+}
+
+// ---- asynchronous copies by threads -----------------------------------------------
+
+// 16 bytes to shared memory, both addresses aligned: the first `have` from
+// global memory, zeros after.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(have) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// All but the thread's last kGroups groups have landed.
+template <int kGroups>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(kGroups) : "memory");
 }
 
 // ---- Philox4x32-10 --------------------------------------------------------------

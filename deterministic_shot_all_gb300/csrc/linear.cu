@@ -779,24 +779,11 @@ bool copyable(const uint16_t* p, uint64_t ld, uint64_t nrows) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (nrows <= 1 || ld % 8 == 0);
 }
 
-// Dynamic shared memory above 48 KB is granted per kernel and device.
-template <auto kKernel>
-cudaError_t allow_smem() {
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kStageBudget + 1024 + kEpilogueBytes));
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
-  return e;
-}
-
 // Launch with clusters of `cluster` blocks.
 template <auto kKernel>
 cudaError_t launch_cluster(uint32_t blocks, uint32_t threads, uint32_t cluster, uint32_t smem, cudaStream_t st,
                            const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq) {
-  cudaError_t e = allow_smem<kKernel>();
+  cudaError_t e = allow_dynamic_smem<kKernel>(kStageBudget + 1024 + kEpilogueBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks);

@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -27,6 +28,19 @@ cudaError_t launch_op(void (*k)(P...), dim3 grid, unsigned threads, size_t smem,
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Dynamic shared memory above 48 KB is granted per kernel and device.
+template <auto kKernel>
+cudaError_t allow_dynamic_smem(size_t bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 // `vec`: every row of every matrix, and every vector of parameters, may be

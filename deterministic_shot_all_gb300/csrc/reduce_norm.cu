@@ -19,7 +19,7 @@ struct ReduceNormArgs {
   float *mean, *rstd;
   const uint64_t* rng;
   size_t rows, cols;
-  float eps, scale;
+  float eps, scale, inv_cols;
   uint32_t threshold;
 };
 
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(TPR* RPC) reduce_norm_kernel(const ReduceNormA
       o.store(a.h + base + c);
     }
   }
-  norm_row<ARX_BF16, TPR, NV, V>(f, cols, a.eps, a.weight, a.norm_bias, ARX_BF16, a.y + base,
+  norm_row<ARX_BF16, TPR, NV, V>(f, cols, a.inv_cols, a.eps, a.weight, a.norm_bias, ARX_BF16, a.y + base,
                                  a.mean ? a.mean + row : nullptr, a.rstd ? a.rstd + row : nullptr,
                                  buf[threadIdx.x / TPR]);
 }
@@ -106,13 +106,13 @@ __global__ void __launch_bounds__(512) reduce_norm_long_kernel(const ReduceNormA
   if (a.threshold) d = load_dropout(a.rng, a.threshold, a.scale);
   float s = 0.0f;
   for (size_t c = threadIdx.x; c < a.cols; c += 512) s += sublayer_sum<W>(a, d, row, c);
-  const float mean = row_sum<512>(s, buf[0]) / float(a.cols);
+  const float mean = row_sum<512, 1>(s, buf[0]) / float(a.cols);
   float q = 0.0f;
   for (size_t c = threadIdx.x; c < a.cols; c += 512) {
     const float v = sublayer_sum<W>(a, d, row, c) - mean;
     q += v * v;
   }
-  const float rstd = 1.0f / sqrtf(row_sum<512>(q, buf[1]) / float(a.cols) + a.eps);
+  const float rstd = 1.0f / sqrtf(row_sum<512, 1>(q, buf[1]) / float(a.cols) + a.eps);
   for (size_t c = threadIdx.x; c < a.cols; c += 512) {
     const float h = sublayer_sum<W>(a, d, row, c);
     float o = (h - mean) * rstd;
@@ -168,6 +168,7 @@ cudaError_t launch_reduce_layer_norm(const arx_reduce_layer_norm_args& c, bool v
   a.rows = c.rows;
   a.cols = c.cols;
   a.eps = c.eps;
+  a.inv_cols = 1.0f / float(c.cols);
   dropout_constants(c.p, &a.threshold, &a.scale);
   switch (c.W) {
     case 1: return run_w<1>(a, vec, st);
