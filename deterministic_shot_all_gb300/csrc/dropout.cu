@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "arx_internal.h"
@@ -19,6 +20,7 @@ namespace arx {
 namespace {
 
 constexpr int kTileThreads = 256;
+constexpr int kTileBlocks = 3;  // to an SM
 
 // Tile of a block: 2^log_tx column groups by 256 >> log_tx rows.
 struct Tile {
@@ -30,41 +32,88 @@ struct Tile {
   __device__ __forceinline__ uint32_t rows() const { return kTileThreads >> log_tx; }
 };
 
-// The 8 columns of a group, or the first n of them where the row ends inside
-// the group.  kVec: aligned vector accesses of whole groups.
-template <int D, bool kVec>
+// How a thread gets the 8 columns of its group:
+//  kVector  one aligned access of the whole group;
+//  kStaged  rows off that alignment, 32 groups to a warp: the warp loads its 256
+//           columns a line at a time, and exchanges them through shared memory;
+//  kSingle  narrow matrices off that alignment: element by element.
+enum Access { kVector, kStaged, kSingle };
+
+// Rows that a thread has in flight at once, within 85 registers.
+template <int D, int kAccess>
+constexpr int kRowsOf = kAccess == kVector ? (D == ARX_F32 ? 2 : 4) : kAccess == kStaged ? 2 : 1;
+
+template <int D, int kAccess>
 struct Group {
   using S = typename Elem<D>::S;
-  Pack<D, kVec ? 8 : 1> w[kVec ? 1 : 8];
+  static constexpr int kStageBytes = kAccess == kStaged ? 256 * int(sizeof(S)) : 0;  // of a warp
+  Pack<D, kAccess == kVector ? 8 : 1> w[kAccess == kVector ? 1 : 8];
+
+  // p: the row's element at the group's first column (kStaged: at the warp's
+  // first); n: the columns from there that exist, up to 8 (kStaged: any number).
   __device__ __forceinline__ void load(const S* p, int n) {
-    if constexpr (kVec) {
+    if constexpr (kAccess == kVector) {
       w[0].load(p);
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n)
-          w[k].load(p + k);
+      for (int k = 0; k < 8; ++k) {
+        const int i = kAccess == kStaged ? 32 * k + int(threadIdx.x & 31) : k;
+        if (i < n)
+          w[k].load(p + i);
         else
           w[k].zero();
+      }
     }
   }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int k = 0; k < (kVec ? 1 : 8); ++k) w[k].zero();
-  }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    if constexpr (kVec) {
+  __device__ __forceinline__ void get(float (&f)[8], S* stage) const {
+    if constexpr (kAccess == kVector) {
       w[0].get(f);
+    } else if constexpr (kAccess == kStaged) {
+      const int lane = threadIdx.x & 31;
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) stage[32 * k + lane] = w[k].w;
+      __syncwarp();
+      const uint4* q = reinterpret_cast<const uint4*>(stage + 8 * lane);
+      Pack<D, 8> v;
+      const uint4 a = q[0];
+      if constexpr (D == ARX_F32) {
+        const uint4 b = q[1];
+        v.w[0] = __uint_as_float(a.x), v.w[1] = __uint_as_float(a.y), v.w[2] = __uint_as_float(a.z),
+        v.w[3] = __uint_as_float(a.w), v.w[4] = __uint_as_float(b.x), v.w[5] = __uint_as_float(b.y),
+        v.w[6] = __uint_as_float(b.z), v.w[7] = __uint_as_float(b.w);
+      } else {
+        v.w[0] = a.x, v.w[1] = a.y, v.w[2] = a.z, v.w[3] = a.w;
+      }
+      v.get(f);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = Elem<D>::widen(w[k].w);
     }
   }
-  static __device__ __forceinline__ void put(S* p, const float (&f)[8], int n) {
-    if constexpr (kVec) {
+  static __device__ __forceinline__ void put(S* p, const float (&f)[8], int n, S* stage) {
+    if constexpr (kAccess == kVector) {
       Pack<D, 8> o;
       o.set(f);
       o.store(p);
+    } else if constexpr (kAccess == kStaged) {
+      const int lane = threadIdx.x & 31;
+      Pack<D, 8> o;
+      o.set(f);
+      __syncwarp();
+      uint4* q = reinterpret_cast<uint4*>(stage + 8 * lane);
+      if constexpr (D == ARX_F32) {
+        q[0] = make_uint4(__float_as_uint(o.w[0]), __float_as_uint(o.w[1]), __float_as_uint(o.w[2]),
+                          __float_as_uint(o.w[3]));
+        q[1] = make_uint4(__float_as_uint(o.w[4]), __float_as_uint(o.w[5]), __float_as_uint(o.w[6]),
+                          __float_as_uint(o.w[7]));
+      } else {
+        q[0] = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (32 * k + lane < n) p[32 * k + lane] = stage[32 * k + lane];
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -73,41 +122,90 @@ struct Group {
   }
 };
 
-__device__ __forceinline__ void load_group_params(const void* p, int dtype, uint32_t c, int n, float (&f)[8]) {
+// A thread's columns: its group, the group's first column, and what the
+// accesses start from.
+template <int D, int kAccess>
+struct Columns {
+  uint32_t group, first;  // generator group, its first column
+  uint32_t at;            // column the accesses start from
+  int n;                  // columns from there that exist (at most 8 unless staged)
+  bool any;               // the thread takes part (all of a staged warp, or none)
+  __device__ __forceinline__ Columns(const Tile& t, uint64_t cols) {
+    group = t.group();
+    first = group * 8u;
+    at = kAccess == kStaged ? first - 8u * (threadIdx.x & 31) : first;
+    any = at < cols;
+    n = any ? (kAccess != kStaged && cols - at > 8 ? 8 : int(cols - at)) : 0;
+  }
+};
+
+__device__ __forceinline__ void load_group_params(const void* p, int dtype, uint32_t c, uint64_t cols, float (&f)[8]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = k < n ? load_param(p, dtype, c + k) : 0.0f;
+  for (int k = 0; k < 8; ++k) f[k] = c + k < cols ? load_param(p, dtype, c + k) : 0.0f;
 }
 
-template <int D, bool kVec>
-__global__ void __launch_bounds__(kTileThreads) dropout_add_kernel(const arx_dropout_add_args a, Tile t,
+// Eight kept-or-not decisions, computed while the row's loads are in flight.
+__device__ __forceinline__ uint32_t keep_mask(const DropoutState& d, uint32_t group, uint32_t row) {
+  const uint4 r = philox4x32_10(group, row, d.o0, d.o1, d.k0, d.k1);
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m |= uint32_t(dropout_value(r, k) >= d.threshold) << k;
+  return m;
+}
+
+__device__ __forceinline__ void apply_mask(float (&f)[8], uint32_t m, float scale) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = (m >> k & 1) ? f[k] * scale : 0.0f;
+}
+
+template <int D, int kAccess>
+__global__ void __launch_bounds__(kTileThreads, kTileBlocks) dropout_add_kernel(const arx_dropout_add_args a, Tile t,
                                                                    uint32_t threshold, float scale) {
+  constexpr int kRows = kRowsOf<D, kAccess>;
+  using G = Group<D, kAccess>;
   using S = typename Elem<D>::S;
+  __shared__ __align__(16) uint8_t stages[kTileThreads / 32 * G::kStageBytes + 16];
+  S* stage = reinterpret_cast<S*>(stages + threadIdx.x / 32 * G::kStageBytes);
   dependent_launch_prologue();
-  const uint32_t g = t.group(), c = g * 8u;
-  if (c >= a.cols) return;
-  const int n = int(a.cols - c < 8 ? a.cols - c : 8);
+  const Columns<D, kAccess> c(t, a.cols);
+  if (!c.any) return;
   DropoutState d{};
   if (threshold) d = load_dropout(a.rng, threshold, scale);
   float b[8] = {};
-  if (a.bias) load_group_params(a.bias, a.wdtype, c, n, b);
-  const S* x = static_cast<const S*>(a.x) + c;
-  const S* r = static_cast<const S*>(a.residual) + c;
-  S* out = static_cast<S*>(a.out) + c;
-  for (size_t row = size_t(blockIdx.y) * t.rows() + t.ty(); row < a.rows; row += size_t(gridDim.y) * t.rows()) {
-    Group<D, kVec> vx, vr;
-    vx.load(x + row * a.ldx, n);
-    if (a.residual) vr.load(r + row * a.ldresidual, n);
-    float f[8], h[8];
-    vx.get(f);
+  if (a.bias) load_group_params(a.bias, a.wdtype, c.first, a.cols, b);
+  const S* x = static_cast<const S*>(a.x) + c.at;
+  const S* r = static_cast<const S*>(a.residual) + c.at;
+  S* out = static_cast<S*>(a.out) + c.at;
+  const size_t step = size_t(gridDim.y) * t.rows();
+  for (size_t row0 = size_t(blockIdx.y) * t.rows() + t.ty(); row0 < a.rows; row0 += kRows * step) {
+    G vx[kRows], vr[kRows];
+    uint32_t keep[kRows];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] += b[k];
-    if (threshold) dropout8(f, d, g, uint32_t(row));
-    if (a.residual) {
-      vr.get(h);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] += h[k];
+    for (int i = 0; i < kRows; ++i) {
+      const size_t row = row0 + i * step;
+      if (row >= a.rows) break;
+      vx[i].load(x + row * a.ldx, c.n);
+      if (a.residual) vr[i].load(r + row * a.ldresidual, c.n);
     }
-    Group<D, kVec>::put(out + row * a.ldout, f, n);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (threshold) keep[i] = keep_mask(d, c.group, uint32_t(row0 + i * step));
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const size_t row = row0 + i * step;
+      if (row >= a.rows) break;
+      float f[8], h[8];
+      vx[i].get(f, stage);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] += b[k];
+      if (threshold) apply_mask(f, keep[i], d.scale);
+      if (a.residual) {
+        vr[i].get(h, stage);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] += h[k];
+      }
+      G::put(out + row * a.ldout, f, c.n, stage);
+    }
   }
 }
 
@@ -131,60 +229,88 @@ __device__ __forceinline__ void store_part(const float (&acc)[8], const Tile& t,
   }
 }
 
-template <int D, bool kVec>
-__global__ void __launch_bounds__(kTileThreads) dropout_add_bwd_kernel(const arx_dropout_add_bwd_args a, Tile t,
+template <int D, int kAccess>
+__global__ void __launch_bounds__(kTileThreads, kTileBlocks) dropout_add_bwd_kernel(const arx_dropout_add_bwd_args a, Tile t,
                                                                        uint32_t threshold, float scale) {
+  constexpr int kRows = kRowsOf<D, kAccess>;
+  using G = Group<D, kAccess>;
   using S = typename Elem<D>::S;
+  __shared__ __align__(16) uint8_t stages[kTileThreads / 32 * G::kStageBytes + 16];
+  S* stage = reinterpret_cast<S*>(stages + threadIdx.x / 32 * G::kStageBytes);
   dependent_launch_prologue();
-  const uint32_t g = t.group(), c = g * 8u;
-  const int n = c >= a.cols ? 0 : int(a.cols - c < 8 ? a.cols - c : 8);
+  const Columns<D, kAccess> c(t, a.cols);
   DropoutState d{};
   if (threshold) d = load_dropout(a.rng, threshold, scale);
   float acc[8] = {};
-  if (n > 0) {
-    const S* dout = static_cast<const S*>(a.dout) + c;
-    S* dx = static_cast<S*>(a.dx) + c;
-    for (size_t row = size_t(blockIdx.y) * t.rows() + t.ty(); row < a.rows; row += size_t(gridDim.y) * t.rows()) {
-      Group<D, kVec> v;
-      v.load(dout + row * a.lddout, n);
-      float f[8];
-      v.get(f);
-      if (threshold) dropout8(f, d, g, uint32_t(row));
+  if (c.any) {
+    const S* dout = static_cast<const S*>(a.dout) + c.at;
+    S* dx = static_cast<S*>(a.dx) + c.at;
+    const size_t step = size_t(gridDim.y) * t.rows();
+    for (size_t row0 = size_t(blockIdx.y) * t.rows() + t.ty(); row0 < a.rows; row0 += kRows * step) {
+      G v[kRows];
+      uint32_t keep[kRows];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += f[k];
-      if (a.dx) Group<D, kVec>::put(dx + row * a.lddx, f, n);
+      for (int i = 0; i < kRows; ++i)
+        if (row0 + i * step < a.rows) v[i].load(dout + (row0 + i * step) * a.lddout, c.n);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (threshold) keep[i] = keep_mask(d, c.group, uint32_t(row0 + i * step));
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (row0 + i * step >= a.rows) break;
+        float f[8];
+        v[i].get(f, stage);
+        if (threshold) apply_mask(f, keep[i], d.scale);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += f[k];
+        if (a.dx) G::put(dx + (row0 + i * step) * a.lddx, f, c.n, stage);
+      }
     }
   }
-  if (a.dbias) store_part(acc, t, c, a.cols, static_cast<float*>(a.workspace));
+  if (a.dbias) store_part(acc, t, c.first, a.cols, static_cast<float*>(a.workspace));
 }
 
-template <int D, bool kVec>
-__global__ void __launch_bounds__(kTileThreads) act_grad_kernel(const ActGradCall a, Tile t) {
+template <int D, int kAccess>
+__global__ void __launch_bounds__(kTileThreads, kTileBlocks) act_grad_kernel(const ActGradCall a, Tile t) {
+  constexpr int kRows = kRowsOf<D, kAccess>;
+  using G = Group<D, kAccess>;
   using S = typename Elem<D>::S;
+  __shared__ __align__(16) uint8_t stages[kTileThreads / 32 * G::kStageBytes + 16];
+  S* stage = reinterpret_cast<S*>(stages + threadIdx.x / 32 * G::kStageBytes);
   dependent_launch_prologue();
-  const uint32_t c = t.group() * 8u;
-  const int n = c >= a.cols ? 0 : int(a.cols - c < 8 ? a.cols - c : 8);
+  const Columns<D, kAccess> c(t, a.cols);
   float acc[8] = {};
-  if (n > 0) {
-    const S* dout = static_cast<const S*>(a.dout) + c;
-    const S* z = static_cast<const S*>(a.z) + c;
-    S* dz = static_cast<S*>(a.dz) + c;
-    for (size_t row = size_t(blockIdx.y) * t.rows() + t.ty(); row < a.rows; row += size_t(gridDim.y) * t.rows()) {
-      Group<D, kVec> v, vz;
-      v.load(dout + row * a.lddout, n);
-      if (a.z) vz.load(z + row * a.ldz, n);
-      float f[8], h[8];
-      v.get(f);
-      if (a.z) {
-        vz.get(h);
-        multiply_activation_grad<8>(f, h, a.act);
+  if (c.any) {
+    const S* dout = static_cast<const S*>(a.dout) + c.at;
+    const S* z = static_cast<const S*>(a.z) + c.at;
+    S* dz = static_cast<S*>(a.dz) + c.at;
+    const size_t step = size_t(gridDim.y) * t.rows();
+    for (size_t row0 = size_t(blockIdx.y) * t.rows() + t.ty(); row0 < a.rows; row0 += kRows * step) {
+      G v[kRows], vz[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const size_t row = row0 + i * step;
+        if (row >= a.rows) break;
+        v[i].load(dout + row * a.lddout, c.n);
+        if (a.z) vz[i].load(z + row * a.ldz, c.n);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += f[k];
-      if (a.dz) Group<D, kVec>::put(dz + row * a.lddz, f, n);
+      for (int i = 0; i < kRows; ++i) {
+        const size_t row = row0 + i * step;
+        if (row >= a.rows) break;
+        float f[8], h[8];
+        v[i].get(f, stage);
+        if (a.z) {
+          vz[i].get(h, stage);
+          multiply_activation_grad<8>(f, h, a.act);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += f[k];
+        if (a.dz) G::put(dz + row * a.lddz, f, c.n, stage);
+      }
     }
   }
-  if (a.dbias) store_part(acc, t, c, a.cols, a.part);
+  if (a.dbias) store_part(acc, t, c.first, a.cols, a.part);
 }
 
 // out[c] = sum over i < parts of p[i][c]: 32 columns per block, 8 lanes of
@@ -218,14 +344,14 @@ Tile tile_of(uint64_t cols) {
   return t;
 }
 
-// Row chunks of the tiled kernels: about eight blocks of 256 threads for
-// each of the 152 SMs over the whole grid, and no chunk without rows.
+// Row chunks of the tiled kernels: as many blocks as 152 SMs hold at once over
+// the whole grid, and no chunk without rows.
 unsigned row_chunks(uint64_t rows, uint64_t cols) {
   const Tile t = tile_of(cols);
   const uint64_t groups = (cols + 7) / 8;
   const uint64_t tiles = (groups + (uint64_t(1) << t.log_tx) - 1) >> t.log_tx;
   const uint64_t per = kTileThreads >> t.log_tx;
-  uint64_t chunks = 1216 / tiles;
+  uint64_t chunks = 152 * kTileBlocks / tiles;
   if (chunks < 1) chunks = 1;
   const uint64_t most = (rows + per - 1) / per;
   if (chunks > most) chunks = most;
@@ -238,13 +364,23 @@ dim3 tile_grid(uint64_t rows, uint64_t cols) {
   return dim3(unsigned((groups + (uint64_t(1) << t.log_tx) - 1) >> t.log_tx), row_chunks(rows, cols));
 }
 
+// Calls f with the access of a matrix as a constant.
+template <typename F>
+cudaError_t with_access(bool vec, uint64_t cols, F f) {
+  if (vec) return f(std::integral_constant<int, kVector>{});
+  if (tile_of(cols).log_tx == 5) return f(std::integral_constant<int, kStaged>{});
+  return f(std::integral_constant<int, kSingle>{});
+}
+
 template <int D>
 cudaError_t dropout_add(const arx_dropout_add_args& a, bool vec, cudaStream_t st) {
   uint32_t T;
   float s;
   dropout_constants(a.p, &T, &s);
-  auto k = vec ? dropout_add_kernel<D, true> : dropout_add_kernel<D, false>;
-  return launch_op(k, tile_grid(a.rows, a.cols), kTileThreads, 0, st, a, tile_of(a.cols), T, s);
+  return with_access(vec, a.cols, [&](auto m) {
+    return launch_op(dropout_add_kernel<D, decltype(m)::value>, tile_grid(a.rows, a.cols), kTileThreads, 0, st, a,
+                     tile_of(a.cols), T, s);
+  });
 }
 
 template <int D>
@@ -252,8 +388,18 @@ cudaError_t dropout_add_bwd(const arx_dropout_add_bwd_args& a, bool vec, cudaStr
   uint32_t T;
   float s;
   dropout_constants(a.p, &T, &s);
-  auto k = vec ? dropout_add_bwd_kernel<D, true> : dropout_add_bwd_kernel<D, false>;
-  return launch_op(k, tile_grid(a.rows, a.cols), kTileThreads, 0, st, a, tile_of(a.cols), T, s);
+  return with_access(vec, a.cols, [&](auto m) {
+    return launch_op(dropout_add_bwd_kernel<D, decltype(m)::value>, tile_grid(a.rows, a.cols), kTileThreads, 0, st, a,
+                     tile_of(a.cols), T, s);
+  });
+}
+
+template <int D>
+cudaError_t act_grad(const ActGradCall& c, bool vec, cudaStream_t st) {
+  return with_access(vec, c.cols, [&](auto m) {
+    return launch_op(act_grad_kernel<D, decltype(m)::value>, tile_grid(c.rows, c.cols), kTileThreads, 0, st, c,
+                     tile_of(c.cols));
+  });
 }
 
 }  // namespace
@@ -290,9 +436,7 @@ cudaError_t launch_act_grad(const ActGradCall& c, bool vec, cudaStream_t st) {
   unsigned parts = 0;
   if (c.rows > 0 && (c.dz || c.dbias)) {
     parts = row_chunks(c.rows, c.cols);
-    auto k = c.dtype == ARX_BF16 ? (vec ? act_grad_kernel<ARX_BF16, true> : act_grad_kernel<ARX_BF16, false>)
-                                 : (vec ? act_grad_kernel<ARX_F16, true> : act_grad_kernel<ARX_F16, false>);
-    const cudaError_t e = launch_op(k, tile_grid(c.rows, c.cols), kTileThreads, 0, st, c, tile_of(c.cols));
+    const cudaError_t e = c.dtype == ARX_BF16 ? act_grad<ARX_BF16>(c, vec, st) : act_grad<ARX_F16>(c, vec, st);
     if (e != cudaSuccess) return e;
   }
   return launch_column_sum(c.part, parts, c.cols, c.dbias, nullptr, nullptr, c.wdtype, st);

@@ -44,8 +44,11 @@ __global__ void __launch_bounds__(TPR* RPC) norm_fwd_kernel(const arx_layer_norm
 // biases in registers and rows coming in through a ring.  (One block to a row
 // reads 8 bytes of 32-bit parameters for every 4 of a 16-bit row: 45.6 us at
 // [8192, 4096], 2.3 times the bytes' time.)
+template <int T, int RPC>
+constexpr int kFwdBlocks = T * RPC >= 512 ? 1 : 3;
+
 template <int D, int T, int RPC, int NV, int V, int kRing>
-__global__ void __launch_bounds__(T* RPC, 512 / (T * RPC) < 1 ? 1 : 512 / (T * RPC))
+__global__ void __launch_bounds__(T* RPC, kFwdBlocks<T, RPC>)
     norm_fwd_ring_kernel(const arx_layer_norm_args a, uint32_t slot, float inv_cols) {
   using S = typename Elem<D>::S;
   constexpr int kWarps = T / 32;
@@ -352,15 +355,19 @@ cudaError_t fwd(const arx_layer_norm_args& a, cudaStream_t st) {
                    1.0f / float(a.cols));
 }
 
+// Shared memory of an SM that its blocks' rings may fill, and of one block.
+constexpr size_t kRingBytes = 222 * 1024, kBlockRingBytes = 220 * 1024;
+
 template <int D, int T, int RPC, int NV, int V>
 cudaError_t fwd_ring(const arx_layer_norm_args& a, cudaStream_t st) {
-  constexpr int kRing = 4, kBlocks = T * RPC >= 512 ? 1 : 2;
+  constexpr int kRing = 5;
   const uint32_t slot = row_slot(a.cols, sizeof(typename Elem<D>::S), V);
-  const size_t smem = size_t(RPC) * kRing * slot;  // at most 4 x 32 KB with 8192 columns of fp32
-  const uint64_t need = (a.rows + RPC - 1) / RPC;
-  const unsigned most = kBlocks * kSms;
+  const size_t smem = size_t(RPC) * kRing * slot;  // at most 5 x 32 KB, 8192 columns of fp32
+  size_t per_sm = kRingBytes / (smem + 2048);
+  if (per_sm > kFwdBlocks<T, RPC>) per_sm = kFwdBlocks<T, RPC>;
+  const uint64_t need = (a.rows + RPC - 1) / RPC, most = per_sm * kSms;
   constexpr auto kernel = norm_fwd_ring_kernel<D, T, RPC, NV, V, kRing>;
-  const cudaError_t e = allow_dynamic_smem<kernel>(136 * 1024);
+  const cudaError_t e = allow_dynamic_smem<kernel>(kBlockRingBytes);
   if (e != cudaSuccess) return e;
   return launch_op(kernel, dim3(unsigned(need < most ? need : most)), T * RPC, smem, st, a, slot,
                    1.0f / float(a.cols));
@@ -394,9 +401,6 @@ cudaError_t fwd_any(const arx_layer_norm_args& a, bool vec, cudaStream_t st) {
 
 // Row chunks of the column-sum kernel for long rows.
 constexpr unsigned kColumnChunks = 64;
-// Shared memory of an SM that its blocks' rings may fill, and of one block.
-constexpr size_t kRingBytes = 222 * 1024, kBlockRingBytes = 220 * 1024;
-
 // As many blocks as 152 SMs hold at once: a constant, so that the order of the
 // sums depends on the sizes alone.
 template <int D, int T, int RPC, int NV, int V, int kRing>

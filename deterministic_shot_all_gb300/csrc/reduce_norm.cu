@@ -136,12 +136,13 @@ cudaError_t run(const ReduceNormArgs& a, cudaStream_t st) {
 template <int W>
 cudaError_t run_w(const ReduceNormArgs& a, bool vec, cudaStream_t st) {
   const size_t n = a.cols;
+  const bool many = a.rows > 4 * 152;
   if (vec) {
     if (n <= 256) return run<W, 32, 4, 1, 8>(a, st);
-    if (n <= 1024) return run<W, 128, 1, 1, 8>(a, st);
-    if (n <= 2048) return run<W, 256, 1, 1, 8>(a, st);
-    if (n <= 4096) return run<W, 512, 1, 1, 8>(a, st);
-    if (n <= 8192) return run<W, 512, 1, 2, 8>(a, st);
+    if (n <= 1024) return many ? run<W, 64, 1, 2, 8>(a, st) : run<W, 128, 1, 1, 8>(a, st);
+    if (n <= 2048) return many ? run<W, 128, 1, 2, 8>(a, st) : run<W, 256, 1, 1, 8>(a, st);
+    if (n <= 4096) return many ? run<W, 256, 1, 2, 8>(a, st) : run<W, 512, 1, 1, 8>(a, st);
+    if (n <= 8192) return many ? run<W, 512, 1, 2, 8>(a, st) : run<W, 1024, 1, 1, 8>(a, st);
     if (n <= 16384) return run<W, 512, 1, 4, 8>(a, st);
   } else {
     if (n <= 256) return run<W, 32, 4, 8, 1>(a, st);
