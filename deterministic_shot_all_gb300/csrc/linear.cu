@@ -49,9 +49,13 @@ constexpr uint32_t kMaxStages = 12;
 // Shared memory of a block's stages.  One wide block, or two split blocks of
 // up to 128 accumulator columns, fit an SM at a time, so the blocks on an SM
 // never want more tensor memory than it has (a block that waited for columns
-// while its cluster waited for it could wait forever).
-constexpr uint32_t kStageBudget = 196608, kSplitBudget = 98304;
-constexpr uint32_t kEpilogueBytes = 8 * 32 * 33 * 4;  // the wide form's epilogue warps
+// while its cluster waited for it could wait forever); of those with loading
+// threads (704) one fits.  Loads of threads pass through what the stages leave
+// of the SM's memory as L1: [1003, 4100] x [2044, 4100] took 64 us beside 96 KB
+// of stages and 125 beside 192.
+constexpr uint32_t kStageBudget = 196608, kSplitBudget = 98304, kLoadedBudget = 98304;
+constexpr uint32_t kStagedBytes = 32 * 33 * 4;  // of an epilogue warp of the wide form
+constexpr uint32_t kMostShared = kStageBudget + 1024 + 8 * kStagedBytes;
 constexpr uint32_t kLoaders = 512;
 
 struct GemmArgs {
@@ -59,6 +63,7 @@ struct GemmArgs {
   uint64_t ldp, ldq;
   uint32_t P, Q, K;
   uint32_t p_mn, q_mn;
+  uint32_t p_copy, q_copy;  // the copy engine brings the operand in, not threads
   uint16_t *out, *z;
   const void* bias;
   const uint16_t* residual;
@@ -114,9 +119,9 @@ __device__ __forceinline__ void copy_operand(uint32_t dst, const CUtensorMap* ma
 //
 // A stage is (128 + bq) rows of eight 16-byte units; a unit's 8 elements may
 // start at any even address, and end outside the matrix (zeros are filled in).
-// A thread reads its units in words that every row of both operands is aligned
-// to -- kWord = 8 bytes, 4, or 2: the five 4-byte words around the unit,
-// shifted by half a word where it lies between words.  The addresses advance
+// A thread reads its units in words of 8 bytes where every row is aligned to
+// them (kWord = 8), else (kWord = 2) in 4-byte words: the five around the unit,
+// shifted by half a word, where it lies between words.  The addresses advance
 // by a constant from stage to stage, so that a unit costs about ten
 // instructions (with its address and bounds worked out anew it cost 70, which
 // took the issue slots: 1.3 us a stage of 32 KB).  The first and the last
@@ -189,12 +194,15 @@ struct Place {
   bool on, fast, shifted;
 };
 
+// Threads beyond the operand's units fetch another's once more and store
+// nothing: a load under a condition of its own is waited for where the
+// condition ends, and the stages in flight with it (64 us became 127).
 template <int kWord>
 __device__ __forceinline__ Place place(const Operand& o, uint32_t id, uint32_t units, uint32_t first) {
   Place c;
-  c.id = id;
   c.on = id < units;
-  const uint32_t row = unit_row(o, id, first * kStep), col = unit_col(o, id, first * kStep);
+  c.id = c.on ? id : id % units;
+  const uint32_t row = unit_row(o, c.id, first * kStep), col = unit_col(o, c.id, first * kStep);
   // Past the matrix's last row (MN-major: column) a unit feeds results that
   // are not stored: whole ones read another row instead, cut ones take the
   // general path.
@@ -209,16 +217,12 @@ __device__ __forceinline__ Place place(const Operand& o, uint32_t id, uint32_t u
 
 template <int kWord>
 __device__ __forceinline__ void fetch(Unit& t, Place& c, const Operand& o, uint32_t stage, bool edge) {
-  if (!c.on) return;
   if (!edge && c.fast) {
     unit_fast<kWord>(t, c.at, c.shifted);
   } else {
     const uint32_t row = unit_row(o, c.id, stage * kStep), col = unit_col(o, c.id, stage * kStep);
     const int n = row < o.nrows ? int(o.ncols) - int(col) : 0;
-    const uint16_t* p = o.p + row * o.ld + col;
-    t = unit_edge(p, n);
-    // The row of a stage's unit past the matrix may differ from the safe one
-    // in its place between words; its zeros are the same either way.
+    t = unit_edge(o.p + row * o.ld + col, n);
   }
   c.at += c.step;
 }
@@ -238,44 +242,48 @@ __device__ __forceinline__ void put(const Unit& t, const Place& c, uint8_t* dst)
 
 // ---- the roles, for one tile -------------------------------------------------------
 
-// One thread.  In a pair each block fills its own half of the stage; both
-// halves count on the first block's barrier.  Returns false after a wait ran
-// out.
+// One thread: the operands that the copy engine can address.  In a pair each
+// block fills its own half of the stage; both halves count on the first
+// block's barrier.  Returns false after a wait ran out.
 template <bool kPair>
 __device__ __forceinline__ bool copy_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
                                           uint8_t* stages, Ring& ring, uint32_t p0, uint32_t q0, uint32_t first,
                                           uint32_t last, uint32_t rank) {
+  const uint32_t bytes = (a.p_copy ? kPBytes : 0) + (a.q_copy ? a.bq * 128 : 0);
   for (uint32_t i = first; i < last; ++i) {
     if (!mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort)) return false;
     uint8_t* dst = stages + ring.slot * a.stage_bytes;
     uint32_t bar = addr_of(&s.full[ring.slot]);
-    if (!kPair || rank == 0) mbar_arrive_expect(bar, kPair ? 2 * a.stage_bytes : a.stage_bytes);
+    if (!kPair || rank == 0) mbar_arrive_expect(bar, kPair ? 2 * bytes : bytes);
     if (kPair) bar = cluster_peer_address(bar, 0);
-    copy_operand<kPair>(addr_of(dst), mp, a.p_mn, p0, i * kStep, kLanes, bar);
-    copy_operand<kPair>(addr_of(dst) + kPBytes, mq, a.q_mn, q0, i * kStep, a.bq, bar);
+    if (a.p_copy) copy_operand<kPair>(addr_of(dst), mp, a.p_mn, p0, i * kStep, kLanes, bar);
+    if (a.q_copy) copy_operand<kPair>(addr_of(dst) + kPBytes, mq, a.q_mn, q0, i * kStep, a.bq, bar);
     ring.next(a.stages);
   }
   return true;
 }
 
-// kLoaders threads: the same as copy_tile where rows are off 16 bytes (bq <=
-// 128: two units of P and up to two of Q to a thread).  The words of the next
-// stages (two; one of the five-word kind) are in flight while a stage is stored.
-template <int kWord, bool kPair>
+// kLoaders threads: the operands whose rows are off 16 bytes -- both, or the
+// one that the copy engine does not bring -- two units of each to a thread (bq
+// <= 128).  The words of the next stages (two; one of the five-word kind) are
+// in flight while a stage is stored.
+template <int kWord, bool kBoth, bool kPair>
 __device__ __forceinline__ bool load_tile(const GemmArgs& a, Shared& s, uint8_t* stages, Ring& ring, uint32_t p0,
                                           uint32_t q0, uint32_t first, uint32_t last, uint32_t tid) {
-  constexpr int kBuffers = kWord == 2 ? 2 : 3;
-  const Operand op = operand(a.p, a.ldp, a.p_mn, a.P, a.K, p0), oq = operand(a.q, a.ldq, a.q_mn, a.Q, a.K, q0);
-  Place c[4];
+  constexpr int kBuffers = kWord == 2 ? 2 : 3, kUnits = kBoth ? 4 : 2;
+  const bool p_first = kBoth || !a.p_copy;
+  const Operand oq = operand(a.q, a.ldq, a.q_mn, a.Q, a.K, q0),
+                o = p_first ? operand(a.p, a.ldp, a.p_mn, a.P, a.K, p0) : oq;
+  Place c[kUnits];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    c[j] = j < 2 ? place<kWord>(op, tid + j * kLoaders, kLanes * 8, first)
+  for (int j = 0; j < kUnits; ++j)
+    c[j] = j < 2 ? place<kWord>(o, tid + j * kLoaders, p_first ? kLanes * 8 : a.bq * 8, first)
                  : place<kWord>(oq, tid + (j - 2) * kLoaders, a.bq * 8, first);
-  Unit t[kBuffers][4];
-  const auto fetch_stage = [&](Unit(&u)[4], uint32_t i) {
+  Unit t[kBuffers][kUnits];
+  const auto fetch_stage = [&](Unit(&u)[kUnits], uint32_t i) {
     const bool edge = i == 0 || i + 1 == a.steps;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fetch<kWord>(u[j], c[j], j < 2 ? op : oq, i, edge);
+    for (int j = 0; j < kUnits; ++j) fetch<kWord>(u[j], c[j], j < 2 ? o : oq, i, edge);
   };
 #pragma unroll
   for (int b = 0; b + 1 < kBuffers; ++b)
@@ -288,7 +296,7 @@ __device__ __forceinline__ bool load_tile(const GemmArgs& a, Shared& s, uint8_t*
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort))) return false;
       uint8_t* dst = stages + ring.slot * a.stage_bytes;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) put<kWord>(t[b][j], c[j], j < 2 ? dst : dst + kPBytes);
+      for (int j = 0; j < kUnits; ++j) put<kWord>(t[b][j], c[j], j < 2 && p_first ? dst : dst + kPBytes);
       fence_async_shared();
       __syncwarp();
       const uint32_t bar = addr_of(&s.full[ring.slot]);
@@ -401,7 +409,7 @@ __device__ __forceinline__ void setup(const GemmArgs& a, const CUtensorMap* mp, 
                                       uint32_t warp) {
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < a.stages; ++i) {
-      mbar_init(addr_of(&s.full[i]), kTma ? 1 : (kPair ? 2 : 1) * (kLoaders / 32));
+      mbar_init(addr_of(&s.full[i]), (a.p_copy | a.q_copy) + (kTma ? 0 : (kPair ? 2 : 1) * (kLoaders / 32)));
       mbar_init(addr_of(&s.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -411,7 +419,8 @@ __device__ __forceinline__ void setup(const GemmArgs& a, const CUtensorMap* mp, 
     mbar_init(addr_of(&s.drain), 1);
     s.abort = 0;
     mbar_init_fence();
-    if (kTma) prefetch_tensor_map(mp), prefetch_tensor_map(mq);
+    if (a.p_copy) prefetch_tensor_map(mp);
+    if (a.q_copy) prefetch_tensor_map(mq);
   }
   if (warp == 1) tmem_alloc<kPair>(addr_of(&s.tmem), a.tmem_columns);
   tmem_fence_before();
@@ -429,7 +438,7 @@ __device__ __forceinline__ void setup(const GemmArgs& a, const CUtensorMap* mp, 
 // are waited for, again with a bound, before the memory is given up.  `ring`,
 // `issued`: the copying thread's next stage and an upper bound of the stages
 // it filled.
-template <bool kTma, bool kPair>
+template <bool kPair>
 __device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint32_t warp, uint32_t lane, uint32_t rank,
                                              Ring ring, uint32_t issued) {
   tmem_fence_before();
@@ -441,7 +450,7 @@ __device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint3
   if (kPair) gave_up |= ld_cluster_u32(cluster_peer_address(addr_of(const_cast<uint32_t*>(&s.abort)), rank ^ 1));
   if (gave_up) {
     volatile uint32_t own = 0;
-    if (kTma && threadIdx.x == 0 && (!kPair || rank == 0)) {
+    if ((a.p_copy | a.q_copy) && threadIdx.x == 0 && (!kPair || rank == 0)) {
       for (uint32_t i = 0; i < issued && i < a.stages; ++i) {
         if (ring.slot == 0) ring.slot = a.stages, ring.phase ^= 1;
         --ring.slot;
@@ -506,7 +515,7 @@ __device__ __forceinline__ void tile_at(const GemmArgs& a, uint32_t t, uint32_t&
   tp = 8u * b + (in - tq * rows);
 }
 
-template <int D, int kWord>
+template <int D, int kWord, bool kBoth>
 __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     gemm_wide_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap mp,
                      const __grid_constant__ CUtensorMap mq) {
@@ -521,17 +530,18 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
 
   Ring ring;
   uint32_t issued = 0;
-  if (kTma ? threadIdx.x == 0 : threadIdx.x >= kFirstLoader<kTma>) {
+  const bool copies = threadIdx.x == 0 && (a.p_copy | a.q_copy), loads = !kTma && threadIdx.x >= kFirstLoader<kTma>;
+  if (copies || loads) {
     for (uint32_t t = first_tile; t < tiles; t += step) {
       uint32_t tp, tq;
       tile_at(a, t, tp, tq);
       const uint32_t p0 = (2 * tp + rank) * kLanes, q0 = tq * a.bn + rank * a.bq;
       issued = a.stages;
-      bool ok;
-      if constexpr (kTma)
+      bool ok = true;
+      if (copies)
         ok = copy_tile<true>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
-      else
-        ok = load_tile<kWord, true>(a, s, stages, ring, p0, q0, 0, a.steps, threadIdx.x - kFirstLoader<kTma>);
+      else if constexpr (!kTma)
+        ok = load_tile<kWord, kBoth, true>(a, s, stages, ring, p0, q0, 0, a.steps, threadIdx.x - kFirstLoader<kTma>);
       if (!ok) break;
     }
   } else if (warp == 1 && lane == 0 && rank == 0 && a.steps > 0) {
@@ -555,7 +565,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
         tmem_fence_after();
       }
       const uint32_t row0 = (2 * tp + rank) * kLanes + quarter * 32, col0 = tq * a.bn;
-      float* staged = reinterpret_cast<float*>(stages + kStageBudget) + (warp - 2) * 32 * 33;
+      float* staged = reinterpret_cast<float*>(stages + a.stages * a.stage_bytes) + (warp - 2) * 32 * 33;
       const bool whole = a.octets && col0 + a.bn <= a.Q;
       const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
       for (uint32_t c = c0; c < c0 + half && col0 + c < a.Q; c += 32) {
@@ -586,13 +596,13 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     }
   }
   __syncwarp();
-  finish_block<kTma, true>(a, s, warp, lane, rank, ring, issued);
+  finish_block<true>(a, s, warp, lane, rank, ring, issued);
 }
 
 // One tile per cluster; block r of the cluster takes the r-th share of the
 // contraction.  P's rows are the output's columns here, Q's rows its rows.
-template <int D, int kWord>
-__global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
+template <int D, int kWord, bool kBoth>
+__global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1)
     gemm_split_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap mp,
                       const __grid_constant__ CUtensorMap mq) {
   constexpr bool kTma = kWord == 16;
@@ -611,11 +621,12 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
   float* part = reinterpret_cast<float*>(stages);  // [bn][128 lanes], once the stages are done with
 
   Ring ring;
-  if (kTma ? threadIdx.x == 0 : threadIdx.x >= kFirstLoader<kTma>) {
-    if constexpr (kTma)
-      copy_tile<false>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, 0);
-    else
-      load_tile<kWord, false>(a, s, stages, ring, p0, q0, first, last, threadIdx.x - kFirstLoader<kTma>);
+  const bool copies = threadIdx.x == 0 && (a.p_copy | a.q_copy), loads = !kTma && threadIdx.x >= kFirstLoader<kTma>;
+  if (copies) {
+    copy_tile<false>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, 0);
+  } else if (loads) {
+    if constexpr (!kTma)
+      load_tile<kWord, kBoth, false>(a, s, stages, ring, p0, q0, first, last, threadIdx.x - kFirstLoader<kTma>);
   } else if (warp == 1 && lane == 0 && first < last) {
     if (multiply_tile<false>(a, s, addr_of(stages), ring, s.tmem, first, last))
       mma_commit<false>(addr_of(&s.acc_full[0]));
@@ -662,7 +673,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
       if (r < a.split) v[0] += in[r].x, v[1] += in[r].y, v[2] += in[r].z, v[3] += in[r].w;
     finish4<D>(a, v, row, j);
   }
-  finish_block<kTma, false>(a, s, warp, lane, rank, ring, last - first);
+  finish_block<false>(a, s, warp, lane, rank, ring, last - first);
 }
 
 // ---- one to four rows ------------------------------------------------------------------
@@ -783,7 +794,7 @@ bool copyable(const uint16_t* p, uint64_t ld, uint64_t nrows) {
 template <auto kKernel>
 cudaError_t launch_cluster(uint32_t blocks, uint32_t threads, uint32_t cluster, uint32_t smem, cudaStream_t st,
                            const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq) {
-  cudaError_t e = allow_dynamic_smem<kKernel>(kStageBudget + 1024 + kEpilogueBytes);
+  cudaError_t e = allow_dynamic_smem<kKernel>(kMostShared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks);
@@ -802,21 +813,20 @@ cudaError_t launch_cluster(uint32_t blocks, uint32_t threads, uint32_t cluster, 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-uint32_t split_budget(uint32_t bn) { return bn <= 128 ? kSplitBudget : kStageBudget; }
-
 // A persistent grid: as many pairs as the device holds at once (two blocks to
 // a pair, one block to an SM), or fewer tiles.
-template <int D, int kWord>
+template <int D, int kWord, bool kBoth>
 cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, int sms, cudaStream_t st) {
   const uint32_t tiles = a.tiles_p * a.tiles_q, pairs = uint32_t(sms) / 2;
-  return launch_cluster<gemm_wide_kernel<D, kWord>>(2 * (tiles < pairs ? tiles : pairs), kGemmThreads<kWord == 16>, 2,
-                                                   kStageBudget + 1024 + kEpilogueBytes, st, a, mp, mq);
+  return launch_cluster<gemm_wide_kernel<D, kWord, kBoth>>(2 * (tiles < pairs ? tiles : pairs), kGemmThreads<kWord == 16>, 2,
+                                                   1024 + a.stages * a.stage_bytes + kEpilogueWarps<kWord == 16> * kStagedBytes,
+                                                   st, a, mp, mq);
 }
 
-template <int D, int kWord>
+template <int D, int kWord, bool kBoth>
 cudaError_t launch_split(const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t st) {
-  return launch_cluster<gemm_split_kernel<D, kWord>>(a.tiles_p * a.tiles_q * a.split, kGemmThreads<kWord == 16>, a.split,
-                                                    split_budget(a.bn) + 1024, st, a, mp, mq);
+  return launch_cluster<gemm_split_kernel<D, kWord, kBoth>>(a.tiles_p * a.tiles_q * a.split, kGemmThreads<kWord == 16>, a.split,
+                                                    1024 + a.stages * a.stage_bytes, st, a, mp, mq);
 }
 
 uint32_t ceil_div(uint64_t a, uint64_t b) { return uint32_t((a + b - 1) / b); }
@@ -828,33 +838,37 @@ struct Form {
   uint32_t bn, split;
 };
 
-Form choose_form(const GemmCall& c, uint32_t steps, uint32_t word, uint32_t sms) {
+Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, uint32_t sms) {
   Form best{};
   double least = 0;
   const auto consider = [&](const Form& f, double cycles) {
     if (best.bn == 0 || cycles < least) best = f, least = cycles;
   };
-  // A stage costs its copies or its products, whichever is longer.  Measured:
-  // an SM takes in 50 bytes a cycle in pairs, 36 for one split block and 44
-  // for two; loading threads 17 (words of 8 bytes) or 12, 10 in pairs; the
-  // products take 2.5 cycles a row of Q.
-  const auto stage = [&](uint32_t bn, uint32_t bq, double rate) {
-    const double copies = (kPBytes + bq * 128.0) / rate, products = 2.5 * bn;
-    return copies > products ? copies : products;
+  // A stage of `rows` rows of c.p and `cols` of c.q costs its copies or its
+  // products, whichever is longer.  Measured: an SM takes in 50 bytes a cycle
+  // in pairs, 36 for one split block and 44 for two, and 16 through loading
+  // threads (12 in pairs, where the slower of two blocks counts); the products
+  // take 2.5 cycles a row of the kernel's Q.
+  const bool threads = !p_copy || !q_copy;
+  const auto stage = [&](uint32_t rows, uint32_t cols, uint32_t bn, double engine, double loaded) {
+    const double copies = rows * 128.0 / (p_copy ? engine : loaded) + cols * 128.0 / (q_copy ? engine : loaded);
+    return copies > 2.5 * bn ? copies : 2.5 * bn;
   };
   for (uint32_t bn = 256; bn >= 128; bn /= 2) {
     const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, bn);
     const double waves = ceil_div(tiles, sms / 2);
-    consider(Form{true, bn, 1}, waves * steps * stage(bn, bn / 2, word == 16 ? 50 : 10) + 6000 + 40 * bn);
+    consider(Form{true, bn, 1}, waves * steps * stage(kLanes, bn / 2, bn, 50, 12) + 6000 + 40 * bn);
   }
   // Joining and storing a tile takes about 25 cycles a row of Q, 45 through
-  // the cluster.
-  for (uint32_t bn = c.p_mn ? 64 : 16; bn <= (word == 16 ? 256 : 128); bn *= 2) {
+  // the cluster; starting and ending a block 6000, which two blocks on an SM
+  // share.
+  for (uint32_t bn = c.p_mn ? 64 : 16; bn <= (threads ? 128 : 256); bn *= 2) {
     const uint32_t tiles = ceil_div(c.cols, kLanes) * ceil_div(c.rows, bn);
+    const bool two = !threads && bn <= 128;  // blocks to an SM
     for (uint32_t split = 1; split <= 8 && (split == 1 || split <= steps); split *= 2) {
-      const double on_sm = ceil_div(uint64_t(tiles) * split, sms), rate = word == 16 ? (bn <= 128 && on_sm > 1 ? 44 : 36) : word == 8 ? 17 : 12;
-      consider(Form{false, bn, split},
-               on_sm * (ceil_div(steps, split) * stage(bn, bn, rate) + (split > 1 ? 45 : 25) * bn) + 6000);
+      const double on_sm = ceil_div(uint64_t(tiles) * split, sms), join = (split > 1 ? 45 : 25) * bn;
+      const double own = ceil_div(steps, split) * stage(bn, kLanes, bn, two && on_sm > 1 ? 44 : 36, 16) + join;
+      consider(Form{false, bn, split}, two ? on_sm * own + 6000 : on_sm * (own + 6000));
     }
     if (bn >= c.rows) break;
   }
@@ -912,26 +926,29 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   }
 
   const auto *cp = static_cast<const uint16_t*>(c.p), *cq = static_cast<const uint16_t*>(c.q);
-  // How the operands are brought in: 16, by the copy engine; else by threads,
-  // in the widest words that every row of both is aligned to (8, 4 or 2 bytes).
+  // The copy engine takes operands whose rows are on 16 bytes (an empty one has
+  // no map); threads read the others, in words of 8 bytes where every row is
+  // aligned to them.
   const uint64_t cp_rows = c.p_mn ? a.K : c.rows, cq_rows = c.q_mn ? a.K : c.cols;
-  uint64_t bits = reinterpret_cast<uintptr_t>(cp) | reinterpret_cast<uintptr_t>(cq);
-  if (cp_rows > 1) bits |= c.ldp * 2;
-  if (cq_rows > 1) bits |= c.ldq * 2;
-  uint32_t word = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
-  if (word == 16 && a.K == 0) word = 8;  // an empty matrix has no map
-  const Form form = choose_form(c, a.steps, word, uint32_t(sms));
+  const bool cp_copy = a.K > 0 && copyable(cp, c.ldp, cp_rows), cq_copy = a.K > 0 && copyable(cq, c.ldq, cq_rows);
+  uint64_t bits = 0;
+  if (!cp_copy) bits |= reinterpret_cast<uintptr_t>(cp) | (cp_rows > 1 ? c.ldp * 2 : 0);
+  if (!cq_copy) bits |= reinterpret_cast<uintptr_t>(cq) | (cq_rows > 1 ? c.ldq * 2 : 0);
+  const uint32_t word = cp_copy && cq_copy ? 16 : bits % 8 == 0 ? 8 : 2;
+  const Form form = choose_form(c, a.steps, cp_copy, cq_copy, uint32_t(sms));
   const bool wide = form.wide;
   a.bn = form.bn;
   a.split = form.split;
   if (wide) {
     a.p = cp, a.q = cq, a.ldp = c.ldp, a.ldq = c.ldq, a.p_mn = c.p_mn, a.q_mn = c.q_mn;
     a.P = uint32_t(c.rows), a.Q = uint32_t(c.cols);
+    a.p_copy = cp_copy, a.q_copy = cq_copy;
     a.bq = a.bn / 2;
     a.tmem_columns = 512;
   } else {
     a.p = cq, a.q = cp, a.ldp = c.ldq, a.ldq = c.ldp, a.p_mn = c.q_mn, a.q_mn = c.p_mn;
     a.P = uint32_t(c.cols), a.Q = uint32_t(c.rows);
+    a.p_copy = cq_copy, a.q_copy = cp_copy;
     a.bq = a.bn;
     a.tmem_columns = a.bn < 32 ? 32 : a.bn;
   }
@@ -939,30 +956,36 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   a.tiles_p = ceil_div(a.P, lanes);
   a.tiles_q = ceil_div(a.Q, a.bn);
   a.stage_bytes = kPBytes + a.bq * 128;
-  a.stages = (wide ? kStageBudget : split_budget(a.bn)) / a.stage_bytes;
+  a.stages = (word != 16 ? kLoadedBudget : wide || a.bn > 128 ? kStageBudget : kSplitBudget) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   a.idesc = mma_descriptor(c.dtype == ARX_BF16, a.p_mn, a.q_mn, lanes, a.bn);
 
   const uint64_t p_rows = a.p_mn ? a.K : a.P, q_rows = a.q_mn ? a.K : a.Q;
   CUtensorMap mp{}, mq{};
-  if (word == 16) {
+  if (a.p_copy) {
     err = encode(&mp, a.p, a.ldp, p_rows, a.p_mn ? a.P : a.K, a.p_mn ? 64 : kLanes, bf16);
     if (err != cudaSuccess) return err;
+  }
+  if (a.q_copy) {
     err = encode(&mq, a.q, a.ldq, q_rows, a.q_mn ? a.Q : a.K, a.q_mn ? 64 : a.bq, bf16);
     if (err != cudaSuccess) return err;
   }
-  const auto run = [&](auto w) {
+  const auto run = [&](auto w, auto both) {
     constexpr int kWord = decltype(w)::value;
+    constexpr bool kBoth = decltype(both)::value;
     if (wide)
-      return bf16 ? launch_wide<ARX_BF16, kWord>(a, mp, mq, sms, st) : launch_wide<ARX_F16, kWord>(a, mp, mq, sms, st);
-    return bf16 ? launch_split<ARX_BF16, kWord>(a, mp, mq, st) : launch_split<ARX_F16, kWord>(a, mp, mq, st);
+      return bf16 ? launch_wide<ARX_BF16, kWord, kBoth>(a, mp, mq, sms, st)
+                  : launch_wide<ARX_F16, kWord, kBoth>(a, mp, mq, sms, st);
+    return bf16 ? launch_split<ARX_BF16, kWord, kBoth>(a, mp, mq, st) : launch_split<ARX_F16, kWord, kBoth>(a, mp, mq, st);
   };
-  switch (word) {
-    case 16: return run(std::integral_constant<int, 16>{});
-    case 8: return run(std::integral_constant<int, 8>{});
-    case 4: return run(std::integral_constant<int, 4>{});
-    default: return run(std::integral_constant<int, 2>{});
-  }
+  using std::integral_constant;
+  const bool both = !cp_copy && !cq_copy;
+  if (word == 16) return run(integral_constant<int, 16>{}, integral_constant<bool, false>{});
+  if (word == 8)
+    return both ? run(integral_constant<int, 8>{}, integral_constant<bool, true>{})
+                : run(integral_constant<int, 8>{}, integral_constant<bool, false>{});
+  return both ? run(integral_constant<int, 2>{}, integral_constant<bool, true>{})
+              : run(integral_constant<int, 2>{}, integral_constant<bool, false>{});
 }
 
 }  // namespace arx
