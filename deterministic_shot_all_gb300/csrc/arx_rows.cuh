@@ -265,7 +265,9 @@ __device__ __forceinline__ uint4 philox4x32_10(uint32_t c0, uint32_t c1, uint32_
 // What dropout needs of a call: the generator's seed and offset, the
 // threshold T = round(65536 p) and the scale 65536 / (65536 - T).
 struct DropoutState {
-  uint32_t k0, k1, o0, o1, threshold;
+  uint32_t k0, k1, o0, o1;
+  uint32_t high;  // T << 16: a value in a word's high half is at least T when the word is at least this
+  bool none;      // T == 65536: nothing is kept
   float scale;
 };
 
@@ -274,28 +276,39 @@ __device__ __forceinline__ DropoutState load_dropout(const uint64_t* rng, uint32
   const uint64_t seed = rng[0], offset = rng[1];
   d.k0 = uint32_t(seed), d.k1 = uint32_t(seed >> 32);
   d.o0 = uint32_t(offset), d.o1 = uint32_t(offset >> 32);
-  d.threshold = threshold, d.scale = scale;
+  d.high = threshold << 16, d.none = threshold >= 65536u, d.scale = scale;
   return d;
 }
 
-// 16-bit value of column 8 * group + k.
-__device__ __forceinline__ uint32_t dropout_value(const uint4& r, int k) {
+// The words of the 8 columns of a group.
+__device__ __forceinline__ uint4 dropout_random(const DropoutState& d, uint32_t group, uint32_t row) {
+  return philox4x32_10(group, row, d.o0, d.o1, d.k0, d.k1);
+}
+
+// Whether column 8 * group + k is kept.
+__device__ __forceinline__ bool dropout_keeps(const DropoutState& d, const uint4& r, int k) {
   const uint32_t w = k < 4 ? (k < 2 ? r.x : r.y) : (k < 6 ? r.z : r.w);
-  return (k & 1) ? w >> 16 : w & 0xFFFFu;
+  return !d.none && ((k & 1) ? w : w << 16) >= d.high;
 }
 
 // Dropout of the 8 columns of a group: kept values scaled, the others +0 (a
 // selection, so what is dropped may be infinite or NaN).
-__device__ __forceinline__ void dropout8(float (&f)[8], const DropoutState& d, uint32_t group, uint32_t row) {
-  const uint4 r = philox4x32_10(group, row, d.o0, d.o1, d.k0, d.k1);
+__device__ __forceinline__ void dropout_apply(float (&f)[8], const DropoutState& d, const uint4& r) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = dropout_value(r, k) >= d.threshold ? f[k] * d.scale : 0.0f;
+  for (int k = 0; k < 8; ++k) f[k] = dropout_keeps(d, r, k) ? f[k] * d.scale : 0.0f;
+}
+
+__device__ __forceinline__ void dropout8(float (&f)[8], const DropoutState& d, uint32_t group, uint32_t row) {
+  dropout_apply(f, d, dropout_random(d, group, row));
 }
 
 // The same for one element.
 __device__ __forceinline__ float dropout1(float f, const DropoutState& d, uint32_t col, uint32_t row) {
-  const uint4 r = philox4x32_10(col >> 3, row, d.o0, d.o1, d.k0, d.k1);
-  return dropout_value(r, int(col & 7u)) >= d.threshold ? f * d.scale : 0.0f;
+  const uint4 r = dropout_random(d, col >> 3, row);
+  bool keep = false;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) keep = (int(col & 7u) == k) ? dropout_keeps(d, r, k) : keep;
+  return keep ? f * d.scale : 0.0f;
 }
 
 }  // namespace arx

@@ -144,20 +144,6 @@ __device__ __forceinline__ void load_group_params(const void* p, int dtype, uint
   for (int k = 0; k < 8; ++k) f[k] = c + k < cols ? load_param(p, dtype, c + k) : 0.0f;
 }
 
-// Eight kept-or-not decisions, computed while the row's loads are in flight.
-__device__ __forceinline__ uint32_t keep_mask(const DropoutState& d, uint32_t group, uint32_t row) {
-  const uint4 r = philox4x32_10(group, row, d.o0, d.o1, d.k0, d.k1);
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m |= uint32_t(dropout_value(r, k) >= d.threshold) << k;
-  return m;
-}
-
-__device__ __forceinline__ void apply_mask(float (&f)[8], uint32_t m, float scale) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = (m >> k & 1) ? f[k] * scale : 0.0f;
-}
-
 template <int D, int kAccess>
 __global__ void __launch_bounds__(kTileThreads, kTileBlocks) dropout_add_kernel(const arx_dropout_add_args a, Tile t,
                                                                    uint32_t threshold, float scale) {
@@ -179,7 +165,6 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) dropout_add_kernel(
   const size_t step = size_t(gridDim.y) * t.rows();
   for (size_t row0 = size_t(blockIdx.y) * t.rows() + t.ty(); row0 < a.rows; row0 += kRows * step) {
     G vx[kRows], vr[kRows];
-    uint32_t keep[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const size_t row = row0 + i * step;
@@ -188,17 +173,16 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) dropout_add_kernel(
       if (a.residual) vr[i].load(r + row * a.ldresidual, c.n);
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      if (threshold) keep[i] = keep_mask(d, c.group, uint32_t(row0 + i * step));
-#pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const size_t row = row0 + i * step;
       if (row >= a.rows) break;
+      uint4 random{};  // needs none of the loads in flight
+      if (threshold) random = dropout_random(d, c.group, uint32_t(row));
       float f[8], h[8];
       vx[i].get(f, stage);
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] += b[k];
-      if (threshold) apply_mask(f, keep[i], d.scale);
+      if (threshold) dropout_apply(f, d, random);
       if (a.residual) {
         vr[i].get(h, stage);
 #pragma unroll
@@ -248,19 +232,17 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) dropout_add_bwd_ker
     const size_t step = size_t(gridDim.y) * t.rows();
     for (size_t row0 = size_t(blockIdx.y) * t.rows() + t.ty(); row0 < a.rows; row0 += kRows * step) {
       G v[kRows];
-      uint32_t keep[kRows];
-#pragma unroll
+  #pragma unroll
       for (int i = 0; i < kRows; ++i)
         if (row0 + i * step < a.rows) v[i].load(dout + (row0 + i * step) * a.lddout, c.n);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        if (threshold) keep[i] = keep_mask(d, c.group, uint32_t(row0 + i * step));
-#pragma unroll
       for (int i = 0; i < kRows; ++i) {
         if (row0 + i * step >= a.rows) break;
+        uint4 random{};  // needs none of the loads in flight
+        if (threshold) random = dropout_random(d, c.group, uint32_t(row0 + i * step));
         float f[8];
         v[i].get(f, stage);
-        if (threshold) apply_mask(f, keep[i], d.scale);
+        if (threshold) dropout_apply(f, d, random);
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] += f[k];
         if (a.dx) G::put(dx + (row0 + i * step) * a.lddx, f, c.n, stage);
@@ -313,27 +295,30 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) act_grad_kernel(con
   if (a.dbias) store_part(acc, t, c.first, a.cols, a.part);
 }
 
-// out[c] = sum over i < parts of p[i][c]: 32 columns per block, 8 lanes of
-// partial rows added in order and then joined in order.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* p0, void* out0, const float* p1, void* out1,
-                                                         unsigned parts, uint64_t cols, int dtype) {
-  __shared__ float join[8][32];
+// out[c] = sum over i < parts of p[i][c]: 32 columns per block, 32 lanes of
+// partial rows, each added in order and then joined in order.
+constexpr unsigned kSumLanes = 32;
+__global__ void __launch_bounds__(32 * kSumLanes) column_sum_kernel(const float* p0, void* out0, const float* p1,
+                                                                    void* out1, unsigned parts, uint64_t cols,
+                                                                    int dtype) {
+  __shared__ float join[kSumLanes][33];
   dependent_launch_prologue();
   const float* p = blockIdx.y ? p1 : p0;
   void* out = blockIdx.y ? out1 : out0;
   if (!out) return;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const unsigned tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const size_t c = size_t(blockIdx.x) * 32 + tx;
   float s = 0.0f;
-  if (c < cols)
-    for (unsigned i = ty; i < parts; i += 8) s += p[size_t(i) * cols + c];
+  if (c < cols) {
+#pragma unroll 4
+    for (unsigned i = ty; i < parts; i += kSumLanes) s += p[size_t(i) * cols + c];
+  }
   join[ty][tx] = s;
   __syncthreads();
-  if (ty == 0 && c < cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += join[i][tx];
-    store_param(out, dtype, c, s);
-  }
+  // Warp ty joins column ty's lanes.
+  s = warp_sum(join[tx][ty]);
+  const size_t mine = size_t(blockIdx.x) * 32 + ty;
+  if (tx == 0 && mine < cols) store_param(out, dtype, mine, s);
 }
 
 // Tile width of a matrix: as many groups as it has, up to 32.
@@ -445,7 +430,7 @@ cudaError_t launch_act_grad(const ActGradCall& c, bool vec, cudaStream_t st) {
 cudaError_t launch_column_sum(const float* p0, unsigned parts, uint64_t cols, void* out0, const float* p1,
                               void* out1, int dtype, cudaStream_t st) {
   if ((!out0 && !out1) || cols == 0) return cudaSuccess;
-  return launch_op(column_sum_kernel, dim3(unsigned((cols + 31) / 32), out1 ? 2 : 1), 256, 0, st, p0, out0, p1, out1,
+  return launch_op(column_sum_kernel, dim3(unsigned((cols + 31) / 32), out1 ? 2 : 1), 32 * kSumLanes, 0, st, p0, out0, p1, out1,
                    parts, cols, dtype);
 }
 

@@ -64,6 +64,7 @@ struct GemmArgs {
   uint32_t P, Q, K;
   uint32_t p_mn, q_mn;
   uint32_t p_copy, q_copy;  // the copy engine brings the operand in, not threads
+  uint32_t p_layout, q_layout;
   uint16_t *out, *z;
   const void* bias;
   const uint16_t* residual;
@@ -105,11 +106,20 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, u
     tma_load_2d(dst, map, x, y, bar);
 }
 
+// Layouts of an operand in memory.
+enum Layout : uint32_t {
+  kKMajor,    // matrix rows: one box of 64 contraction elements
+  kMnMajor,   // contraction rows: a box for every 64 matrix rows
+  kMnBlocks,  // the same with whole blocks of 64: one box over the blocks of a map (64, k, block)
+};
+
 template <bool kPair>
-__device__ __forceinline__ void copy_operand(uint32_t dst, const CUtensorMap* map, bool mn, uint32_t row0, uint32_t k0,
-                                             uint32_t rows, uint32_t bar) {
-  if (!mn) {
+__device__ __forceinline__ void copy_operand(uint32_t dst, const CUtensorMap* map, uint32_t layout, uint32_t row0,
+                                             uint32_t k0, uint32_t rows, uint32_t bar) {
+  if (layout == kKMajor) {
     copy_box<kPair>(dst, map, k0, row0, bar);
+  } else if (layout == kMnBlocks) {
+    tma_load_3d<kPair>(dst, map, k0, row0 / 64, bar);
   } else {
     for (uint32_t r = 0; r < rows; r += 64) copy_box<kPair>(dst + r * 128, map, row0 + r, k0, bar);
   }
@@ -256,8 +266,8 @@ __device__ __forceinline__ bool copy_tile(const GemmArgs& a, const CUtensorMap* 
     uint32_t bar = addr_of(&s.full[ring.slot]);
     if (!kPair || rank == 0) mbar_arrive_expect(bar, kPair ? 2 * bytes : bytes);
     if (kPair) bar = cluster_peer_address(bar, 0);
-    if (a.p_copy) copy_operand<kPair>(addr_of(dst), mp, a.p_mn, p0, i * kStep, kLanes, bar);
-    if (a.q_copy) copy_operand<kPair>(addr_of(dst) + kPBytes, mq, a.q_mn, q0, i * kStep, a.bq, bar);
+    if (a.p_copy) copy_operand<kPair>(addr_of(dst), mp, a.p_layout, p0, i * kStep, kLanes, bar);
+    if (a.q_copy) copy_operand<kPair>(addr_of(dst) + kPBytes, mq, a.q_layout, q0, i * kStep, a.bq, bar);
     ring.next(a.stages);
   }
   return true;
@@ -770,18 +780,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_function(cudaError_t* err) {
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
-// Map of an operand: boxes of 64 elements along its rows, `box_rows` rows.
-cudaError_t encode(CUtensorMap* m, const uint16_t* base, uint64_t ld, uint64_t nrows, uint64_t ncols, uint32_t box_rows,
-                   bool bf16) {
+// Map of an operand of `rows` by `k`, for tiles of `tile` rows by 64 of the
+// contraction.
+cudaError_t encode(CUtensorMap* m, uint32_t* layout, const uint16_t* base, uint64_t ld, uint32_t rows, uint32_t k,
+                   bool mn, uint32_t tile, bool bf16) {
   cudaError_t err = cudaSuccess;
   auto f = encode_function(&err);
   if (!f) return err;
-  const cuuint64_t dims[2] = {ncols, nrows};
-  const cuuint64_t strides[1] = {(nrows > 1 ? ld : (ncols + 7) / 8 * 8) * 2};
-  const cuuint32_t box[2] = {64, box_rows}, el[2] = {1, 1};
-  const CUresult r = f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                       const_cast<uint16_t*>(base), dims, strides, box, el, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  *layout = !mn ? kKMajor : rows % 64 == 0 ? kMnBlocks : kMnMajor;
+  const uint64_t inner = mn ? rows : k, outer = mn ? k : rows;
+  const cuuint64_t pitch = (outer > 1 ? ld : (inner + 7) / 8 * 8) * 2;
+  const cuuint64_t dims[3] = {*layout == kMnBlocks ? 64 : inner, outer, rows / 64}, strides[2] = {pitch, 128};
+  const cuuint32_t box[3] = {64, mn ? 64 : tile, tile / 64}, el[3] = {1, 1, 1};
+  const CUresult r = f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                       *layout == kMnBlocks ? 3 : 2, const_cast<uint16_t*>(base), dims, strides, box, el,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -960,14 +973,13 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   a.idesc = mma_descriptor(c.dtype == ARX_BF16, a.p_mn, a.q_mn, lanes, a.bn);
 
-  const uint64_t p_rows = a.p_mn ? a.K : a.P, q_rows = a.q_mn ? a.K : a.Q;
   CUtensorMap mp{}, mq{};
   if (a.p_copy) {
-    err = encode(&mp, a.p, a.ldp, p_rows, a.p_mn ? a.P : a.K, a.p_mn ? 64 : kLanes, bf16);
+    err = encode(&mp, &a.p_layout, a.p, a.ldp, a.P, a.K, a.p_mn, kLanes, bf16);
     if (err != cudaSuccess) return err;
   }
   if (a.q_copy) {
-    err = encode(&mq, a.q, a.ldq, q_rows, a.q_mn ? a.Q : a.K, a.q_mn ? 64 : a.bq, bf16);
+    err = encode(&mq, &a.q_layout, a.q, a.ldq, a.Q, a.K, a.q_mn, a.bq, bf16);
     if (err != cudaSuccess) return err;
   }
   const auto run = [&](auto w, auto both) {

@@ -75,6 +75,21 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       :: "r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
+// Box at (0, y, z) of a three-dimensional map (see copy_operand).
+template <bool kPair>
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t y, uint32_t z, uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(dst), "l"(m), "r"(0u), "r"(y), "r"(z), "r"(bar) : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(dst), "l"(m), "r"(0u), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
 // The same by a block of a pair, counted on a barrier that may be the other
 // block's (a shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, uint32_t x, uint32_t y,
