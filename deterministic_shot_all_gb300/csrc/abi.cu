@@ -115,6 +115,8 @@ arx_status report(arx_status s, const char* fmt, ...) {
   return s;
 }
 
+arx_status succeed() { return ok(); }
+
 }  // namespace arx
 
 extern "C" {

@@ -16,6 +16,9 @@ arx_status validate_io(const void* const* in, int W, const void* out, size_t n, 
 // Sets the calling thread's arx_last_error() text and returns `s`.
 arx_status report(arx_status s, const char* fmt, ...);
 
+// Clears it and returns ARX_OK.
+arx_status succeed();
+
 // One stateless reduce: out[i] = bf16(sum_r slot[r][i]) for 0 <= i < n.
 struct ReduceCall {
   const uint16_t* slot[8];

@@ -262,12 +262,11 @@ __device__ __forceinline__ uint4 philox4x32_10(uint32_t c0, uint32_t c1, uint32_
   return make_uint4(c0, c1, c2, c3);
 }
 
-// What dropout needs of a call: the generator's seed and offset, the
-// threshold T = round(65536 p) and the scale 65536 / (65536 - T).
+// What dropout with a threshold T = round(65536 p) of at least 1 needs of a
+// call: the generator's seed and offset, T and the scale 65536 / (65536 - T).
 struct DropoutState {
   uint32_t k0, k1, o0, o1;
-  uint32_t high;  // T << 16: a value in a word's high half is at least T when the word is at least this
-  bool none;      // T == 65536: nothing is kept
+  uint32_t below;  // (T << 16) - 1: a value in a word's high half is at least T when the word is above this
   float scale;
 };
 
@@ -276,7 +275,7 @@ __device__ __forceinline__ DropoutState load_dropout(const uint64_t* rng, uint32
   const uint64_t seed = rng[0], offset = rng[1];
   d.k0 = uint32_t(seed), d.k1 = uint32_t(seed >> 32);
   d.o0 = uint32_t(offset), d.o1 = uint32_t(offset >> 32);
-  d.high = threshold << 16, d.none = threshold >= 65536u, d.scale = scale;
+  d.below = uint32_t((uint64_t(threshold) << 16) - 1u), d.scale = scale;  // T = 65536: no word is above
   return d;
 }
 
@@ -288,7 +287,7 @@ __device__ __forceinline__ uint4 dropout_random(const DropoutState& d, uint32_t 
 // Whether column 8 * group + k is kept.
 __device__ __forceinline__ bool dropout_keeps(const DropoutState& d, const uint4& r, int k) {
   const uint32_t w = k < 4 ? (k < 2 ? r.x : r.y) : (k < 6 ? r.z : r.w);
-  return !d.none && ((k & 1) ? w : w << 16) >= d.high;
+  return ((k & 1) ? w : w << 16) > d.below;
 }
 
 // Dropout of the 8 columns of a group: kept values scaled, the others +0 (a

@@ -15,7 +15,7 @@ using arx::report;
 
 constexpr uint64_t kMaxDim = (uint64_t(1) << 31) - 1;
 
-arx_status ok() { return report(ARX_OK, "%s", ""); }
+arx_status ok() { return arx::succeed(); }
 
 arx_status launched(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return ok();
