@@ -20,7 +20,8 @@
 //         spans both SMs, each holding half of either operand: a single SM
 //         at 128 x 256 would need 96 bytes a cycle from L2, against the 64
 //         it can take; the pair needs 64), two accumulators in tensor memory,
-//         so a tile's epilogue runs under the next tile's products;
+//         so a tile's epilogue runs under the next tile's products; or over
+//         tiles of 256 x 512 on both accumulators, which needs 48 bytes a cycle;
 //  split  for few tiles (decode, small matrices): the output's columns take
 //         the 128 accumulator lanes, its few rows the instruction's N, and a
 //         cluster of up to 8 blocks splits the contraction; the partials
@@ -71,7 +72,7 @@ struct GemmArgs {
   uint64_t ldout, ldz, ldresidual;
   uint32_t* status;
   int act, wdtype;
-  uint32_t bn, bq;     // rows of Q in a tile, and in a block's stage
+  uint32_t bn, bq;     // rows of Q under one accumulator, and a block's share of them in a stage
   uint32_t stages, stage_bytes;
   uint32_t steps;      // stages' worth of contraction: ceil(K / 64)
   uint32_t split;      // blocks of a cluster that share a tile's contraction
@@ -255,11 +256,11 @@ __device__ __forceinline__ void put(const Unit& t, const Place& c, uint8_t* dst)
 // One thread: the operands that the copy engine can address.  In a pair each
 // block fills its own half of the stage; both halves count on the first
 // block's barrier.  Returns false after a wait ran out.
-template <bool kPair>
+template <bool kPair, uint32_t kSubs>
 __device__ __forceinline__ bool copy_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
                                           uint8_t* stages, Ring& ring, uint32_t p0, uint32_t q0, uint32_t first,
                                           uint32_t last, uint32_t rank) {
-  const uint32_t bytes = (a.p_copy ? kPBytes : 0) + (a.q_copy ? a.bq * 128 : 0);
+  const uint32_t bytes = (a.p_copy ? kPBytes : 0) + (a.q_copy ? kSubs * a.bq * 128 : 0);
   for (uint32_t i = first; i < last; ++i) {
     if (!mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort)) return false;
     uint8_t* dst = stages + ring.slot * a.stage_bytes;
@@ -267,7 +268,10 @@ __device__ __forceinline__ bool copy_tile(const GemmArgs& a, const CUtensorMap* 
     if (!kPair || rank == 0) mbar_arrive_expect(bar, kPair ? 2 * bytes : bytes);
     if (kPair) bar = cluster_peer_address(bar, 0);
     if (a.p_copy) copy_operand<kPair>(addr_of(dst), mp, a.p_layout, p0, i * kStep, kLanes, bar);
-    if (a.q_copy) copy_operand<kPair>(addr_of(dst) + kPBytes, mq, a.q_layout, q0, i * kStep, a.bq, bar);
+    if (a.q_copy)
+#pragma unroll
+      for (uint32_t j = 0; j < kSubs; ++j)
+        copy_operand<kPair>(addr_of(dst) + kPBytes + j * a.bq * 128, mq, a.q_layout, q0 + j * a.bn, i * kStep, a.bq, bar);
     ring.next(a.stages);
   }
   return true;
@@ -323,7 +327,7 @@ __device__ __forceinline__ bool load_tile(const GemmArgs& a, Shared& s, uint8_t*
 }
 
 // One thread (of a pair's first block) issues the tile's products into `tmem`.
-template <bool kPair>
+template <bool kPair, uint32_t kSubs>
 __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint32_t stages, Ring& ring, uint32_t tmem,
                                               uint32_t first, uint32_t last) {
   // A contraction step of 16 is 32 bytes along a K-major row, 16 rows of an
@@ -335,8 +339,11 @@ __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint
     const uint32_t base = stages + ring.slot * a.stage_bytes;
     const uint64_t dp = operand_descriptor(base, kStep * 128), dq = operand_descriptor(base + kPBytes, kStep * 128);
 #pragma unroll
-    for (uint32_t k = 0; k < kStep / 16; ++k)
+    for (uint32_t k = 0; k < kStep / 16; ++k) {
       mma_f16<kPair>(tmem, dp + k * adv_p, dq + k * adv_q, a.idesc, i != first || k != 0);
+      if (kSubs == 2)
+        mma_f16<kPair>(tmem + 256, dp + k * adv_p, dq + a.bq * 8 + k * adv_q, a.idesc, i != first || k != 0);
+    }
     mma_commit<kPair>(addr_of(&s.empty[ring.slot]));
     ring.next(a.stages);
   }
@@ -525,7 +532,8 @@ __device__ __forceinline__ void tile_at(const GemmArgs& a, uint32_t t, uint32_t&
   tp = 8u * b + (in - tq * rows);
 }
 
-template <int D, int kWord, bool kBoth>
+// kSubs: accumulators to a tile.
+template <int D, int kWord, bool kBoth, uint32_t kSubs>
 __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     gemm_wide_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap mp,
                      const __grid_constant__ CUtensorMap mq) {
@@ -545,11 +553,11 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     for (uint32_t t = first_tile; t < tiles; t += step) {
       uint32_t tp, tq;
       tile_at(a, t, tp, tq);
-      const uint32_t p0 = (2 * tp + rank) * kLanes, q0 = tq * a.bn + rank * a.bq;
+      const uint32_t p0 = (2 * tp + rank) * kLanes, q0 = tq * kSubs * a.bn + rank * a.bq;
       issued = a.stages;
       bool ok = true;
       if (copies)
-        ok = copy_tile<true>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
+        ok = copy_tile<true, kSubs>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
       else if constexpr (!kTma)
         ok = load_tile<kWord, kBoth, true>(a, s, stages, ring, p0, q0, 0, a.steps, threadIdx.x - kFirstLoader<kTma>);
       if (!ok) break;
@@ -557,10 +565,11 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
   } else if (warp == 1 && lane == 0 && rank == 0 && a.steps > 0) {
     uint32_t n = 0;
     for (uint32_t t = first_tile; t < tiles; t += step, ++n) {
-      const uint32_t b = n & 1, use = n >> 1;
+      // One accumulator to a tile: two tiles' alternate.  Two: the tile has both.
+      const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
       if (!mbar_wait(addr_of(&s.acc_empty[b]), (use & 1) ^ 1, &s.abort)) break;
       tmem_fence_after();
-      if (!multiply_tile<true>(a, s, addr_of(stages), ring, s.tmem + b * 256, 0, a.steps)) break;
+      if (!multiply_tile<true, kSubs>(a, s, addr_of(stages), ring, s.tmem + b * 256, 0, a.steps)) break;
       mma_commit<true>(addr_of(&s.acc_full[b]));
     }
   } else if (warp >= 2 && warp < 2 + kEpilogueWarps<kTma>) {
@@ -569,35 +578,38 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     for (uint32_t t = first_tile; t < tiles; t += step, ++n) {
       uint32_t tp, tq;
       tile_at(a, t, tp, tq);
-      const uint32_t b = n & 1, use = n >> 1;
+      const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
       if (a.steps > 0) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.abort))) break;
         tmem_fence_after();
       }
-      const uint32_t row0 = (2 * tp + rank) * kLanes + quarter * 32, col0 = tq * a.bn;
+      const uint32_t row0 = (2 * tp + rank) * kLanes + quarter * 32;
       float* staged = reinterpret_cast<float*>(stages + a.stages * a.stage_bytes) + (warp - 2) * 32 * 33;
-      const bool whole = a.octets && col0 + a.bn <= a.Q;
-      const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
-      for (uint32_t c = c0; c < c0 + half && col0 + c < a.Q; c += 32) {
+      for (uint32_t j = 0; j < kSubs; ++j) {
+        const uint32_t col0 = (tq * kSubs + j) * a.bn, acc = s.tmem + (b + j) * 256 + (quarter * 32 << 16);
+        const bool whole = a.octets && col0 + a.bn <= a.Q;
+        const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
+        for (uint32_t c = c0; c < c0 + half && col0 + c < a.Q; c += 32) {
 #pragma unroll
-        for (uint32_t h = 0; h < 32; h += 16) {
-          float v[16];
-          if (a.steps > 0)
-            tmem_load16(s.tmem + b * 256 + c + h + (quarter * 32 << 16), v);
-          else
+          for (uint32_t h = 0; h < 32; h += 16) {
+            float v[16];
+            if (a.steps > 0)
+              tmem_load16(acc + c + h, v);
+            else
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-          if (whole) {
-            if (row0 + lane < a.P) finish16<D>(a, v, row0 + lane, col0 + c + h);
-          } else {
+              for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+            if (whole) {
+              if (row0 + lane < a.P) finish16<D>(a, v, row0 + lane, col0 + c + h);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) staged[lane * 33 + h + k] = v[k];
+              for (int k = 0; k < 16; ++k) staged[lane * 33 + h + k] = v[k];
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        }
-        if (!whole) {
-          finish_staged<D>(a, staged, row0, col0 + c + lane, lane);
-          __syncwarp();
+          if (!whole) {
+            finish_staged<D>(a, staged, row0, col0 + c + lane, lane);
+            __syncwarp();
+          }
         }
       }
       tmem_fence_before();
@@ -633,12 +645,12 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
   Ring ring;
   const bool copies = threadIdx.x == 0 && (a.p_copy | a.q_copy), loads = !kTma && threadIdx.x >= kFirstLoader<kTma>;
   if (copies) {
-    copy_tile<false>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, 0);
+    copy_tile<false, 1>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, 0);
   } else if (loads) {
     if constexpr (!kTma)
       load_tile<kWord, kBoth, false>(a, s, stages, ring, p0, q0, first, last, threadIdx.x - kFirstLoader<kTma>);
   } else if (warp == 1 && lane == 0 && first < last) {
-    if (multiply_tile<false>(a, s, addr_of(stages), ring, s.tmem, first, last))
+    if (multiply_tile<false, 1>(a, s, addr_of(stages), ring, s.tmem, first, last))
       mma_commit<false>(addr_of(&s.acc_full[0]));
   } else if (warp >= 2 && warp < 2 + kEpilogueWarps<kTma>) {
     const uint32_t quarter = warp & 3;
@@ -828,10 +840,10 @@ cudaError_t launch_cluster(uint32_t blocks, uint32_t threads, uint32_t cluster, 
 
 // A persistent grid: as many pairs as the device holds at once (two blocks to
 // a pair, one block to an SM), or fewer tiles.
-template <int D, int kWord, bool kBoth>
+template <int D, int kWord, bool kBoth, uint32_t kSubs>
 cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, int sms, cudaStream_t st) {
   const uint32_t tiles = a.tiles_p * a.tiles_q, pairs = uint32_t(sms) / 2;
-  return launch_cluster<gemm_wide_kernel<D, kWord, kBoth>>(2 * (tiles < pairs ? tiles : pairs), kGemmThreads<kWord == 16>, 2,
+  return launch_cluster<gemm_wide_kernel<D, kWord, kBoth, kSubs>>(2 * (tiles < pairs ? tiles : pairs), kGemmThreads<kWord == 16>, 2,
                                                    1024 + a.stages * a.stage_bytes + kEpilogueWarps<kWord == 16> * kStagedBytes,
                                                    st, a, mp, mq);
 }
@@ -848,7 +860,7 @@ uint32_t ceil_div(uint64_t a, uint64_t b) { return uint32_t((a + b - 1) / b); }
 // tile's contraction: the one with the least estimated time, in SM cycles.
 struct Form {
   bool wide;
-  uint32_t bn, split;
+  uint32_t bn, split, subs;
 };
 
 Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, uint32_t sms) {
@@ -858,19 +870,26 @@ Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, ui
     if (best.bn == 0 || cycles < least) best = f, least = cycles;
   };
   // A stage of `rows` rows of c.p and `cols` of c.q costs its copies or its
-  // products, whichever is longer.  Measured: an SM takes in 50 bytes a cycle
+  // products, whichever is longer.  Measured: an SM takes in 46 bytes a cycle
   // in pairs, 36 for one split block and 44 for two, and 16 through loading
   // threads (12 in pairs, where the slower of two blocks counts); the products
   // take 2.5 cycles a row of the kernel's Q.
   const bool threads = !p_copy || !q_copy;
   const auto stage = [&](uint32_t rows, uint32_t cols, uint32_t bn, double engine, double loaded) {
     const double copies = rows * 128.0 / (p_copy ? engine : loaded) + cols * 128.0 / (q_copy ? engine : loaded);
-    return copies > 2.5 * bn ? copies : 2.5 * bn;
+    return copies > 2.1 * bn ? copies : 2.1 * bn;
   };
   for (uint32_t bn = 256; bn >= 128; bn /= 2) {
     const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, bn);
     const double waves = ceil_div(tiles, sms / 2);
-    consider(Form{true, bn, 1}, waves * steps * stage(kLanes, bn / 2, bn, 50, 12) + 6000 + 40 * bn);
+    consider(Form{true, bn, 1, 1}, waves * steps * stage(kLanes, bn / 2, bn, 46, 12) + 6000 + 40 * bn);
+  }
+  // Two accumulators to a tile: 1290 cycles a stage (630 us against 681 at
+  // 8192^3, where the card's power sets the clock), and no tile's epilogue runs
+  // under the next one's products.
+  if (!threads) {
+    const double waves = ceil_div(ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, 512), sms / 2);
+    consider(Form{true, 256, 1, 2}, waves * (steps * 1290.0 + 4000) + 6000 + 40 * 256);
   }
   // Joining and storing a tile takes about 25 cycles a row of Q, 45 through
   // the cluster; starting and ending a block 6000, which two blocks on an SM
@@ -881,7 +900,7 @@ Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, ui
     for (uint32_t split = 1; split <= 8 && (split == 1 || split <= steps); split *= 2) {
       const double on_sm = ceil_div(uint64_t(tiles) * split, sms), join = (split > 1 ? 45 : 25) * bn;
       const double own = ceil_div(steps, split) * stage(bn, kLanes, bn, two && on_sm > 1 ? 44 : 36, 16) + join;
-      consider(Form{false, bn, split}, two ? on_sm * own + 6000 : on_sm * (own + 6000));
+      consider(Form{false, bn, split, 1}, two ? on_sm * own + 6000 : on_sm * (own + 6000));
     }
     if (bn >= c.rows) break;
   }
@@ -967,8 +986,8 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   }
   const uint32_t lanes = wide ? 2 * kLanes : kLanes;
   a.tiles_p = ceil_div(a.P, lanes);
-  a.tiles_q = ceil_div(a.Q, a.bn);
-  a.stage_bytes = kPBytes + a.bq * 128;
+  a.tiles_q = ceil_div(a.Q, form.subs * a.bn);
+  a.stage_bytes = kPBytes + form.subs * a.bq * 128;
   a.stages = (word != 16 ? kLoadedBudget : wide || a.bn > 128 ? kStageBudget : kSplitBudget) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   a.idesc = mma_descriptor(c.dtype == ARX_BF16, a.p_mn, a.q_mn, lanes, a.bn);
@@ -985,9 +1004,13 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   const auto run = [&](auto w, auto both) {
     constexpr int kWord = decltype(w)::value;
     constexpr bool kBoth = decltype(both)::value;
+    if constexpr (kWord == 16)
+      if (wide && form.subs == 2)
+        return bf16 ? launch_wide<ARX_BF16, kWord, kBoth, 2>(a, mp, mq, sms, st)
+                    : launch_wide<ARX_F16, kWord, kBoth, 2>(a, mp, mq, sms, st);
     if (wide)
-      return bf16 ? launch_wide<ARX_BF16, kWord, kBoth>(a, mp, mq, sms, st)
-                  : launch_wide<ARX_F16, kWord, kBoth>(a, mp, mq, sms, st);
+      return bf16 ? launch_wide<ARX_BF16, kWord, kBoth, 1>(a, mp, mq, sms, st)
+                  : launch_wide<ARX_F16, kWord, kBoth, 1>(a, mp, mq, sms, st);
     return bf16 ? launch_split<ARX_BF16, kWord, kBoth>(a, mp, mq, st) : launch_split<ARX_F16, kWord, kBoth>(a, mp, mq, st);
   };
   using std::integral_constant;
