@@ -84,6 +84,38 @@ def test_strides_and_alignment(arx, M, N, K, pad, lead, opad, olead):
     _forward(arx, M, N, K, torch.bfloat16, "gelu", pad=pad, lead=lead, opad=opad, olead=olead)
 
 
+# Sizes that take the forms the shapes above do not: tiles on two accumulators
+# (long contractions, whole and cut tiles), a cluster over 256 rows.
+@pytest.mark.parametrize("M,N,K", [(1000, 8136, 2048), (1000, 8130, 2056), (512, 2048, 4096), (500, 2045, 4096)])
+def test_large_forms(arx, M, N, K):
+    _forward(arx, M, N, K, torch.bfloat16, "gelu")
+    _forward(arx, M, N, K, torch.float16, residual=False, bias=False, z=False)
+
+
+@pytest.mark.parametrize("M,N,K", [(1000, 2048, 8192), (2050, 1000, 8192), (2050, 1000, 8200)])
+def test_backward_large_forms(arx, M, N, K):
+    _backward(arx, M, N, K, torch.bfloat16)
+
+
+# One operand by the copy engine, the other by threads.
+@pytest.mark.parametrize("M,N,K", [(5, 72, 136), (300, 2047, 520), (1400, 2600, 264), (3, 200, 1000)])
+@pytest.mark.parametrize("xpad,wpad", [(3, 0), (0, 3), (4, 0), (0, 4), (8, 1)])
+def test_operands_of_different_alignment(arx, M, N, K, xpad, wpad):
+    x, w = make((M, K), torch.bfloat16, 1), make((N, K), torch.bfloat16, 2, K ** -0.5)
+    d = make((M, N), torch.bfloat16, 3)
+    out, want = Out((M, N), torch.bfloat16), torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    xs, ws = strided(x, xpad), strided(w, wpad)
+    arx.arx_linear(xs, ws, out.t)
+    wd = _matmul(f64(x), f64(w).T.copy())
+    assert_close(out, wd, _chain(K) * _matmul(np.abs(f64(x)), np.abs(f64(w)).T.copy()), "out")
+    dx, dw = Out((M, K), torch.bfloat16), Out((N, K), torch.bfloat16)
+    arx.arx_linear_bwd(d, xs, ws, dx=dx.t, dw=dw.t)
+    torch.cuda.synchronize()
+    dd, ad = f64(d), np.abs(f64(d))
+    assert_close(dx, _matmul(dd, f64(w)), _chain(N) * _matmul(ad, np.abs(f64(w))), "dx")
+    assert_close(dw, _matmul(dd.T.copy(), f64(x)), _chain(M) * _matmul(ad.T.copy(), np.abs(f64(x))), "dw")
+
+
 @pytest.mark.parametrize("M,N", [(3, 40), (1300, 2600)])
 def test_empty_contraction(arx, M, N):
     _forward(arx, M, N, 0, torch.bfloat16, "silu")
