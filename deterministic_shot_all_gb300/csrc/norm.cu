@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(TPR* RPC) norm_fwd_kernel(const arx_layer_norm
 // reads 8 bytes of 32-bit parameters for every 4 of a 16-bit row: 45.6 us at
 // [8192, 4096], 2.3 times the bytes' time.)
 template <int T, int RPC>
-constexpr int kFwdBlocks = T * RPC >= 512 ? 1 : 3;
+constexpr int kFwdBlocks = T * RPC >= 512 ? 1 : T * RPC > 256 ? 2 : 3;
 
 template <int D, int T, int RPC, int NV, int V, int kRing>
 __global__ void __launch_bounds__(T* RPC, kFwdBlocks<T, RPC>)
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(512) norm_fwd_long_kernel(const arx_layer_norm
 // to the sums over 16 warps and each row's bookkeeping; 32 to a thread with the
 // weights read anew for every row 88 us, waiting for them.
 template <int T, int RPC>
-constexpr int kBwdBlocks = T * RPC >= 512 ? 1 : 2;
+constexpr int kBwdBlocks = T * RPC > 256 ? 1 : 2;
 
 template <int D, int T, int RPC, int NV, int V, int kRing>
 __global__ void __launch_bounds__(T* RPC, kBwdBlocks<T, RPC>) norm_bwd_kernel(const arx_layer_norm_bwd_args a,
@@ -385,6 +385,7 @@ cudaError_t fwd_any(const arx_layer_norm_args& a, bool vec, cudaStream_t st) {
     if (n <= 1024) return many ? fwd_ring<D, 64, 4, 2, 8>(a, st) : fwd<D, 128, 1, 1, 8>(a, st);
     if (n <= 2048) return many ? fwd_ring<D, 128, 2, 2, 8>(a, st) : fwd<D, 256, 1, 1, 8>(a, st);
     if (n <= 4096) return many ? fwd_ring<D, 256, 1, 2, 8>(a, st) : fwd<D, 512, 1, 1, 8>(a, st);
+    if (n <= 5120 && many) return fwd_ring<D, 320, 1, 2, 8>(a, st);
     if (n <= 8192) return many ? fwd_ring<D, 512, 1, 2, 8>(a, st) : fwd<D, 1024, 1, 1, 8>(a, st);
     if (n <= 16384) return fwd<D, 512, 1, 4, 8>(a, st);
   } else {
@@ -393,6 +394,7 @@ cudaError_t fwd_any(const arx_layer_norm_args& a, bool vec, cudaStream_t st) {
     if (n <= 1024) return many ? fwd_ring<D, 64, 4, 16, 1>(a, st) : fwd<D, 128, 1, 8, 1>(a, st);
     if (n <= 2048) return many ? fwd_ring<D, 128, 2, 16, 1>(a, st) : fwd<D, 256, 1, 8, 1>(a, st);
     if (n <= 4096) return many ? fwd_ring<D, 256, 1, 16, 1>(a, st) : fwd<D, 512, 1, 8, 1>(a, st);
+    if (n <= 5120 && many) return fwd_ring<D, 320, 1, 16, 1>(a, st);
     if (n <= 8192) return many ? fwd_ring<D, 512, 1, 16, 1>(a, st) : fwd<D, 1024, 1, 8, 1>(a, st);
     if (n <= 16384) return fwd<D, 512, 1, 32, 1>(a, st);
   }
@@ -464,6 +466,8 @@ cudaError_t bwd_any(const arx_layer_norm_bwd_args& a, bool vec, unsigned* parts,
       e = bwd<D, 128, 2, 16, 1>(a, parts, &done, st);
     else if (n <= 4096)
       e = bwd<D, 256, 1, 16, 1>(a, parts, &done, st);
+    else if (n <= 5120)
+      e = bwd<D, 320, 1, 16, 1>(a, parts, &done, st);
     else if (n <= 8192)
       e = bwd<D, 512, 1, 16, 1>(a, parts, &done, st);
     else if (n <= 16384)
