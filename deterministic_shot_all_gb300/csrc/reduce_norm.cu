@@ -151,8 +151,11 @@ cudaError_t run_w(const ReduceNormArgs& a, bool vec, cudaStream_t st) {
     if (n <= 16384) return run<W, 512, 1, 4, 8>(a, st);
   } else {
     if (n <= 256) return run<W, 32, 4, 8, 1>(a, st);
+    if (n <= 1024) return run<W, 128, 1, 8, 1>(a, st);
     if (n <= 2048) return run<W, 256, 1, 8, 1>(a, st);
-    if (n <= 8192) return run<W, 512, 1, 16, 1>(a, st);
+    if (n <= 4096) return run<W, 512, 1, 8, 1>(a, st);
+    if (n <= 5120) return run<W, 640, 1, 8, 1>(a, st);
+    if (n <= 8192) return run<W, 1024, 1, 8, 1>(a, st);
   }
   return launch_op(reduce_norm_long_kernel<W>, dim3(unsigned(a.rows)), 512, 0, st, a);
 }
