@@ -14,7 +14,7 @@
 // stages.
 //
 // Three forms:
-//  vector one to four rows (decode): dot products on the CUDA cores, see
+//  vector one or two rows (decode): dot products on the CUDA cores, see
 //         dot_kernel; the tensor cores' set-up would cost more than the work.
 //  wide   persistent pairs of blocks over tiles of 256 x 256 (one instruction
 //         spans both SMs, each holding half of either operand: a single SM
@@ -698,15 +698,16 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
   finish_block<false>(a, s, warp, lane, rank, ring, last - first);
 }
 
-// ---- one to four rows ------------------------------------------------------------------
+// ---- one or two rows --------------------------------------------------------------------
 //
 // out[m][j] = sum_k x[m][k] w[j][k]: w is read once, which bounds the kernel,
-// at 2 M operations to an element.  A warp (or `split` warps of a block) takes
+// at 2 M operations to an element.  Two tokens of 4096 -> 2048: 4.6 us, the
+// split form 5.8; three: 5.3, but 33 against 25 at 8192 x 8192.  A warp (or `split` warps of a block) takes
 // a feature j; its lanes take 16-byte units of the row, kBatch of them in
 // flight, and x comes from L1.  The lanes' sums meet in a butterfly and the
 // split warps' in warp order.  kV = 1: rows off 16 bytes, element by element.
 
-constexpr uint32_t kDotRows = 4;
+constexpr uint32_t kDotRows = 2;
 constexpr uint32_t kDotThreads = 256;
 constexpr int kDotBatch = 8;
 
@@ -718,7 +719,9 @@ __global__ void __launch_bounds__(kDotThreads) dot_kernel(const __grid_constant_
   const uint32_t j = blockIdx.x * per + warp / a.split, share = warp % a.split;
   // A hint only (as in the reduce kernels): the weights' way to L2 starts
   // while the stream's previous kernel, whose output x may be, still runs.
-  if (kV == 8 && share == 0 && lane == 0 && j < a.Q && a.K > 0) prefetch_l2_bulk(a.q + j * a.ldq, a.K * 2);
+  // The lanes' first batch of the row: asked for whole, rows of 16 KB came
+  // twice (one token, 8192 x 8192: 34.6 us against 23.5; none 26.0).
+  if (kV == 8 && share == 0 && lane == 0 && j < a.Q && a.K > 0) prefetch_l2_bulk(a.q + j * a.ldq, a.K < 2048 ? a.K * 2 : 4096);
   dependent_launch_prologue();
   float acc[kM] = {};
   if (j < a.Q) {
@@ -898,7 +901,11 @@ Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, ui
     const uint32_t tiles = ceil_div(c.cols, kLanes) * ceil_div(c.rows, bn);
     const bool two = !threads && bn <= 128;  // blocks to an SM
     for (uint32_t split = 1; split <= 8 && (split == 1 || split <= steps); split *= 2) {
-      const double on_sm = ceil_div(uint64_t(tiles) * split, sms), join = (split > 1 ? 45 : 25) * bn;
+      // Clusters at work at once, one block to an SM: those of 4 and 8 leave some
+      // SMs of a processing cluster over.
+      const uint32_t at_once = split == 8 ? sms * 14 / 152 : split == 4 ? sms * 36 / 152 : sms / split;
+      const double join = (split > 1 ? 45 : 25) * bn;
+      const double on_sm = two ? ceil_div(uint64_t(tiles) * split, sms) : ceil_div(tiles, at_once);
       const double own = ceil_div(steps, split) * stage(bn, kLanes, bn, two && on_sm > 1 ? 44 : 36, 16) + join;
       consider(Form{false, bn, split, 1}, two ? on_sm * own + 6000 : on_sm * (own + 6000));
     }
@@ -910,12 +917,8 @@ Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, ui
 template <int D, int kV>
 cudaError_t launch_dot(const GemmArgs& a, cudaStream_t st) {
   const dim3 grid(ceil_div(a.Q, kDotThreads / 32 / a.split));
-  switch (a.P) {
-    case 1: return launch_op(dot_kernel<D, 1, kV>, grid, kDotThreads, 0, st, a);
-    case 2: return launch_op(dot_kernel<D, 2, kV>, grid, kDotThreads, 0, st, a);
-    case 3: return launch_op(dot_kernel<D, 3, kV>, grid, kDotThreads, 0, st, a);
-    default: return launch_op(dot_kernel<D, 4, kV>, grid, kDotThreads, 0, st, a);
-  }
+  return a.P == 1 ? launch_op(dot_kernel<D, 1, kV>, grid, kDotThreads, 0, st, a)
+                  : launch_op(dot_kernel<D, 2, kV>, grid, kDotThreads, 0, st, a);
 }
 
 }  // namespace
@@ -945,11 +948,15 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   a.octets = out_aligned(8) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
 
   const bool bf16 = c.dtype == ARX_BF16;
-  if (c.rows <= kDotRows && !c.p_mn && !c.q_mn) {
+  const bool units = c.k % 8 == 0 && copyable(static_cast<const uint16_t*>(c.p), c.ldp, c.rows) &&
+                     copyable(static_cast<const uint16_t*>(c.q), c.ldq, c.cols);
+  // Element by element the dot form is the slower one from about 8 million
+  // weights (one token of 4099 -> 2047: 15.9 us against the split form's 15.6;
+  // of 8193 -> 8191: 138 against 49).
+  if (c.rows <= kDotRows && !c.p_mn && !c.q_mn && (units || c.cols * c.k < (uint64_t(1) << 23))) {
     a.p = static_cast<const uint16_t*>(c.p), a.q = static_cast<const uint16_t*>(c.q);
     a.ldp = c.ldp, a.ldq = c.ldq;
     a.P = uint32_t(c.rows), a.Q = uint32_t(c.cols);
-    const bool units = a.K % 8 == 0 && copyable(a.p, a.ldp, a.P) && copyable(a.q, a.ldq, a.Q);
     // Warps for about 16 to an SM, while each keeps 256 elements or more.
     a.split = 1;
     while (a.split < 8 && uint64_t(a.Q) * a.split < 2432 && a.K / a.split > 512) a.split *= 2;
