@@ -549,7 +549,8 @@ arx_status arx_step_noalloc(const void* const* inputs, int W, void* out, size_t 
  *    once (nearest even) where it is stored, except where a call says so.
  *    Infinities and NaN follow the formulas.
  *  - The same call on the same values gives the same bits on every run: sums
- *    are taken in an order that depends on the sizes alone (no atomics).
+ *    are taken in an order that depends on the sizes and the alignment of the
+ *    arguments alone (no atomics).
  *  - An output may be exactly one of the inputs that a call names (same
  *    address, same leading dimension: each element is read before it is
  *    written); any other overlap of an output with an input, another output
@@ -749,7 +750,8 @@ arx_status arx_linear(const arx_linear_args* a, void* stream);
  *   dx      [M, K], dw [N, K], dbias [N] of `wdtype`; any may be NULL.
  *           M == 0 sets dw and dbias to zero.
  *   workspace  arx_linear_bwd_workspace_bytes(M, N) bytes (dz and partial sums);
- *           may be NULL when act is ARX_ACT_NONE and dbias is NULL */
+ *           may be NULL when act is ARX_ACT_NONE and dbias is NULL (given all
+ *           the same, a dout whose rows are not on 16 bytes is copied to it) */
 typedef struct arx_linear_bwd_args {
   const void* dout;
   const void* z;
