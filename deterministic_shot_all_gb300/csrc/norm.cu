@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(T* RPC, kBwdBlocks<T, RPC>) norm_bwd_kernel(co
                                                                            uint32_t slot, float inv_cols) {
   using S = typename Elem<D>::S;
   constexpr int kWarps = T / 32;
-  constexpr bool kHold = NV * V <= 16;  // the weights, xh and q stay in registers
+  constexpr bool kHold = NV * V <= 16 && T <= 512;  // the weights, xh and q stay in registers
   __shared__ float buf[2][RPC][2 * kWarps];
   extern __shared__ __align__(16) uint8_t smem[];  // [RPC][kRing][x, dy, dresidual][slot]
   dependent_launch_prologue();
@@ -396,7 +396,7 @@ cudaError_t fwd_any(const arx_layer_norm_args& a, bool vec, cudaStream_t st) {
     if (n <= 4096) return many ? fwd_ring<D, 256, 1, 16, 1>(a, st) : fwd<D, 512, 1, 8, 1>(a, st);
     if (n <= 5120 && many) return fwd_ring<D, 320, 1, 16, 1>(a, st);
     if (n <= 8192) return many ? fwd_ring<D, 512, 1, 16, 1>(a, st) : fwd<D, 1024, 1, 8, 1>(a, st);
-    if (n <= 16384) return fwd<D, 512, 1, 32, 1>(a, st);
+    if (n <= 16384) return fwd<D, 1024, 1, 16, 1>(a, st);
   }
   return launch_op(norm_fwd_long_kernel<D>, dim3(unsigned(a.rows)), 512, 0, st, a);
 }
@@ -471,7 +471,7 @@ cudaError_t bwd_any(const arx_layer_norm_bwd_args& a, bool vec, unsigned* parts,
     else if (n <= 8192)
       e = bwd<D, 512, 1, 16, 1>(a, parts, &done, st);
     else if (n <= 16384)
-      e = bwd<D, 512, 1, 32, 1>(a, parts, &done, st);
+      e = bwd<D, 1024, 1, 16, 1>(a, parts, &done, st);
     else
       done = false;
   }
