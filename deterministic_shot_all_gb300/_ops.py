@@ -44,11 +44,11 @@ arx_reduce_layer_norm_args = _struct(
     "arx_reduce_layer_norm_args", (_vp, "slots bias residual weight norm_bias h y mean rstd rng"), (_u64, "rows cols"),
     (_f64, "p"), (_f32, "eps"), (_i32, "W"))
 arx_linear_args = _struct(
-    "arx_linear_args", (_vp, "x w bias residual out z status"), (_u64, "M N K ldx ldw ldresidual ldout ldz"),
+    "arx_linear_args", (_vp, "x w bias residual out z status copies"), (_u64, "copies_bytes M N K ldx ldw ldresidual ldout ldz"),
     (_i32, "act dtype wdtype reserved"))
 arx_linear_bwd_args = _struct(
-    "arx_linear_bwd_args", (_vp, "dout z x w dx dw dbias workspace"), (_u64, "workspace_bytes"), (_vp, "status"),
-    (_u64, "M N K lddout ldz ldx ldw lddx lddw"), (_i32, "act dtype wdtype reserved"))
+    "arx_linear_bwd_args", (_vp, "dout z x w dx dw dbias workspace"), (_u64, "workspace_bytes"), (_vp, "status copies"),
+    (_u64, "copies_bytes M N K lddout ldz ldx ldw lddx lddw"), (_i32, "act dtype wdtype reserved"))
 
 SIGNATURES = {
     **{f"arx_{op}": ([ctypes.POINTER(t), _vp], ctypes.c_int) for op, t in (
@@ -58,6 +58,8 @@ SIGNATURES = {
         ("linear_bwd", arx_linear_bwd_args))},
     **{f"arx_{op}_workspace_bytes": ([_u64, _u64], ctypes.c_size_t)
        for op in ("layer_norm_bwd", "dropout_add_bwd", "linear_bwd")},
+    **{f"arx_{op}_copies_bytes": ([ctypes.POINTER(t)], ctypes.c_size_t) for op, t in (
+        ("linear", arx_linear_args), ("linear_bwd", arx_linear_bwd_args))},
 }
 
 
@@ -206,6 +208,32 @@ class _Marshal:
         self.a.workspace_bytes = t.numel() * t.element_size()
         self.refs.append(t)
 
+    def copies(self, t, query, operands, stream):
+        """``t``: a buffer, None (allocated where the call is faster with one) or False (none)."""
+        if t is False:
+            return
+        if t is None:
+            # Rows on 16 bytes need none; a leading dimension counts from the second row on.
+            off = 0
+            for m, name in operands:
+                if m is not None:
+                    off |= m.data_ptr() | (getattr(self.a, "ld" + name) * 2 if m.numel() > m.shape[-1] else 0)
+            n = query(ctypes.byref(self.a)) if off & 15 else 0
+            if n == 0:
+                return
+            import torch
+            if stream is None:
+                t = torch.empty(n, dtype=torch.uint8, device=f"cuda:{self.device}")
+            else:  # the stream's own memory: what was freed on it is not in use by another
+                with torch.cuda.stream(torch.cuda.ExternalStream(_core()._stream(stream))):
+                    t = torch.empty(n, dtype=torch.uint8, device=f"cuda:{self.device}")
+        elif not t.is_contiguous():
+            raise ValueError("copies: must be contiguous")
+        self._on_device(t, "copies")
+        self.a.copies = t.data_ptr() or None
+        self.a.copies_bytes = t.numel() * t.element_size()
+        self.refs.append(t)
+
     def done(self):
         if hasattr(self.a, "wdtype"):
             self.a.wdtype = self.a.dtype if self.wdtype in (None, self.dtype) else ARX_F32
@@ -216,7 +244,7 @@ _ROW_TYPES = (ARX_BF16, ARX_F16, ARX_F32)
 _PRODUCT_TYPES = (ARX_BF16, ARX_F16)
 
 
-def _layer_norm(x, y, weight=None, bias=None, mean=None, rstd=None, eps=1e-5):
+def _layer_norm(x, y, weight=None, bias=None, mean=None, rstd=None, eps=1e-5, stream=None):
     import torch
     m = _Marshal(arx_layer_norm_args(eps=eps), x, "x", _ROW_TYPES)
     rows, cols = m.matrix(x, "x")
@@ -230,7 +258,7 @@ def _layer_norm(x, y, weight=None, bias=None, mean=None, rstd=None, eps=1e-5):
 
 
 def _layer_norm_bwd(dy, x, mean, rstd, dx=None, weight=None, dresidual=None, dweight=None, dbias=None,
-                    workspace=None):
+                    workspace=None, stream=None):
     import torch
     m = _Marshal(arx_layer_norm_bwd_args(), x, "x", _ROW_TYPES)
     rows, cols = m.matrix(x, "x")
@@ -246,7 +274,7 @@ def _layer_norm_bwd(dy, x, mean, rstd, dx=None, weight=None, dresidual=None, dwe
     return m.done()
 
 
-def _dropout_add(x, out, p, rng=None, bias=None, residual=None):
+def _dropout_add(x, out, p, rng=None, bias=None, residual=None, stream=None):
     m = _Marshal(arx_dropout_add_args(), x, "x", _ROW_TYPES)
     rows, cols = m.matrix(x, "x")
     m.matrix(residual, "residual", rows, cols)
@@ -257,7 +285,7 @@ def _dropout_add(x, out, p, rng=None, bias=None, residual=None):
     return m.done()
 
 
-def _dropout_add_bwd(dout, dx, p, rng=None, dbias=None, workspace=None):
+def _dropout_add_bwd(dout, dx, p, rng=None, dbias=None, workspace=None, stream=None):
     m = _Marshal(arx_dropout_add_bwd_args(), dout, "dout", _ROW_TYPES)
     rows, cols = m.matrix(dout, "dout")
     m.matrix(dx, "dx", rows, cols)
@@ -269,7 +297,7 @@ def _dropout_add_bwd(dout, dx, p, rng=None, dbias=None, workspace=None):
 
 
 def _reduce_layer_norm(slots, h, y, bias=None, residual=None, weight=None, norm_bias=None, mean=None, rstd=None,
-                       eps=1e-5, p=0.0, rng=None):
+                       eps=1e-5, p=0.0, rng=None, stream=None):
     import torch
     a = arx_reduce_layer_norm_args(eps=eps)
     if y.dtype is not torch.bfloat16:
@@ -295,7 +323,7 @@ def _reduce_layer_norm(slots, h, y, bias=None, residual=None, weight=None, norm_
     return m.done()
 
 
-def _linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, status=None):
+def _linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, status=None, copies=None, stream=None):
     m = _Marshal(arx_linear_args(act=act), x, "x", _PRODUCT_TYPES)
     M, K = m.matrix(x, "x")
     N, _ = m.matrix(w, "w", None, K)
@@ -305,10 +333,12 @@ def _linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, statu
     m.vector(bias, "bias", N)
     m.status(status)
     m.a.M, m.a.N, m.a.K = M, N, K
+    m.copies(copies, _core().lib.arx_linear_copies_bytes, ((x, "x"), (w, "w")), stream)
     return m.done()
 
 
-def _linear_bwd(dout, x, w, dx=None, dw=None, dbias=None, z=None, act=ARX_ACT_NONE, workspace=None, status=None):
+def _linear_bwd(dout, x, w, dx=None, dw=None, dbias=None, z=None, act=ARX_ACT_NONE, workspace=None, status=None,
+                copies=None, stream=None):
     m = _Marshal(arx_linear_bwd_args(act=act), dout, "dout", _PRODUCT_TYPES)
     M, N = m.matrix(dout, "dout")
     K = next((t.shape[-1] for t in (x, w) if t is not None), 0)
@@ -321,6 +351,7 @@ def _linear_bwd(dout, x, w, dx=None, dw=None, dbias=None, z=None, act=ARX_ACT_NO
     m.workspace(workspace)
     m.status(status)
     m.a.M, m.a.N, m.a.K = M, N, K
+    m.copies(copies, _core().lib.arx_linear_bwd_copies_bytes, ((dout, "dout"), (x, "x"), (w, "w")), stream)
     return m.done()
 
 
@@ -331,7 +362,7 @@ class _Plan:
 
     def __init__(self, *args, stream=None, **kwargs):
         core = _core()
-        self._args, self._refs = type(self)._marshal(*args, **kwargs)
+        self._args, self._refs = type(self)._marshal(*args, stream=stream, **kwargs)
         self._ref = ctypes.byref(self._args)
         self._stream = core._stream(stream)
         self._fn = getattr(core.lib, self._name)
@@ -343,10 +374,12 @@ class _Plan:
 
 
 def _function(name, marshal, doc):
+    """The call and its plan; ``marshal`` also gets the stream, for buffers that it allocates."""
     def call(*args, stream=None, check=True, **kwargs):
         core = _core()
-        a, _ = marshal(*args, **kwargs)
+        a, refs = marshal(*args, stream=stream, **kwargs)  # refs: held until the call is enqueued
         st = getattr(core.lib, name)(ctypes.byref(a), core._stream(stream))
+        del refs
         if check:
             core._check(st)
         return st
@@ -403,20 +436,22 @@ Enqueue h = residual + keep(rank-order sum of slots + bias) / (1 - p), y = layer
 arx_linear, arx_linear_plan = _function("arx_linear", _linear, """\
 Enqueue out = act(x w^T + bias) + residual on the tensor cores.
 
-    ``arx_linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, status=None, stream=None,
-    check=True)``
+    ``arx_linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, status=None, copies=None,
+    stream=None, check=True)``
 
     bf16 or fp16; x [M, K], w [N, K]; bias of the same type or fp32.  ``z`` receives
-    x w^T + bias for the backward pass.  ``out`` may be ``residual``.
+    x w^T + bias for the backward pass.  ``out`` may be ``residual``.  ``copies``: a buffer of
+    ``arx_linear_copies_bytes`` bytes for operands whose rows are off 16 bytes; None: one is
+    allocated on the stream where the call is faster with it (a plan keeps it); False: none.
     """)
 arx_linear_bwd, arx_linear_bwd_plan = _function("arx_linear_bwd", _linear_bwd, """\
 Enqueue dz = dout * act'(z), dx = dz w, dw = dz^T x, dbias = sum over rows of dz.
 
     ``arx_linear_bwd(dout, x, w, dx=None, dw=None, dbias=None, z=None, act=ARX_ACT_NONE, workspace=None,
-    status=None, stream=None, check=True)``
+    status=None, copies=None, stream=None, check=True)``
 
     ``workspace`` of ``arx_linear_bwd_workspace_bytes(M, N)`` bytes, unless there is no
-    activation and no dbias.
+    activation and no dbias.  ``copies`` as in ``arx_linear``.
     """)
 
 
@@ -432,6 +467,18 @@ def arx_linear_bwd_workspace_bytes(M: int, N: int) -> int:
     return int(_core().lib.arx_linear_bwd_workspace_bytes(M, N))
 
 
+def arx_linear_copies_bytes(x, w) -> int:
+    """Bytes of ``copies`` for ``arx_linear`` of these operands; 0: it is faster without."""
+    a, _ = _linear(x, w, None, copies=False)
+    return int(_core().lib.arx_linear_copies_bytes(ctypes.byref(a)))
+
+
+def arx_linear_bwd_copies_bytes(dout, x=None, w=None, dx=None, dw=None, act=ARX_ACT_NONE, workspace=None) -> int:
+    """Bytes of ``copies`` for ``arx_linear_bwd`` with these arguments."""
+    a, _ = _linear_bwd(dout, x, w, dx=dx, dw=dw, act=act, workspace=workspace, copies=False)
+    return int(_core().lib.arx_linear_bwd_copies_bytes(ctypes.byref(a)))
+
+
 __all__ = [
     "ARX_BF16", "ARX_F16", "ARX_F32", "ARX_ACT_NONE", "ARX_ACT_RELU", "ARX_ACT_GELU", "ARX_ACT_GELU_TANH",
     "ARX_ACT_SILU",
@@ -439,4 +486,5 @@ __all__ = [
                                      "reduce_layer_norm", "linear", "linear_bwd")
       for suffix in ("", "_plan", "_args")),
     "arx_layer_norm_bwd_workspace_bytes", "arx_dropout_add_bwd_workspace_bytes", "arx_linear_bwd_workspace_bytes",
+    "arx_linear_copies_bytes", "arx_linear_bwd_copies_bytes",
 ]

@@ -7,11 +7,14 @@
 // brings 64-element boxes into 128-byte-swizzled shared memory either way and
 // the descriptors name the layout, so nothing is transposed in memory.
 //
-// Roles (warps): one copies, one issues the matrix instructions, four read
+// Roles (warps): one copies, one issues the matrix instructions, eight read
 // the accumulators and run the epilogue; operands pass through a ring of
-// stages guarded by mbarriers.  Matrices that the copy engine cannot address
+// stages guarded by mbarriers.  Operands that the copy engine cannot address
 // (rows off 16 bytes) are loaded by 512 more threads into the same swizzled
-// stages.
+// stages, beside four epilogue warps.
+//
+// Every wait on a barrier is bounded (tensor_core.cuh); a block whose wait ran
+// out sets the call's status word, waits for what it has in flight, and ends.
 //
 // Three forms:
 //  vector one or two rows (decode): dot products on the CUDA cores, see
@@ -51,9 +54,7 @@ constexpr uint32_t kMaxStages = 12;
 // up to 128 accumulator columns, fit an SM at a time, so the blocks on an SM
 // never want more tensor memory than it has (a block that waited for columns
 // while its cluster waited for it could wait forever); of those with loading
-// threads (704) one fits.  Loads of threads pass through what the stages leave
-// of the SM's memory as L1: [1003, 4100] x [2044, 4100] took 64 us beside 96 KB
-// of stages and 125 beside 192.
+// threads (704) one fits, and two to four stages took the same time.
 constexpr uint32_t kStageBudget = 196608, kSplitBudget = 98304, kLoadedBudget = 98304;
 constexpr uint32_t kStagedBytes = 32 * 33 * 4;  // of an epilogue warp of the wide form
 constexpr uint32_t kMostShared = kStageBudget + 1024 + 8 * kStagedBytes;
@@ -111,7 +112,8 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, u
 enum Layout : uint32_t {
   kKMajor,    // matrix rows: one box of 64 contraction elements
   kMnMajor,   // contraction rows: a box for every 64 matrix rows
-  kMnBlocks,  // the same with whole blocks of 64: one box over the blocks of a map (64, k, block)
+  kMnBlocks,  // the same with whole blocks of 64: one box over the blocks of a map (64, k, block);
+              // dz^T x of 8192 x 4096 over 8185 tokens: 309 us, with a box to each block 361
 };
 
 template <bool kPair>
@@ -904,17 +906,19 @@ cudaError_t launch_split(const GemmArgs& a, const CUtensorMap (&m)[4], cudaStrea
 uint32_t ceil_div(uint64_t a, uint64_t b) { return uint32_t((a + b - 1) / b); }
 
 // Which form, with how many rows of Q to a tile and how many blocks to a
-// tile's contraction: the one with the least estimated time, in SM cycles.
+// tile's contraction: the one with the least estimated time, in SM cycles, on
+// 152 SMs (a constant: the form decides the order of a sum).
 struct Form {
   bool wide;
   uint32_t bn, split, subs;
+  double cycles;
 };
 
-Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, uint32_t sms) {
+Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy) {
+  constexpr uint32_t sms = 152;
   Form best{};
-  double least = 0;
-  const auto consider = [&](const Form& f, double cycles) {
-    if (best.bn == 0 || cycles < least) best = f, least = cycles;
+  const auto consider = [&](const Form& f) {
+    if (best.bn == 0 || f.cycles < best.cycles) best = f;
   };
   // A stage of `rows` rows of c.p and `cols` of c.q costs its copies or its
   // products, whichever is longer.  Measured: an SM takes in 46 bytes a cycle
@@ -929,14 +933,14 @@ Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, ui
   for (uint32_t bn = 256; bn >= 128; bn /= 2) {
     const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, bn);
     const double waves = ceil_div(tiles, sms / 2);
-    consider(Form{true, bn, 1, 1}, waves * steps * stage(kLanes, bn / 2, bn, 46, 12) + 6000 + 40 * bn);
+    consider({true, bn, 1, 1, waves * steps * stage(kLanes, bn / 2, bn, 46, 12) + 6000 + 40 * bn});
   }
   // Two accumulators to a tile: 1290 cycles a stage (630 us against 681 at
   // 8192^3, where the card's power sets the clock), and no tile's epilogue runs
   // under the next one's products.
   if (!threads) {
     const double waves = ceil_div(ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, 512), sms / 2);
-    consider(Form{true, 256, 1, 2}, waves * (steps * 1290.0 + 4000) + 6000 + 40 * 256);
+    consider({true, 256, 1, 2, waves * (steps * 1290.0 + 4000) + 6000 + 40 * 256});
   }
   // Joining and storing a tile takes about 25 cycles a row of Q, 45 through
   // the cluster; starting and ending a block 6000, which two blocks on an SM
@@ -947,13 +951,59 @@ Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, ui
     for (uint32_t split = 1; split <= 8 && (split == 1 || split <= steps); split *= 2) {
       // Clusters at work at once, one block to an SM: those of 4 and 8 leave some
       // SMs of a processing cluster over.
-      const uint32_t at_once = split == 8 ? sms * 14 / 152 : split == 4 ? sms * 36 / 152 : sms / split;
+      const uint32_t at_once = split == 8 ? 14 : split == 4 ? 36 : sms / split;
       const double join = (split > 1 ? 45 : 25) * bn;
       const double on_sm = two ? ceil_div(uint64_t(tiles) * split, sms) : ceil_div(tiles, at_once);
       const double own = ceil_div(steps, split) * stage(bn, kLanes, bn, two && on_sm > 1 ? 44 : 36, 16) + join;
-      consider(Form{false, bn, split, 1}, two ? on_sm * own + 6000 : on_sm * (own + 6000));
+      consider({false, bn, split, 1, two ? on_sm * own + 6000 : on_sm * (own + 6000)});
     }
     if (bn >= c.rows) break;
+  }
+  return best;
+}
+
+// Does the dot form take the call, and with units of 8 elements?
+bool dot_units(const GemmCall& c) {
+  return c.k % 8 == 0 && copyable(static_cast<const uint16_t*>(c.p), c.ldp, c.rows) &&
+         copyable(static_cast<const uint16_t*>(c.q), c.ldq, c.cols);
+}
+bool dot_form(const GemmCall& c) {
+  // Element by element the dot form is the slower one from about 8 million
+  // weights (one token of 4099 -> 2047: 15.9 us against the split form's 15.6;
+  // of 8193 -> 8191: 138 against 49).
+  return c.rows <= kDotRows && !c.p_mn && !c.q_mn && (dot_units(c) || c.cols * c.k < (uint64_t(1) << 23));
+}
+
+// The copy engine takes operands whose rows are on 16 bytes; an empty one has no map.
+bool p_copyable(const GemmCall& c) {
+  return c.k > 0 && copyable(static_cast<const uint16_t*>(c.p), c.ldp, c.p_mn ? c.k : c.rows);
+}
+bool q_copyable(const GemmCall& c) {
+  return c.k > 0 && copyable(static_cast<const uint16_t*>(c.q), c.ldq, c.q_mn ? c.k : c.cols);
+}
+
+// Operands to be brought onto rows of 16 bytes first: the set with the least
+// estimated time of copies and product.
+struct Copies {
+  bool p, q;
+  uint64_t p_bytes, q_bytes;  // 0 for an operand that stays
+};
+uint64_t copy_pitch(uint64_t inner) { return (inner + 7) / 8 * 8; }
+
+Copies choose_copies(const GemmCall& c) {
+  const bool p_copy = p_copyable(c), q_copy = q_copyable(c);
+  Copies best{};
+  if (c.rows == 0 || c.cols == 0 || c.k == 0 || (p_copy && q_copy) || dot_form(c)) return best;
+  const uint32_t steps = ceil_div(c.k, kStep);
+  const uint64_t p_bytes = (c.p_mn ? c.k * copy_pitch(c.rows) : c.rows * copy_pitch(c.k)) * 2,
+                 q_bytes = (c.q_mn ? c.k * copy_pitch(c.cols) : c.cols * copy_pitch(c.k)) * 2;
+  double least = choose_form(c, steps, p_copy, q_copy).cycles;
+  for (int set = 1; set < 4; ++set) {
+    const bool p = set & 1, q = set & 2;
+    if ((p && p_copy) || (q && q_copy)) continue;
+    const uint64_t bytes = (p ? p_bytes : 0) + (q ? q_bytes : 0);
+    const double cycles = choose_form(c, steps, p_copy || p, q_copy || q).cycles + 2500 + double(bytes) / 1500;
+    if (cycles < least) least = cycles, best = {p, q, p ? p_bytes : 0, q ? q_bytes : 0};
   }
   return best;
 }
@@ -967,8 +1017,35 @@ cudaError_t launch_dot(const GemmArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+size_t gemm_copies_bytes(const GemmCall& c) {
+  const Copies k = choose_copies(c);
+  return size_t((k.p_bytes + 15) / 16 * 16 + k.q_bytes);
+}
+
 cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   cudaError_t err = cudaSuccess;
+  if (c.copies) {
+    const Copies k = choose_copies(c);
+    if (k.p || k.q) {
+      GemmCall on = c;
+      on.copies = nullptr;
+      RealignPair r{};
+      const auto add = [&](const void* src, uint64_t ld, uint64_t rows, uint64_t cols, void* dst) {
+        r.m[r.n++] = {static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), rows, ld, copy_pitch(cols), int64_t(cols)};
+      };
+      if (k.p) {
+        add(c.p, c.ldp, c.p_mn ? c.k : c.rows, c.p_mn ? c.rows : c.k, c.copies);
+        on.p = c.copies, on.ldp = r.m[0].ld_dst;
+      }
+      if (k.q) {
+        void* dst = static_cast<uint8_t*>(c.copies) + (k.p_bytes + 15) / 16 * 16;
+        add(c.q, c.ldq, c.q_mn ? c.k : c.cols, c.q_mn ? c.cols : c.k, dst);
+        on.q = dst, on.ldq = r.m[r.n - 1].ld_dst;
+      }
+      err = launch_realign(r, st);
+      return err != cudaSuccess ? err : launch_gemm(on, st);
+    }
+  }
   const int sms = current_sm_count(&err);
   if (sms < 1) return err;
   GemmArgs a{};
@@ -992,12 +1069,8 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   a.octets = out_aligned(8) && c.cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
 
   const bool bf16 = c.dtype == ARX_BF16;
-  const bool units = c.k % 8 == 0 && copyable(static_cast<const uint16_t*>(c.p), c.ldp, c.rows) &&
-                     copyable(static_cast<const uint16_t*>(c.q), c.ldq, c.cols);
-  // Element by element the dot form is the slower one from about 8 million
-  // weights (one token of 4099 -> 2047: 15.9 us against the split form's 15.6;
-  // of 8193 -> 8191: 138 against 49).
-  if (c.rows <= kDotRows && !c.p_mn && !c.q_mn && (units || c.cols * c.k < (uint64_t(1) << 23))) {
+  if (dot_form(c)) {
+    const bool units = dot_units(c);
     a.p = static_cast<const uint16_t*>(c.p), a.q = static_cast<const uint16_t*>(c.q);
     a.ldp = c.ldp, a.ldq = c.ldq;
     a.P = uint32_t(c.rows), a.Q = uint32_t(c.cols);
@@ -1009,16 +1082,15 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   }
 
   const auto *cp = static_cast<const uint16_t*>(c.p), *cq = static_cast<const uint16_t*>(c.q);
-  // The copy engine takes operands whose rows are on 16 bytes (an empty one has
-  // no map); threads read the others, in words of 8 bytes where every row is
-  // aligned to them.
+  // Threads read what the copy engine cannot, in words of 8 bytes where every
+  // row is aligned to them.
   const uint64_t cp_rows = c.p_mn ? a.K : c.rows, cq_rows = c.q_mn ? a.K : c.cols;
-  const bool cp_copy = a.K > 0 && copyable(cp, c.ldp, cp_rows), cq_copy = a.K > 0 && copyable(cq, c.ldq, cq_rows);
+  const bool cp_copy = p_copyable(c), cq_copy = q_copyable(c);
   uint64_t bits = 0;
   if (!cp_copy) bits |= reinterpret_cast<uintptr_t>(cp) | (cp_rows > 1 ? c.ldp * 2 : 0);
   if (!cq_copy) bits |= reinterpret_cast<uintptr_t>(cq) | (cq_rows > 1 ? c.ldq * 2 : 0);
   const uint32_t word = cp_copy && cq_copy ? 16 : bits % 8 == 0 ? 8 : 2;
-  const Form form = choose_form(c, a.steps, cp_copy, cq_copy, uint32_t(sms));
+  const Form form = choose_form(c, a.steps, cp_copy, cq_copy);
   const bool wide = form.wide;
   a.bn = form.bn;
   a.split = form.split;

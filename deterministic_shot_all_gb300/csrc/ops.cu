@@ -132,6 +132,59 @@ uint64_t round16(uint64_t x) { return (x + 15) / 16 * 16; }
     if (s_ != ARX_OK) return s_;           \
   } while (0)
 
+arx_status check_copies(const void* p, uint64_t have, uint64_t need) {
+  if (need == 0) return ARX_OK;
+  if (reinterpret_cast<uintptr_t>(p) % 16) return report(ARX_EINVAL, "copies not 16-byte aligned");
+  if (have < need)
+    return report(ARX_EINVAL, "copies %llu bytes, need %llu", (unsigned long long)have, (unsigned long long)need);
+  return ARX_OK;
+}
+
+// The products of a layer, without their outputs: sizes, operands, types.
+arx::GemmCall product(const void* p, uint64_t ldp, bool p_mn, const void* q, uint64_t ldq, bool q_mn, uint64_t rows,
+                      uint64_t cols, uint64_t k, int dtype, int wdtype, uint32_t* status) {
+  arx::GemmCall c{};
+  c.p = p, c.ldp = (p_mn ? k : rows) <= 1 ? (p_mn ? rows : k) : ldp, c.p_mn = p_mn;
+  c.q = q, c.ldq = (q_mn ? k : cols) <= 1 ? (q_mn ? cols : k) : ldq, c.q_mn = q_mn;
+  c.rows = rows, c.cols = cols, c.k = k;
+  c.act = ARX_ACT_NONE, c.dtype = dtype, c.wdtype = wdtype, c.status = status;
+  return c;
+}
+arx::GemmCall forward_product(const arx_linear_args& a) {
+  return product(a.x, a.ldx, false, a.w, a.ldw, false, a.M, a.N, a.K, a.dtype, a.wdtype, a.status);
+}
+// dx = dz w: w's rows are the contraction.
+arx::GemmCall dx_product(const arx_linear_bwd_args& a, const void* dz, uint64_t lddz) {
+  return product(dz, lddz, false, a.w, a.ldw, true, a.M, a.K, a.N, a.dtype, a.wdtype, a.status);
+}
+// dw = dz^T x: the rows of both are.
+arx::GemmCall dw_product(const arx_linear_bwd_args& a, const void* dz, uint64_t lddz) {
+  return product(dz, lddz, true, a.x, a.ldx, true, a.N, a.K, a.M, a.dtype, a.wdtype, a.status);
+}
+
+// Where the products of a backward pass find dz: in the workspace (rows of N
+// rounded up to 8), or dout itself without an activation -- unless its rows are
+// off 16 bytes and there is a workspace: a copy on aligned rows costs its
+// bytes, and both products load their larger operand by the copy engine
+// ([1001, 2047] x 2049: 148 us without, 117 with).
+bool dz_in_workspace(const arx_linear_bwd_args& a) {
+  if (!a.dx && !a.dw) return false;
+  if (a.act != ARX_ACT_NONE) return true;
+  const bool off = reinterpret_cast<uintptr_t>(a.dout) % 16 || (a.M > 1 && a.lddout % 8);
+  return off && a.workspace && reinterpret_cast<uintptr_t>(a.workspace) % 16 == 0 &&
+         a.workspace_bytes >= arx_linear_bwd_workspace_bytes(a.M, a.N);
+}
+
+size_t backward_copies_bytes(const arx_linear_bwd_args& a) {
+  const bool ws = dz_in_workspace(a);
+  // Any address on 16 bytes stands for a workspace that is not there yet.
+  const void* dz = ws ? reinterpret_cast<const void*>(uintptr_t(16)) : a.dout;
+  const uint64_t lddz = ws ? (a.N + 7) / 8 * 8 : a.lddout;
+  const size_t dx = a.dx ? arx::gemm_copies_bytes(dx_product(a, dz, lddz)) : 0,
+               dw = a.dw ? arx::gemm_copies_bytes(dw_product(a, dz, lddz)) : 0;
+  return dx > dw ? dx : dw;
+}
+
 }  // namespace
 
 extern "C" {
@@ -262,33 +315,37 @@ arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stre
   return launched(arx::launch_reduce_layer_norm(*a, v, static_cast<cudaStream_t>(stream)), "arx_reduce_layer_norm");
 }
 
+size_t arx_linear_copies_bytes(const arx_linear_args* a) {
+  if (!a || a->M > kMaxDim || a->N > kMaxDim || a->K > kMaxDim) return 0;
+  return arx::gemm_copies_bytes(forward_product(*a));
+}
+
 arx_status arx_linear(const arx_linear_args* a, void* stream) {
   if (!a) return report(ARX_EINVAL, "null arguments");
   ARX_TRY(check_types(a->dtype, a->wdtype, false));
   ARX_TRY(check_dims(a->M, a->N, a->K));
   if (a->act < ARX_ACT_NONE || a->act > ARX_ACT_SILU) return report(ARX_EINVAL, "unknown activation %d", a->act);
   if (a->M == 0 || a->N == 0) return ok();
+  arx::GemmCall c = forward_product(*a);
+  const size_t copies = a->copies ? arx::gemm_copies_bytes(c) : 0;
+  ARX_TRY(check_copies(a->copies, a->copies_bytes, copies));
   const Mat in[] = {mat("residual", a->residual, a->M, a->N, a->ldresidual, a->dtype),
                     mat("x", a->x, a->M, a->K, a->ldx, a->dtype), mat("w", a->w, a->N, a->K, a->ldw, a->dtype),
                     vec("bias", a->bias, a->N, a->wdtype)};
   const Mat out[] = {mat("out", a->out, a->M, a->N, a->ldout, a->dtype), mat("z", a->z, a->M, a->N, a->ldz, a->dtype),
-                     vec("status", a->status, 1, ARX_F32)};
+                     vec("status", a->status, 1, ARX_F32), vec("copies", a->copies, copies / 2, ARX_BF16)};
   for (int i = 0; i < 4; ++i) ARX_TRY(check_mat(in[i], i == 1 || i == 2));
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     ARX_TRY(check_mat(out[i], i == 0));
     ARX_TRY(check_output(out[i], in, 4, i == 0 ? 1u : 0u));
     ARX_TRY(check_output(out[i], out, i, 0));
   }
-  arx::GemmCall c{};
-  c.p = a->x, c.ldp = in[1].ld;
-  c.q = a->w, c.ldq = in[2].ld;
-  c.rows = a->M, c.cols = a->N, c.k = a->K;
   c.out = a->out, c.ldout = out[0].ld;
   c.z = a->z, c.ldz = out[1].ld;
   c.bias = a->bias;
   c.residual = a->residual, c.ldresidual = in[0].ld;
-  c.act = a->act, c.dtype = a->dtype, c.wdtype = a->wdtype;
-  c.status = a->status;
+  c.act = a->act;
+  if (copies) c.copies = a->copies;
   return launched(arx::launch_gemm(c, static_cast<cudaStream_t>(stream)), "arx_linear");
 }
 
@@ -296,6 +353,11 @@ arx_status arx_linear(const arx_linear_args* a, void* stream) {
 size_t arx_linear_bwd_workspace_bytes(uint64_t M, uint64_t N) {
   if (M > kMaxDim || N > kMaxDim) return 0;
   return size_t(round16(M * ((N + 7) / 8 * 8) * 2) + arx::column_parts(M, N) * N * 4);
+}
+
+size_t arx_linear_bwd_copies_bytes(const arx_linear_bwd_args* a) {
+  if (!a || a->M > kMaxDim || a->N > kMaxDim || a->K > kMaxDim) return 0;
+  return backward_copies_bytes(*a);
 }
 
 arx_status arx_linear_bwd(const arx_linear_bwd_args* a, void* stream) {
@@ -311,38 +373,35 @@ arx_status arx_linear_bwd(const arx_linear_bwd_args* a, void* stream) {
                     mat("w", a->dx ? a->w : nullptr, a->N, a->K, a->ldw, a->dtype)};
   const bool first_pass = (act && products) || a->dbias;
   const uint64_t need = first_pass ? arx_linear_bwd_workspace_bytes(a->M, a->N) : 0;
+  const size_t copies = a->copies ? backward_copies_bytes(*a) : 0;
+  ARX_TRY(check_copies(a->copies, a->copies_bytes, copies));
   const Mat out[] = {mat("dx", a->dx, a->M, a->K, a->lddx, a->dtype), mat("dw", a->dw, a->N, a->K, a->lddw, a->dtype),
                      vec("dbias", a->dbias, a->N, a->wdtype),
                      vec("workspace", a->workspace, a->workspace_bytes / 2, ARX_BF16),
-                     vec("status", a->status, 1, ARX_F32)};
+                     vec("status", a->status, 1, ARX_F32), vec("copies", a->copies, copies / 2, ARX_BF16)};
   ARX_TRY(check_workspace(a->workspace, a->workspace_bytes, need));
   ARX_TRY(check_mat(in[0], true));
   ARX_TRY(check_mat(in[1], act));
   ARX_TRY(check_mat(in[2], a->dw != nullptr));
   ARX_TRY(check_mat(in[3], a->dx != nullptr));
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < 6; ++i) {
     ARX_TRY(check_mat(out[i], false));
     ARX_TRY(check_output(out[i], in, 4, 0));
     ARX_TRY(check_output(out[i], out, i, 0));
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
-  // dz and dbias in one pass over dout; dout itself is dz without an activation
-  // -- unless its rows are off 16 bytes and there is a workspace: a copy on
-  // aligned rows costs its bytes, and both products load their larger operand
-  // by the copy engine ([1001, 2047] x 2049: 148 us without, 117 with).
+  // dz and dbias in one pass over dout.
   const void* dz = a->dout;
   uint64_t lddz = in[0].ld;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-  const bool off = in[0].begin() % 16 || (in[0].rows > 1 && in[0].ld % 8);
-  const bool copy = products && !act && off && ws && reinterpret_cast<uintptr_t>(ws) % 16 == 0 &&
-                    a->workspace_bytes >= arx_linear_bwd_workspace_bytes(a->M, a->N);
-  if ((first_pass || copy) && a->N) {
+  const bool store = dz_in_workspace(*a);
+  if ((first_pass || store) && a->N) {
     arx::ActGradCall g{};
     g.dout = a->dout, g.lddout = in[0].ld;
     g.rows = a->M, g.cols = a->N;
     if (act) g.z = a->z, g.ldz = in[1].ld;
-    if (products && (act || copy)) {
+    if (store) {
       lddz = g.lddz = (a->N + 7) / 8 * 8;
       dz = g.dz = ws;
     }
@@ -352,22 +411,17 @@ arx_status arx_linear_bwd(const arx_linear_bwd_args* a, void* stream) {
     const cudaError_t e = arx::launch_act_grad(g, units(in[0]) && units(in[1]), st);
     if (e != cudaSuccess) return launched(e, "arx_linear_bwd");
   }
-  arx::GemmCall c{};
-  c.p = dz, c.ldp = lddz;
-  c.act = ARX_ACT_NONE, c.dtype = a->dtype, c.wdtype = a->wdtype;
-  c.status = a->status;
-  if (a->dx && a->M && a->K) {  // dx = dz w: w's rows are the contraction
-    c.q = a->w, c.ldq = in[3].ld, c.q_mn = true;
-    c.rows = a->M, c.cols = a->K, c.k = a->N;
+  if (a->dx && a->M && a->K) {
+    arx::GemmCall c = dx_product(*a, dz, lddz);
     c.out = a->dx, c.ldout = out[0].ld;
+    if (copies) c.copies = a->copies;
     const cudaError_t e = arx::launch_gemm(c, st);
     if (e != cudaSuccess) return launched(e, "arx_linear_bwd");
   }
-  if (a->dw && a->N && a->K) {  // dw = dz^T x: the rows of both are the contraction
-    c.p_mn = true;
-    c.q = a->x, c.ldq = in[2].ld, c.q_mn = true;
-    c.rows = a->N, c.cols = a->K, c.k = a->M;
+  if (a->dw && a->N && a->K) {  // its copies take the place of the other's, which have been read by then
+    arx::GemmCall c = dw_product(*a, dz, lddz);
     c.out = a->dw, c.ldout = out[1].ld;
+    if (copies) c.copies = a->copies;
     const cudaError_t e = arx::launch_gemm(c, st);
     if (e != cudaSuccess) return launched(e, "arx_linear_bwd");
   }

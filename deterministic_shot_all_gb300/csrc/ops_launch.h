@@ -87,7 +87,25 @@ struct GemmCall {
   uint64_t ldout, ldz, ldresidual;
   int act, dtype, wdtype;
   uint32_t* status;
+  void* copies;           // gemm_copies_bytes(c) bytes, or null
 };
 cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st);
+// Bytes for copies of the operands whose rows are off 16 bytes, 0 where the
+// product is faster without.
+size_t gemm_copies_bytes(const GemmCall& c);
+
+// Copies of 16-bit matrices: rows of `cols` elements from `ld` to `ld_dst`
+// (a multiple of 2, at least cols) apart, dst on 4 bytes.
+struct Realign {
+  const uint16_t* src;
+  uint16_t* dst;
+  uint64_t rows, ld, ld_dst;
+  int64_t cols;
+};
+struct RealignPair {
+  Realign m[2];
+  int n;
+};
+cudaError_t launch_realign(const RealignPair& pair, cudaStream_t st);
 
 }  // namespace arx

@@ -1,5 +1,6 @@
 /*
- * arx.h -- C ABI of the deterministic W-way bf16 reduce on one GB300 (sm_103a).
+ * arx.h -- C ABI of the deterministic W-way bf16 reduce on one GB300 (sm_103a),
+ * and of the operators around it in a tensor-parallel sublayer (last section).
  *
  * The operation is the data-parallel core of the one-shot all-reduce of
  * arx.cu ("one-shot all-reduce over RoCE for GB10, no NCCL"): the sum of W
@@ -24,9 +25,10 @@
  *  - Errors are returned as arx_status; nothing calls exit() or throws.
  *    Argument errors are detected on the host before anything is enqueued.
  *    arx_last_error() gives a one-line detail for the calling thread.
- *  - Enqueuing entry points (arx_reduce, arx_step) launch kernels only, so
- *    they can be captured into a CUDA graph (arx.cu: allreduce "runs on the
- *    current stream and is CUDA-graph capturable").
+ *  - Enqueuing entry points (arx_reduce, arx_step and the operators of the
+ *    last section) launch kernels only, so they can be captured into a CUDA
+ *    graph (arx.cu: allreduce "runs on the current stream and is CUDA-graph
+ *    capturable").
  */
 #ifndef ARX_H_
 #define ARX_H_
@@ -718,8 +720,13 @@ arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stre
  *         device error word (ARX_ETIMEOUT in the low byte) if a wait of the
  *         kernel for its own copies or products ran out; the outputs are then
  *         unspecified.  No input causes it.
- * Rows whose address or leading dimension is not a multiple of 16 bytes are
- * loaded by threads instead of by the copy engine, at a lower rate. */
+ *   copies  arx_linear_copies_bytes(a) bytes on 16 bytes, or NULL.  The copy
+ *         engine takes rows whose address and leading dimension are multiples of
+ *         16 bytes.  An operand of other rows is loaded by threads, at a lower
+ *         rate, or first copied here where that is estimated to be faster
+ *         (arx_linear_copies_bytes is 0 where it is not).  It looks at sizes,
+ *         alignment and types only.  The two ways may differ in the order of
+ *         the sums. */
 #define ARX_ACT_NONE 0
 #define ARX_ACT_RELU 1
 #define ARX_ACT_GELU 2
@@ -734,11 +741,14 @@ typedef struct arx_linear_args {
   void* out;
   void* z;
   uint32_t* status;
+  void* copies;
+  uint64_t copies_bytes;
   uint64_t M, N, K, ldx, ldw, ldresidual, ldout, ldz;
   int32_t act, dtype, wdtype;
   int32_t reserved;
 } arx_linear_args;
 
+size_t arx_linear_copies_bytes(const arx_linear_args* a);
 arx_status arx_linear(const arx_linear_args* a, void* stream);
 
 /* Its backward pass:
@@ -751,7 +761,9 @@ arx_status arx_linear(const arx_linear_args* a, void* stream);
  *           M == 0 sets dw and dbias to zero.
  *   workspace  arx_linear_bwd_workspace_bytes(M, N) bytes (dz and partial sums);
  *           may be NULL when act is ARX_ACT_NONE and dbias is NULL (given all
- *           the same, a dout whose rows are not on 16 bytes is copied to it) */
+ *           the same, a dout whose rows are not on 16 bytes is copied to it)
+ *   copies  as in the forward, arx_linear_bwd_copies_bytes(a) bytes: of w, then
+ *           of x.  Asked for with the workspace already in `a`. */
 typedef struct arx_linear_bwd_args {
   const void* dout;
   const void* z;
@@ -763,12 +775,15 @@ typedef struct arx_linear_bwd_args {
   void* workspace;
   uint64_t workspace_bytes;
   uint32_t* status;
+  void* copies;
+  uint64_t copies_bytes;
   uint64_t M, N, K, lddout, ldz, ldx, ldw, lddx, lddw;
   int32_t act, dtype, wdtype;
   int32_t reserved;
 } arx_linear_bwd_args;
 
 size_t arx_linear_bwd_workspace_bytes(uint64_t M, uint64_t N);
+size_t arx_linear_bwd_copies_bytes(const arx_linear_bwd_args* a);
 arx_status arx_linear_bwd(const arx_linear_bwd_args* a, void* stream);
 
 #ifdef __cplusplus

@@ -31,7 +31,7 @@ def _matmul(a, b):
 
 
 def _forward(arx, M, N, K, dtype, act="none", bias=True, residual=True, z=True, wdtype=None, pad=0, lead=0, opad=0,
-             olead=0):
+             olead=0, copies=None):
     x = strided(make((M, K), dtype, 1), pad, lead)
     w = strided(make((N, K), dtype, 2, max(K, 1) ** -0.5), pad, lead)
     b = make((N,), wdtype or dtype, 3) if bias else None
@@ -39,7 +39,8 @@ def _forward(arx, M, N, K, dtype, act="none", bias=True, residual=True, z=True, 
     out = Out((M, N), dtype, opad, olead)
     zo = Out((M, N), dtype, opad, olead) if z else None
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    arx.arx_linear(x, w, out.t, bias=b, residual=r, z=zo.t if z else None, act=_code(arx, act), status=status)
+    arx.arx_linear(x, w, out.t, bias=b, residual=r, z=zo.t if z else None, act=_code(arx, act), status=status,
+                   copies=copies)
     torch.cuda.synchronize()
     assert int(status) == 0
     xd, wd = f64(x), f64(w)
@@ -169,7 +170,7 @@ def test_activation_limits(arx, act):
     assert_close(out[0], want, 24 * E * (1 + np.abs(np.where(np.isfinite(z), z, 0))), act)
 
 
-def _backward(arx, M, N, K, dtype, act="none", wdtype=None, pad=0, lead=0, which="xwb"):
+def _backward(arx, M, N, K, dtype, act="none", wdtype=None, pad=0, lead=0, which="xwb", copies=None):
     x = strided(make((M, K), dtype, 1), pad, lead)
     w = strided(make((N, K), dtype, 2), pad, lead)
     d = strided(make((M, N), dtype, 3), pad, lead)
@@ -180,7 +181,7 @@ def _backward(arx, M, N, K, dtype, act="none", wdtype=None, pad=0, lead=0, which
     ws = scratch(arx.arx_linear_bwd_workspace_bytes(M, N))
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     arx.arx_linear_bwd(d, x, w, dx=dx.t if dx else None, dw=dw.t if dw else None, dbias=db.t if db else None, z=z,
-                       act=_code(arx, act), workspace=ws, status=status)
+                       act=_code(arx, act), workspace=ws, status=status, copies=copies)
     torch.cuda.synchronize()
     assert int(status) == 0
     dz, edz = f64(d), np.zeros((M, N))
@@ -348,3 +349,81 @@ def test_offsets_past_32_bits(arx):
     far = buf.as_strided((5, N), (ld, 1))
     arx.arx_linear(src, w, far)
     assert torch.equal(bits(far), bits(want))
+
+
+# Sizes at which operands off 16 bytes are copied to aligned rows, if there is a buffer.
+COPIED = [(300, 2047, 4099), (1003, 2044, 4100), (1300, 2600, 1026)]
+
+
+@pytest.mark.parametrize("copies", [None, False])
+@pytest.mark.parametrize("M,N,K", COPIED)
+@pytest.mark.parametrize("pad,lead", [(0, 0), (0, 1), (3, 2), (5, 7)])
+def test_operands_copied_to_aligned_rows_or_loaded_by_threads(arx, M, N, K, pad, lead, copies):
+    _forward(arx, M, N, K, torch.float16, "silu", pad=pad, lead=lead, copies=copies)
+    _backward(arx, M, N, K, torch.bfloat16, "gelu", pad=pad, lead=lead, copies=copies)
+
+
+@pytest.mark.parametrize("K", [1024, 1025, 1030, 1031, 1535, 1537])
+@pytest.mark.parametrize("xlead,wlead", [(1, 1), (0, 3), (2, 5), (7, 4)])
+def test_copied_operands_give_the_bits_of_aligned_ones(arx, K, xlead, wlead):
+    M, N = 1300, 2600
+    x, w = make((M, K), torch.bfloat16, 1), make((N, K), torch.bfloat16, 2)
+    up = -K % 8
+    got, want = Out((M, N), torch.bfloat16), Out((M, N), torch.bfloat16)
+    xo, wo = strided(x, up, xlead), strided(w, up, wlead)
+    plan = arx.arx_linear_plan(xo, wo, got.t)
+    assert plan._args.copies_bytes == arx.arx_linear_copies_bytes(xo, wo) > 0
+    plan()
+    arx.arx_linear(strided(x, up), strided(w, up), want.t)
+    assert torch.equal(bits(got.t), bits(want.t))
+    got.check_guards()
+
+
+def test_a_row_past_its_end_is_not_read(arx):
+    # NaN around and between the rows of both operands.
+    M, N, K, ld = 1300, 2600, 1027, 1031
+    buf = [torch.full((n * ld + 9,), float("nan"), dtype=torch.bfloat16, device="cuda") for n in (M, N)]
+    x, w = (b[5:5 + n * ld].view(n, ld)[:, :K] for b, n in zip(buf, (M, N)))
+    x.copy_(make((M, K), torch.bfloat16, 1))
+    w.copy_(make((N, K), torch.bfloat16, 2))
+    for copies in (None, False):
+        o = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        dx, dw = torch.empty(M, K, dtype=torch.bfloat16, device="cuda"), torch.empty(N, K, dtype=torch.bfloat16, device="cuda")
+        arx.arx_linear(x, w, o, copies=copies)
+        arx.arx_linear_bwd(o, x, w, dx=dx, dw=dw, copies=copies)
+        assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dw).all())
+
+
+def test_copies_on_a_side_stream_and_in_a_graph(arx):
+    M, N, K = COPIED[0]
+    x, w = make((M, K), torch.bfloat16, 1), make((N, K), torch.bfloat16, 2)
+    want, a, b, c = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    arx.arx_linear(x, w, want)
+    buf = torch.empty(arx.arx_linear_copies_bytes(x, w), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        arx.arx_linear(x, w, a, stream=side)
+        arx.arx_linear(x, w, b, copies=buf)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        arx.arx_linear(x, w, c)
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(bits(t), bits(want)) for t in (a, b, c))
+
+
+def test_large_copies(arx):
+    # Rows of x past an offset of 2^32 elements, one element off alignment.
+    M, N, K, ld = 300, 2047, 4099, 1 << 24
+    buf = torch.zeros(M * ld + 1, dtype=torch.bfloat16, device="cuda")
+    x = buf[1:].as_strided((M, K), (ld, 1), 1)
+    src, w = make((M, K), torch.bfloat16, 4), make((N, K), torch.bfloat16, 5)
+    x.copy_(src)
+    got, want = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert arx.arx_linear_copies_bytes(x, w) > 0
+    arx.arx_linear(x, w, got)
+    arx.arx_linear(src, w, want)
+    assert torch.equal(bits(got), bits(want))

@@ -297,3 +297,39 @@ def test_binding_rejects_tensors_of_the_wrong_kind(arx):
         arx.arx_reduce_layer_norm([x], x, x.half())
     with pytest.raises(ValueError, match="CUDA tensor"):
         arx.arx_linear_plan(x, x, torch.zeros(4, 4, dtype=torch.bfloat16))
+
+
+def _odd(arx, op):
+    """Operands whose rows are off 16 bytes, at a size where copies of them pay."""
+    a = _good(arx, op)
+    M, N, K = 1003, 2044, 4100
+    a.M, a.N, a.K = M, N, K
+    if op == "linear":
+        a.ldx = a.ldw = K
+        a.ldresidual = a.ldout = a.ldz = N
+    else:
+        a.lddout = a.ldz = N
+        a.ldx = a.ldw = a.lddx = a.lddw = K
+        a.workspace_bytes = arx.arx_linear_bwd_workspace_bytes(M, N)
+    return a
+
+
+@pytest.mark.parametrize("op,operand", [("linear", "x"), ("linear_bwd", "w")])
+def test_copies_are_asked_for_and_checked(arx, op, operand):
+    query, call = getattr(arx.lib, f"arx_{op}_copies_bytes"), getattr(arx.lib, f"arx_{op}")
+    a = _odd(arx, op)
+    n = query(ctypes.byref(a))
+    rows = {"linear": 1003 + 2044, "linear_bwd": 2044}[op]
+    assert n == rows * 4104 * 2
+    a.copies, a.copies_bytes = _region(40), n - 1
+    assert call(ctypes.byref(a), None) == arx.ARX_EINVAL and "copies" in arx.arx_last_error()
+    a.copies, a.copies_bytes = _region(40) + 8, n
+    assert call(ctypes.byref(a), None) == arx.ARX_EINVAL and "copies not 16-byte aligned" in arx.arx_last_error()
+    a.copies = getattr(a, operand)
+    assert call(ctypes.byref(a), None) == arx.ARX_EOVERLAP and "copies" in arx.arx_last_error()
+    for name in ("ldx", "ldw"):
+        setattr(a, name, 4104)
+    assert query(ctypes.byref(a)) == 0
+    a.M = 1 << 31
+    assert query(ctypes.byref(a)) == 0
+    assert query(None) == 0
