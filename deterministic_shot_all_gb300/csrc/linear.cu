@@ -415,22 +415,43 @@ __device__ __forceinline__ void finish_boxes(const GemmArgs& a, const CUtensorMa
 // Else: a warp's 32 rows by 32 columns, staged in shared memory
 // as [row][33].  A lane takes a column and walks down the rows, so that the
 // warp accesses a row's line at a time; each lane on its own row, element by
-// element, would touch 32 lines with every access.
-template <int D>
+// element, would touch 32 lines with every access.  kRows rows go together:
+// the activation's branches and the residual's latency once for each of them
+// were 230 cycles a row.
+template <int D, uint32_t kRows>
 __device__ __forceinline__ void finish_staged(const GemmArgs& a, const float* staged, uint32_t row0, uint32_t col,
                                               uint32_t lane) {
   const uint32_t rows = row0 < a.P ? (a.P - row0 < 32 ? a.P - row0 : 32) : 0;
   if (col >= a.Q) return;
   const float bias = a.bias ? load_param(a.bias, a.wdtype, col) : 0.0f;
-#pragma unroll 8
-  for (uint32_t r = 0; r < rows; ++r) {
+#pragma unroll 1
+  for (uint32_t r = 0; r < rows; r += kRows) {
     const uint64_t row = row0 + r;
-    float v[1] = {staged[r * 33 + lane] + bias};
-    float res = 0.0f;
-    if (a.residual) res = Elem<D>::widen(a.residual[row * a.ldresidual + col]);
-    if (a.z) a.z[row * a.ldz + col] = Elem<D>::round(v[0]);
-    activate<1>(v, a.act);
-    a.out[row * a.ldout + col] = Elem<D>::round(v[0] + res);
+    const uint32_t n = rows - r;
+    uint16_t res[kRows];
+    if (a.residual) {
+      const uint16_t* p = a.residual + row * a.ldresidual + col;
+#pragma unroll
+      for (uint32_t k = 0; k < kRows; ++k) res[k] = k < n ? p[k * a.ldresidual] : 0;
+    }
+    float v[kRows];
+#pragma unroll
+    for (uint32_t k = 0; k < kRows; ++k) v[k] = staged[(r + k) * 33 + lane] + bias;
+    if (a.z) {
+      uint16_t* z = a.z + row * a.ldz + col;
+#pragma unroll
+      for (uint32_t k = 0; k < kRows; ++k)
+        if (k < n) z[k * a.ldz] = Elem<D>::round(v[k]);
+    }
+    activate<kRows>(v, a.act);
+    if (a.residual) {
+#pragma unroll
+      for (uint32_t k = 0; k < kRows; ++k) v[k] += Elem<D>::widen(res[k]);
+    }
+    uint16_t* out = a.out + row * a.ldout + col;
+#pragma unroll
+    for (uint32_t k = 0; k < kRows; ++k)
+      if (k < n) out[k * a.ldout] = Elem<D>::round(v[k]);
   }
 }
 
@@ -640,7 +661,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
               for (int k = 0; k < 16; ++k) staged[lane * 33 + h + k] = v[k];
             }
             __syncwarp();
-            finish_staged<D>(a, staged, row0, col0 + c + lane, lane);
+            finish_staged<D, kTma ? 16 : 8>(a, staged, row0, col0 + c + lane, lane);
           }
         }
       }
