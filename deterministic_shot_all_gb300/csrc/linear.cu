@@ -77,6 +77,7 @@ struct GemmArgs {
   uint32_t stages, stage_bytes;
   uint32_t steps;      // stages' worth of contraction: ceil(K / 64)
   uint32_t split;      // blocks of a cluster that share a tile's contraction
+  uint32_t whole, pieces;  // wide form: tiles that are one piece, and pieces in all
   uint32_t tiles_p, tiles_q;
   uint32_t idesc, tmem_columns;
   uint32_t quads, octets;  // out, z and residual allow accesses of 4 elements; of 8, bias and width too
@@ -576,6 +577,26 @@ __device__ __forceinline__ void tile_at(const GemmArgs& a, uint32_t t, uint32_t&
   tp = 8u * b + (in - tq * rows);
 }
 
+// The kernel's work in order.  Two accumulators to a tile (kSubs == 2): where
+// the tiles past the last whole round of the grid would leave half of it or
+// more without one, each of them is two pieces of one accumulator.
+struct Piece {
+  uint32_t tp, q0, subs;
+};
+template <uint32_t kSubs>
+__device__ __forceinline__ Piece piece_at(const GemmArgs& a, uint32_t t) {
+  Piece w{0, 0, kSubs};
+  uint32_t tq, sub = 0;
+  if (kSubs == 2 && t >= a.whole) {
+    sub = (t - a.whole) & 1;
+    w.subs = 1;
+    t = a.whole + (t - a.whole) / 2;
+  }
+  tile_at(a, t, w.tp, tq);
+  w.q0 = (tq * kSubs + sub) * a.bn;
+  return w;
+}
+
 // kSubs: accumulators to a tile.
 template <int D, int kWord, bool kBoth, uint32_t kSubs>
 __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
@@ -589,32 +610,36 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31, rank = cluster_ctarank();
   setup<kTma, true>(a, &mp, &mq, s, warp);
   dependent_launch_prologue();
-  const uint32_t tiles = a.tiles_p * a.tiles_q, first_tile = blockIdx.x / 2, step = gridDim.x / 2;
+  const uint32_t pieces = a.pieces, first_piece = blockIdx.x / 2, step = gridDim.x / 2;
 
   Ring ring;
   uint32_t issued = 0;
   const bool copies = threadIdx.x == 0 && (a.p_copy | a.q_copy), loads = !kTma && threadIdx.x >= kFirstLoader<kTma>;
   if (copies || loads) {
-    for (uint32_t t = first_tile; t < tiles; t += step) {
-      uint32_t tp, tq;
-      tile_at(a, t, tp, tq);
-      const uint32_t p0 = (2 * tp + rank) * kLanes, q0 = tq * kSubs * a.bn + rank * a.bq;
+    for (uint32_t t = first_piece; t < pieces; t += step) {
+      const Piece w = piece_at<kSubs>(a, t);
+      const uint32_t p0 = (2 * w.tp + rank) * kLanes, q0 = w.q0 + rank * a.bq;
       issued = a.stages;
       bool ok = true;
-      if (copies)
+      if (copies && kSubs == 2 && w.subs == 2)
         ok = copy_tile<true, kSubs>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
+      else if (copies)
+        ok = copy_tile<true, 1>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
       else if constexpr (!kTma)
         ok = load_tile<kWord, kBoth, true>(a, s, stages, ring, p0, q0, 0, a.steps, threadIdx.x - kFirstLoader<kTma>);
       if (!ok) break;
     }
   } else if (warp == 1 && lane == 0 && rank == 0 && a.steps > 0) {
     uint32_t n = 0;
-    for (uint32_t t = first_tile; t < tiles; t += step, ++n) {
+    for (uint32_t t = first_piece; t < pieces; t += step, ++n) {
       // One accumulator to a tile: two tiles' alternate.  Two: the tile has both.
       const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
       if (!mbar_wait(addr_of(&s.acc_empty[b]), (use & 1) ^ 1, &s.abort)) break;
       tmem_fence_after();
-      if (!multiply_tile<true, kSubs>(a, s, addr_of(stages), ring, s.tmem + b * 256, 0, a.steps)) break;
+      const uint32_t subs = piece_at<kSubs>(a, t).subs;
+      if (!(kSubs == 2 && subs == 2 ? multiply_tile<true, kSubs>(a, s, addr_of(stages), ring, s.tmem, 0, a.steps)
+                                    : multiply_tile<true, 1>(a, s, addr_of(stages), ring, s.tmem + b * 256, 0, a.steps)))
+        break;
       mma_commit<true>(addr_of(&s.acc_full[b]));
     }
   } else if (warp >= 2 && warp < 2 + kEpilogueWarps<kTma>) {
@@ -622,17 +647,16 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     float* staged = reinterpret_cast<float*>(stages + a.stages * a.stage_bytes) + (warp - 2) * 32 * 33;
     Boxes boxes{addr_of(stages + a.stages * a.stage_bytes) + (warp - 2) * 4096, 0};
     uint32_t n = 0;
-    for (uint32_t t = first_tile; t < tiles; t += step, ++n) {
-      uint32_t tp, tq;
-      tile_at(a, t, tp, tq);
+    for (uint32_t t = first_piece; t < pieces; t += step, ++n) {
+      const Piece w = piece_at<kSubs>(a, t);
       const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
       if (a.steps > 0) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.abort))) break;
         tmem_fence_after();
       }
-      const uint32_t row0 = (2 * tp + rank) * kLanes + quarter * 32;
-      for (uint32_t j = 0; j < kSubs; ++j) {
-        const uint32_t col0 = (tq * kSubs + j) * a.bn, acc = s.tmem + (b + j) * 256 + (quarter * 32 << 16);
+      const uint32_t row0 = (2 * w.tp + rank) * kLanes + quarter * 32;
+      for (uint32_t j = 0; j < w.subs; ++j) {
+        const uint32_t col0 = w.q0 + j * a.bn, acc = s.tmem + (b + j) * 256 + (quarter * 32 << 16);
         const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
         for (uint32_t c = c0; c < c0 + half && col0 + c < a.Q; c += 32) {
           if (row0 >= a.P) break;  // the whole warp
@@ -912,10 +936,14 @@ cudaError_t launch_cluster(uint32_t blocks, uint32_t threads, uint32_t cluster, 
 // a pair, one block to an SM), or fewer tiles.
 template <int D, int kWord, bool kBoth, uint32_t kSubs>
 cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap (&m)[4], int sms, cudaStream_t st) {
-  const uint32_t tiles = a.tiles_p * a.tiles_q, pairs = uint32_t(sms) / 2;
-  return launch_cluster<gemm_wide_kernel<D, kWord, kBoth, kSubs>>(2 * (tiles < pairs ? tiles : pairs), kGemmThreads<kWord == 16>, 2,
-                                                   1024 + a.stages * a.stage_bytes + kEpilogueWarps<kWord == 16> * kStagedBytes,
-                                                   st, a, m[0], m[1], m[2], m[3]);
+  const uint32_t tiles = a.tiles_p * a.tiles_q, pairs = uint32_t(sms) / 2, rest = tiles % pairs;
+  const bool halves = kSubs == 2 && 2 * rest <= pairs;
+  GemmArgs g = a;
+  g.whole = halves ? tiles - rest : tiles;
+  g.pieces = halves ? tiles + rest : tiles;
+  return launch_cluster<gemm_wide_kernel<D, kWord, kBoth, kSubs>>(
+      2 * (g.pieces < pairs ? g.pieces : pairs), kGemmThreads<kWord == 16>, 2,
+      1024 + g.stages * g.stage_bytes + kEpilogueWarps<kWord == 16> * kStagedBytes, st, g, m[0], m[1], m[2], m[3]);
 }
 
 template <int D, int kWord, bool kBoth>
@@ -960,8 +988,11 @@ Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy) {
   // 8192^3, where the card's power sets the clock), and no tile's epilogue runs
   // under the next one's products.
   if (!threads) {
-    const double waves = ceil_div(ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, 512), sms / 2);
-    consider({true, 256, 1, 2, waves * (steps * 1290.0 + 4000) + 6000 + 40 * 256});
+    const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, 512), rest = tiles % (sms / 2);
+    const bool halves = rest && 2 * rest <= sms / 2;
+    const double waves = tiles / (sms / 2) + (rest && !halves);
+    consider({true, 256, 1, 2,
+              waves * (steps * 1290.0 + 4000) + (halves ? steps * 712.0 + 4000 : 0) + 6000 + 40 * 256});
   }
   // Joining and storing a tile takes about 25 cycles a row of Q, 45 through
   // the cluster; starting and ending a block 6000, which two blocks on an SM
