@@ -970,43 +970,50 @@ Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy) {
     if (best.bn == 0 || f.cycles < best.cycles) best = f;
   };
   // A stage of `rows` rows of c.p and `cols` of c.q costs its copies or its
-  // products, whichever is longer.  Measured: an SM takes in 46 bytes a cycle
-  // in pairs, 36 for one split block and 44 for two, and 16 through loading
-  // threads (12 in pairs, where the slower of two blocks counts); the products
-  // take 2.5 cycles a row of the kernel's Q.
+  // products (2.1 cycles a row of the kernel's Q), whichever is longer.
+  // Measured, bytes a cycle into an SM: 46 in pairs when all of them are at
+  // work, 53 for half of them, a seventh less with 128 rows of Q; 41 for a
+  // split block alone on its SM, 55 for one with the whole shared memory, 66 for
+  // two; through loading threads 16 (12 in pairs, where the slower of two blocks
+  // counts).
   const bool threads = !p_copy || !q_copy;
   const auto stage = [&](uint32_t rows, uint32_t cols, uint32_t bn, double engine, double loaded) {
     const double copies = rows * 128.0 / (p_copy ? engine : loaded) + cols * 128.0 / (q_copy ? engine : loaded);
     return copies > 2.1 * bn ? copies : 2.1 * bn;
   };
+  // Starting and ending a block takes about 6000 cycles, joining and storing a
+  // tile 25 a row of Q, 30 to 40 through a cluster; of a wide tile all but the last
+  // run under the next one's products, 2800 + 7 a row at the least.
+  constexpr uint32_t pairs = sms / 2;
   for (uint32_t bn = 256; bn >= 128; bn /= 2) {
     const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, bn);
-    const double waves = ceil_div(tiles, sms / 2);
-    consider({true, bn, 1, 1, waves * steps * stage(kLanes, bn / 2, bn, 46, 12) + 6000 + 40 * bn});
+    const double engine = (58 - 12.0 * (tiles < pairs ? tiles : pairs) / pairs) * (bn == 128 ? 0.86 : 1);
+    const double products = steps * stage(kLanes, bn / 2, bn, engine, 12), store = 2800 + 7 * bn;
+    consider({true, bn, 1, 1, ceil_div(tiles, pairs) * (products > store ? products : store) + 6000 + 25 * bn});
   }
   // Two accumulators to a tile: 1290 cycles a stage (630 us against 681 at
   // 8192^3, where the card's power sets the clock), and no tile's epilogue runs
   // under the next one's products.
   if (!threads) {
-    const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, 512), rest = tiles % (sms / 2);
-    const bool halves = rest && 2 * rest <= sms / 2;
-    const double waves = tiles / (sms / 2) + (rest && !halves);
+    const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, 512), rest = tiles % pairs;
+    const bool halves = rest && 2 * rest <= pairs;
+    const double rounds = tiles / pairs + (rest && !halves);
     consider({true, 256, 1, 2,
-              waves * (steps * 1290.0 + 4000) + (halves ? steps * 712.0 + 4000 : 0) + 6000 + 40 * 256});
+              rounds * (steps * 1290.0 + 4000) + (halves ? steps * 712.0 + 4000 : 0) + 6000 + 25 * 256});
   }
-  // Joining and storing a tile takes about 25 cycles a row of Q, 45 through
-  // the cluster; starting and ending a block 6000, which two blocks on an SM
-  // share.
   for (uint32_t bn = c.p_mn ? 64 : 16; bn <= (threads ? 128 : 256); bn *= 2) {
     const uint32_t tiles = ceil_div(c.cols, kLanes) * ceil_div(c.rows, bn);
     const bool two = !threads && bn <= 128;  // blocks to an SM
     for (uint32_t split = 1; split <= 8 && (split == 1 || split <= steps); split *= 2) {
-      // Clusters at work at once, one block to an SM: those of 4 and 8 leave some
-      // SMs of a processing cluster over.
-      const uint32_t at_once = split == 8 ? 14 : split == 4 ? 36 : sms / split;
-      const double join = (split > 1 ? 45 : 25) * bn;
-      const double on_sm = two ? ceil_div(uint64_t(tiles) * split, sms) : ceil_div(tiles, at_once);
-      const double own = ceil_div(steps, split) * stage(bn, kLanes, bn, two && on_sm > 1 ? 44 : 36, 16) + join;
+      // Clusters at work at once: those of 4 and 8 leave some SMs of a processing
+      // cluster over.
+      const uint32_t at_once = two ? (split == 8 ? 36 : split == 4 ? 72 : 2 * sms / split)
+                                   : (split == 8 ? 14 : split == 4 ? 36 : sms / split);
+      const double join = (split == 8 ? 40 : split > 1 ? 30 : 25) * bn;
+      const uint32_t rounds = ceil_div(tiles, at_once);
+      const double on_sm = !two ? rounds : rounds > 1 ? 2 * rounds : ceil_div(uint64_t(tiles) * split, sms);
+      const double engine = two && on_sm > 1 ? 66 : bn > 128 ? 55 : 41;
+      const double own = ceil_div(steps, split) * stage(bn, kLanes, bn, engine, 16) + join;
       consider({false, bn, split, 1, two ? on_sm * own + 6000 : on_sm * (own + 6000)});
     }
     if (bn >= c.rows) break;
