@@ -353,6 +353,45 @@ __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint
   return true;
 }
 
+__device__ __forceinline__ void prefetch_l2_line(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" :: "l"(p));
+}
+
+// Loads of the residual, zero without `on`: predicated, as a load inside a
+// branch is waited for where the branch ends, and volatile, so that they stay
+// ahead of what they are to overlap with.
+__device__ __forceinline__ uint4 load_ahead16(const void* p, bool on) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@q ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"(uint32_t(on)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 load_ahead8(const void* p, bool on) {
+  uint2 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+      "@q ld.global.v2.b32 {%0, %1}, [%2];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y) : "l"(p), "r"(uint32_t(on)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint16_t load_ahead2(const void* p, bool on) {
+  uint16_t v;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b16 %0, 0;\n\t@q ld.global.b16 %0, [%1];\n\t}"
+               : "=&h"(v) : "l"(p), "r"(uint32_t(on)) : "memory");
+  return v;
+}
+
+// The lines of a residual's row, from `col` on to `end`, on their way to L2
+// while the products run: the epilogue reads them in a chain of loops
+// ([1003, 4096] x [2048, 4096]: 29.0 us without, RES_US with).
+__device__ __forceinline__ void prefetch_row(const uint16_t* row, uint32_t col, uint32_t end) {
+  for (; col < end; col += 64) prefetch_l2_line(row + col);
+  if (end > 0) prefetch_l2_line(row + end - 1);
+}
+
 // Rows on 16 bytes (and operands by the copy engine: the threads that load
 // others leave too few registers): a warp's 32 rows by 32 columns go to shared
 // memory as the copy engine's box (64-byte rows, its 64-byte swizzle) and from
@@ -386,7 +425,8 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const float (&
 
 template <int D>
 __device__ __forceinline__ void finish_boxes(const GemmArgs& a, const CUtensorMap* mout, const CUtensorMap* mz,
-                                             float (&v)[32], uint32_t row0, uint32_t col, Boxes& boxes, uint32_t lane) {
+                                             float (&v)[32], const uint4 (&res)[4], uint32_t row0, uint32_t col,
+                                             Boxes& boxes, uint32_t lane) {
   if (a.bias) {
 #pragma unroll
     for (uint32_t h = 0; h < 32; h += 8) {
@@ -398,16 +438,15 @@ __device__ __forceinline__ void finish_boxes(const GemmArgs& a, const CUtensorMa
   }
   if (a.z) store_box<D>(mz, v, row0, col, boxes, lane);
   activate<32>(v, a.act);
-  if (a.residual && row0 + lane < a.P) {
-    Pack<D, 8> o;
-    float r[8];
+  if (a.residual) {
 #pragma unroll
-    for (uint32_t h = 0; h < 32; h += 8) {
-      if (col + h >= a.Q) break;
-      o.load(a.residual + uint64_t(row0 + lane) * a.ldresidual + col + h);
-      o.get(r);
+    for (uint32_t h = 0; h < 4; ++h) {
+      const uint32_t w[4] = {res[h].x, res[h].y, res[h].z, res[h].w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[h + k] += r[k];
+      for (uint32_t k = 0; k < 4; ++k) {
+        v[8 * h + 2 * k] += Elem<D>::widen(uint16_t(w[k]));
+        v[8 * h + 2 * k + 1] += Elem<D>::widen(uint16_t(w[k] >> 16));
+      }
     }
   }
   store_box<D>(mout, v, row0, col, boxes, lane);
@@ -430,11 +469,9 @@ __device__ __forceinline__ void finish_staged(const GemmArgs& a, const float* st
     const uint64_t row = row0 + r;
     const uint32_t n = rows - r;
     uint16_t res[kRows];
-    if (a.residual) {
-      const uint16_t* p = a.residual + row * a.ldresidual + col;
+    const uint16_t* p = a.residual + row * a.ldresidual + col;
 #pragma unroll
-      for (uint32_t k = 0; k < kRows; ++k) res[k] = k < n ? p[k * a.ldresidual] : 0;
-    }
+    for (uint32_t k = 0; k < kRows; ++k) res[k] = load_ahead2(p + k * a.ldresidual, a.residual && k < n);
     float v[kRows];
 #pragma unroll
     for (uint32_t k = 0; k < kRows; ++k) v[k] = staged[(r + k) * 33 + lane] + bias;
@@ -535,37 +572,44 @@ __device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint3
   if (warp == 1) tmem_free<kPair>(s.tmem, a.tmem_columns);
 }
 
-// The same of 4 consecutive columns.
+// Four consecutive columns of a row.  The residual's are asked for first and
+// used last (res: their bits).
+__device__ __forceinline__ uint2 residual4(const GemmArgs& a, uint32_t row, uint32_t col) {
+  const uint16_t* p = a.residual + row * a.ldresidual + col;
+  const uint32_t n = col < a.P ? a.P - col : 0;
+  const bool whole = a.residual && a.quads && n >= 4, single = a.residual && !whole;
+  const uint2 w = load_ahead8(p, whole);
+  uint32_t r[4];
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k) r[k] = load_ahead2(p + k, single && k < n);
+  return make_uint2(w.x | r[0] | r[1] << 16, w.y | r[2] | r[3] << 16);
+}
+
 template <int D>
-__device__ __forceinline__ void finish4(const GemmArgs& a, float (&v)[4], uint32_t row, uint32_t col) {
-  uint16_t* out = a.out + row * a.ldout + col;
+__device__ __forceinline__ void finish4(const GemmArgs& a, float (&v)[4], uint2 res, uint32_t row, uint32_t col) {
   const uint32_t n = col < a.P ? a.P - col : 0;
   const bool whole = a.quads && n >= 4;
+  const auto store = [&](uint16_t* p) {
+    const uint2 w = make_uint2(Elem<D>::round2(v[0], v[1]), Elem<D>::round2(v[2], v[3]));
+    if (whole) {
+      st_global(reinterpret_cast<uint2*>(p), w);
+    } else {
+      const uint32_t half[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)
+        if (k < n) p[k] = uint16_t(half[k]);
+    }
+  };
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k)
     if (a.bias && k < n) v[k] += load_param(a.bias, a.wdtype, col + k);
-  if (a.z) {
-    uint16_t* z = a.z + row * a.ldz + col;
-    if (whole) {
-      st_global(reinterpret_cast<uint2*>(z), make_uint2(Elem<D>::round2(v[0], v[1]), Elem<D>::round2(v[2], v[3])));
-    } else {
-#pragma unroll
-      for (uint32_t k = 0; k < 4; ++k)
-        if (k < n) z[k] = Elem<D>::round(v[k]);
-    }
-  }
+  if (a.z) store(a.z + row * a.ldz + col);
   activate<4>(v, a.act);
-  if (a.residual)
-#pragma unroll
-    for (uint32_t k = 0; k < 4; ++k)
-      if (k < n) v[k] += Elem<D>::widen(a.residual[row * a.ldresidual + col + k]);
-  if (whole) {
-    st_global(reinterpret_cast<uint2*>(out), make_uint2(Elem<D>::round2(v[0], v[1]), Elem<D>::round2(v[2], v[3])));
-  } else {
-#pragma unroll
-    for (uint32_t k = 0; k < 4; ++k)
-      if (k < n) out[k] = Elem<D>::round(v[k]);
+  if (a.residual) {
+    v[0] += Elem<D>::widen(uint16_t(res.x)), v[1] += Elem<D>::widen(uint16_t(res.x >> 16));
+    v[2] += Elem<D>::widen(uint16_t(res.y)), v[3] += Elem<D>::widen(uint16_t(res.y >> 16));
   }
+  store(a.out + row * a.ldout + col);
 }
 
 // Tile order: bands of 8 row tiles, down the band first, so that the blocks
@@ -650,6 +694,10 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     for (uint32_t t = first_piece; t < pieces; t += step, ++n) {
       const Piece w = piece_at<kSubs>(a, t);
       const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
+      if (const uint32_t row = (2 * w.tp + rank) * kLanes + quarter * 32 + lane; a.residual && row < a.P && warp < 6) {
+        const uint32_t end = w.q0 + w.subs * a.bn;
+        prefetch_row(a.residual + row * a.ldresidual, w.q0, end < a.Q ? end : a.Q);
+      }
       if (a.steps > 0) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.abort))) break;
         tmem_fence_after();
@@ -661,6 +709,11 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
         for (uint32_t c = c0; c < c0 + half && col0 + c < a.Q; c += 32) {
           if (row0 >= a.P) break;  // the whole warp
           if (kTma && a.octets) {
+            uint4 res[4];
+            const uint16_t* p = a.residual + uint64_t(row0 + lane) * a.ldresidual + col0 + c;
+#pragma unroll
+            for (uint32_t h = 0; h < 4; ++h)
+              res[h] = load_ahead16(p + 8 * h, a.residual && row0 + lane < a.P && col0 + c + 8 * h < a.Q);
             float v[32];
             if (a.steps > 0) {
               uint32_t lo[16], hi[16];
@@ -674,7 +727,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
 #pragma unroll
               for (int k = 0; k < 32; ++k) v[k] = 0.0f;
             }
-            finish_boxes<D>(a, &mout, &mz, v, row0, col0 + c, boxes, lane);
+            finish_boxes<D>(a, &mout, &mz, v, res, row0, col0 + c, boxes, lane);
           } else {
             __syncwarp();
 #pragma unroll
@@ -732,6 +785,10 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
       mma_commit<false>(addr_of(&s.acc_full[0]));
   } else if (warp >= 2 && warp < 2 + kEpilogueWarps<kTma>) {
     const uint32_t quarter = warp & 3;
+    if (a.residual)
+      for (uint32_t i = rank * 32 * kEpilogueWarps<kTma> + threadIdx.x - 64; i < a.bn && q0 + i < a.Q;
+           i += a.split * 32 * kEpilogueWarps<kTma>)
+        prefetch_row(a.residual + (q0 + i) * a.ldresidual, p0, p0 + kLanes < a.P ? p0 + kLanes : a.P);
     bool ok = true;
     if (first < last) {
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[0]), 0, &s.abort));
@@ -763,6 +820,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
   const uint32_t at = addr_of(part);
   for (uint32_t i = rank * per + threadIdx.x; i < end; i += kGemmThreads<kTma>) {
     const uint32_t j = p0 + (i * 4 & (kLanes - 1)), row = q0 + i / (kLanes / 4);
+    const uint2 res = residual4(a, row, j);
     float4 in[8];
 #pragma unroll
     for (uint32_t r = 0; r < 8; ++r)
@@ -771,7 +829,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
 #pragma unroll
     for (uint32_t r = 0; r < 8; ++r)
       if (r < a.split) v[0] += in[r].x, v[1] += in[r].y, v[2] += in[r].z, v[3] += in[r].w;
-    finish4<D>(a, v, row, j);
+    finish4<D>(a, v, res, row, j);
   }
   finish_block<false>(a, s, warp, lane, rank, ring, last - first);
 }

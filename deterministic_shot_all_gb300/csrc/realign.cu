@@ -17,7 +17,7 @@
 namespace arx {
 namespace {
 
-constexpr uint32_t kWarps = 8, kWords = 8, kChunk = 64 * kWords;  // kWords words to a lane; elements to a warp
+constexpr uint32_t kWarps = 4, kWords = 16, kChunk = 64 * kWords;  // kWords words to a lane; elements to a warp
 
 __global__ void __launch_bounds__(32 * kWarps) realign_kernel(const __grid_constant__ RealignPair pair) {
   dependent_launch_prologue();
