@@ -377,6 +377,12 @@ __device__ __forceinline__ uint2 load_ahead8(const void* p, bool on) {
       : "=&r"(v.x), "=&r"(v.y) : "l"(p), "r"(uint32_t(on)) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t load_ahead4(const void* p, bool on) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.b32 %0, [%1];\n\t}"
+               : "=&r"(v) : "l"(p), "r"(uint32_t(on)) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint16_t load_ahead2(const void* p, bool on) {
   uint16_t v;
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b16 %0, 0;\n\t@q ld.global.b16 %0, [%1];\n\t}"
@@ -423,25 +429,42 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const float (&
   if (lane == 0) tma_store_2d(map, col, row0, box);
 }
 
+// What 32 columns from `col` on need from memory: the bias of column col + lane
+// and this lane's row of the residual.  Asked for when the last 32 columns'
+// were used, so that their way overlaps with the boxes' stores, the
+// accumulator's loads and the activation; asked for in place, bias and residual
+// took 10 us each at [1024, 8192] x [8192, 8192] (79 us without).
+struct Ahead {
+  uint4 res[4];
+  uint32_t bias32;
+  uint16_t bias16;
+};
+__device__ __forceinline__ void ask(const GemmArgs& a, Ahead& h, uint32_t row, uint32_t col, bool on, uint32_t lane) {
+  const bool bias = on && a.bias && col + lane < a.Q, wide = a.wdtype == ARX_F32;
+  h.bias32 = load_ahead4(static_cast<const float*>(a.bias) + col + lane, bias && wide);
+  h.bias16 = load_ahead2(static_cast<const uint16_t*>(a.bias) + col + lane, bias && !wide);
+  const uint16_t* p = a.residual + uint64_t(row) * a.ldresidual + col;
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k)
+    h.res[k] = load_ahead16(p + 8 * k, on && a.residual && row < a.P && col + 8 * k < a.Q);  // Q is a multiple of 8
+}
+
+// `next`: the following 32 columns, if there are any.
 template <int D>
 __device__ __forceinline__ void finish_boxes(const GemmArgs& a, const CUtensorMap* mout, const CUtensorMap* mz,
-                                             float (&v)[32], const uint4 (&res)[4], uint32_t row0, uint32_t col,
-                                             Boxes& boxes, uint32_t lane) {
+                                             float (&v)[32], Ahead& ahead, uint32_t row0, uint32_t col, uint32_t next,
+                                             bool more, Boxes& boxes, uint32_t lane) {
   if (a.bias) {
+    const float b = a.wdtype == ARX_F32 ? __uint_as_float(ahead.bias32) : Elem<D>::widen(ahead.bias16);
 #pragma unroll
-    for (uint32_t h = 0; h < 32; h += 8) {
-      float b[8] = {};
-      if (col + h < a.Q) load_params<8>(a.bias, a.wdtype, col + h, b);  // Q is a multiple of 8
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[h + k] += b[k];
-    }
+    for (int k = 0; k < 32; ++k) v[k] += __shfl_sync(0xFFFFFFFFu, b, k);
   }
   if (a.z) store_box<D>(mz, v, row0, col, boxes, lane);
   activate<32>(v, a.act);
   if (a.residual) {
 #pragma unroll
     for (uint32_t h = 0; h < 4; ++h) {
-      const uint32_t w[4] = {res[h].x, res[h].y, res[h].z, res[h].w};
+      const uint32_t w[4] = {ahead.res[h].x, ahead.res[h].y, ahead.res[h].z, ahead.res[h].w};
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k) {
         v[8 * h + 2 * k] += Elem<D>::widen(uint16_t(w[k]));
@@ -449,6 +472,7 @@ __device__ __forceinline__ void finish_boxes(const GemmArgs& a, const CUtensorMa
       }
     }
   }
+  ask(a, ahead, row0 + lane, next, more, lane);
   store_box<D>(mout, v, row0, col, boxes, lane);
 }
 
@@ -694,52 +718,53 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     for (uint32_t t = first_piece; t < pieces; t += step, ++n) {
       const Piece w = piece_at<kSubs>(a, t);
       const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
-      if (const uint32_t row = (2 * w.tp + rank) * kLanes + quarter * 32 + lane; a.residual && row < a.P && warp < 6) {
+      const uint32_t row0 = (2 * w.tp + rank) * kLanes + quarter * 32;
+      const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
+      // The warp's runs of 32 columns: `half` of each accumulator.
+      const uint32_t runs = row0 < a.P ? w.subs * (half / 32) : 0;
+      const auto column = [&](uint32_t i) {
+        const uint32_t j = i * 32 >= half;
+        return w.q0 + j * a.bn + c0 + i * 32 - j * half;
+      };
+      if (a.residual && row0 + lane < a.P && warp < 6) {
         const uint32_t end = w.q0 + w.subs * a.bn;
-        prefetch_row(a.residual + row * a.ldresidual, w.q0, end < a.Q ? end : a.Q);
+        prefetch_row(a.residual + (row0 + lane) * a.ldresidual, w.q0, end < a.Q ? end : a.Q);
       }
+      Ahead ahead;
+      if (kTma && a.octets) ask(a, ahead, row0 + lane, column(0), runs > 0, lane);
       if (a.steps > 0) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.abort))) break;
         tmem_fence_after();
       }
-      const uint32_t row0 = (2 * w.tp + rank) * kLanes + quarter * 32;
-      for (uint32_t j = 0; j < w.subs; ++j) {
-        const uint32_t col0 = w.q0 + j * a.bn, acc = s.tmem + (b + j) * 256 + (quarter * 32 << 16);
-        const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
-        for (uint32_t c = c0; c < c0 + half && col0 + c < a.Q; c += 32) {
-          if (row0 >= a.P) break;  // the whole warp
-          if (kTma && a.octets) {
-            uint4 res[4];
-            const uint16_t* p = a.residual + uint64_t(row0 + lane) * a.ldresidual + col0 + c;
+      for (uint32_t i = 0; i < runs; ++i) {
+        const uint32_t col = column(i), acc = s.tmem + b * 256 + (quarter * 32 << 16) + (col - w.q0);
+        if (col >= a.Q) break;  // and so are those after it
+        if (kTma && a.octets) {
+          float v[32];
+          if (a.steps > 0) {
+            uint32_t lo[16], hi[16];
+            tmem_load16_start(acc, lo);
+            tmem_load16_start(acc + 16, hi);
+            tmem_load_wait(lo);
+            tmem_load_wait(hi);
 #pragma unroll
-            for (uint32_t h = 0; h < 4; ++h)
-              res[h] = load_ahead16(p + 8 * h, a.residual && row0 + lane < a.P && col0 + c + 8 * h < a.Q);
-            float v[32];
-            if (a.steps > 0) {
-              uint32_t lo[16], hi[16];
-              tmem_load16_start(acc + c, lo);
-              tmem_load16_start(acc + c + 16, hi);
-              tmem_load_wait(lo);
-              tmem_load_wait(hi);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(lo[k]), v[16 + k] = __uint_as_float(hi[k]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = 0.0f;
-            }
-            finish_boxes<D>(a, &mout, &mz, v, res, row0, col0 + c, boxes, lane);
+            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(lo[k]), v[16 + k] = __uint_as_float(hi[k]);
           } else {
-            __syncwarp();
 #pragma unroll
-            for (uint32_t h = 0; h < 32; h += 16) {
-              float v[16] = {};
-              if (a.steps > 0) tmem_load16(acc + c + h, v);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) staged[lane * 33 + h + k] = v[k];
-            }
-            __syncwarp();
-            finish_staged<D, kTma ? 16 : 8>(a, staged, row0, col0 + c + lane, lane);
+            for (int k = 0; k < 32; ++k) v[k] = 0.0f;
           }
+          finish_boxes<D>(a, &mout, &mz, v, ahead, row0, col, column(i + 1), i + 1 < runs, boxes, lane);
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (uint32_t h = 0; h < 32; h += 16) {
+            float v[16] = {};
+            if (a.steps > 0) tmem_load16(acc + h, v);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) staged[lane * 33 + h + k] = v[k];
+          }
+          __syncwarp();
+          finish_staged<D, kTma ? 16 : 8>(a, staged, row0, col + lane, lane);
         }
       }
       tmem_fence_before();
