@@ -10,8 +10,11 @@
 // Roles (warps): one copies, one issues the matrix instructions, eight read
 // the accumulators and run the epilogue; operands pass through a ring of
 // stages guarded by mbarriers.  Operands that the copy engine cannot address
-// (rows off 16 bytes) are loaded by 512 more threads into the same swizzled
-// stages, beside four epilogue warps.
+// (rows off 16 bytes) are first copied to aligned rows (realign.cu) where the
+// caller gave a buffer and that is faster -- nearly always: [4000, 4100] x
+// [2044, 4100] 74 us against 221 -- or loaded by 512 more threads into the same
+// swizzled stages, beside four epilogue warps, 18 bytes a cycle into an SM
+// where the copy engine brings 50.
 //
 // Every wait on a barrier is bounded (tensor_core.cuh); a block whose wait ran
 // out sets the call's status word, waits for what it has in flight, and ends.
@@ -24,13 +27,16 @@
 //         at 128 x 256 would need 96 bytes a cycle from L2, against the 64
 //         it can take; the pair needs 64), two accumulators in tensor memory,
 //         so a tile's epilogue runs under the next tile's products; or over
-//         tiles of 256 x 512 on both accumulators, which needs 48 bytes a cycle;
+//         tiles of 256 x 512 on both accumulators, which needs 48 bytes a cycle.
+//         8192^3 in bf16: 614 to 624 us, 1760 to 1790 TFLOP/s; bound by the clock
+//         that the card's power allows.  [1024, 8192] x [8192, 8192]: 79 us, and
+//         86 with bias, gelu and z, whose last stores nothing hides;
 //  split  for few tiles (decode, small matrices): the output's columns take
 //         the 128 accumulator lanes, its few rows the instruction's N, and a
 //         cluster of up to 8 blocks splits the contraction; the partials
 //         meet in distributed shared memory and are added in block order, the
 //         rank-order sum of a one-shot all-reduce.  Bound by reading the
-//         weights once.
+//         weights once (32 tokens of 8192 -> 8192: 25.6 us, 5.3 TB/s).
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -391,8 +397,8 @@ __device__ __forceinline__ uint16_t load_ahead2(const void* p, bool on) {
 }
 
 // The lines of a residual's row, from `col` on to `end`, on their way to L2
-// while the products run: the epilogue reads them in a chain of loops
-// ([1003, 4096] x [2048, 4096]: 29.0 us without, RES_US with).
+// while the products run, for the epilogues that read it in a chain of loops
+// ([4000, 1024] x [4095, 1024]: 52.4 us without, 49.6 with).
 __device__ __forceinline__ void prefetch_row(const uint16_t* row, uint32_t col, uint32_t end) {
   for (; col < end; col += 64) prefetch_l2_line(row + col);
   if (end > 0) prefetch_l2_line(row + end - 1);
@@ -726,7 +732,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
         const uint32_t j = i * 32 >= half;
         return w.q0 + j * a.bn + c0 + i * 32 - j * half;
       };
-      if (a.residual && row0 + lane < a.P && warp < 6) {
+      if (!(kTma && a.octets) && a.residual && row0 + lane < a.P && warp < 6) {
         const uint32_t end = w.q0 + w.subs * a.bn;
         prefetch_row(a.residual + (row0 + lane) * a.ldresidual, w.q0, end < a.Q ? end : a.Q);
       }
@@ -882,7 +888,8 @@ __global__ void __launch_bounds__(kDotThreads) dot_kernel(const __grid_constant_
   // while the stream's previous kernel, whose output x may be, still runs.
   // The lanes' first batch of the row: asked for whole, rows of 16 KB came
   // twice (one token, 8192 x 8192: 34.6 us against 23.5; none 26.0).
-  if (kV == 8 && share == 0 && lane == 0 && j < a.Q && a.K > 0) prefetch_l2_bulk(a.q + j * a.ldq, a.K < 2048 ? a.K * 2 : 4096);
+  if (kV == 8 && share == 0 && lane == 0 && j < a.Q && a.K > 0)
+    prefetch_l2_bulk(a.q + j * a.ldq, a.K < 2048 ? a.K * 2 : 4096);
   dependent_launch_prologue();
   float acc[kM] = {};
   if (j < a.Q) {
@@ -1031,8 +1038,9 @@ cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap (&m)[4], int sms, c
 
 template <int D, int kWord, bool kBoth>
 cudaError_t launch_split(const GemmArgs& a, const CUtensorMap (&m)[4], cudaStream_t st) {
-  return launch_cluster<gemm_split_kernel<D, kWord, kBoth>>(a.tiles_p * a.tiles_q * a.split, kGemmThreads<kWord == 16>, a.split,
-                                                    1024 + a.stages * a.stage_bytes, st, a, m[0], m[1]);
+  return launch_cluster<gemm_split_kernel<D, kWord, kBoth>>(a.tiles_p * a.tiles_q * a.split,
+                                                            kGemmThreads<kWord == 16>, a.split,
+                                                            1024 + a.stages * a.stage_bytes, st, a, m[0], m[1]);
 }
 
 uint32_t ceil_div(uint64_t a, uint64_t b) { return uint32_t((a + b - 1) / b); }
@@ -1180,7 +1188,8 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
       on.copies = nullptr;
       RealignPair r{};
       const auto add = [&](const void* src, uint64_t ld, uint64_t rows, uint64_t cols, void* dst) {
-        r.m[r.n++] = {static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), rows, ld, copy_pitch(cols), int64_t(cols)};
+        r.m[r.n++] = {static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), rows, ld, copy_pitch(cols),
+                      int64_t(cols)};
       };
       if (k.p) {
         add(c.p, c.ldp, c.p_mn ? c.k : c.rows, c.p_mn ? c.rows : c.k, c.copies);

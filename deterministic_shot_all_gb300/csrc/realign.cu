@@ -5,7 +5,8 @@
 // access of a warp.  The destination's words are the source's, or (a row on an
 // odd element) joined from the halves of two neighbours, the second one from
 // the next lane: loads of single elements would bring 18 bytes a cycle into an
-// SM, a quarter of this.
+// SM.  About 2.3 us and 2.9 TB/s read (16.8 MB: 8.0 us); 16 words to a lane in
+// flight and blocks of four warps: 4 words took 3 us more at 25 MB, 32 words 4.
 #include <cuda_runtime.h>
 
 #include <cstdint>
