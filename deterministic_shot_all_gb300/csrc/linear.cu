@@ -488,6 +488,34 @@ __device__ __forceinline__ void finish_boxes(const GemmArgs& a, const CUtensorMa
 // element, would touch 32 lines with every access.  kRows rows go together:
 // the activation's branches and the residual's latency once for each of them
 // were 230 cycles a row.
+template <int D, uint32_t kRows, bool kFull>  // kFull: n >= kRows
+__device__ __forceinline__ void finish_rows(const GemmArgs& a, const float* staged, uint64_t row, uint32_t n, uint32_t col,
+                                            float bias) {
+  uint16_t res[kRows];
+  const uint16_t* p = a.residual + row * a.ldresidual + col;
+  const bool on = a.residual != nullptr;
+#pragma unroll
+  for (uint32_t k = 0; k < kRows; ++k, p += a.ldresidual) res[k] = load_ahead2(p, on && (kFull || k < n));
+  float v[kRows];
+#pragma unroll
+  for (uint32_t k = 0; k < kRows; ++k) v[k] = staged[k * 33] + bias;
+  if (a.z) {
+    uint16_t* z = a.z + row * a.ldz + col;
+#pragma unroll
+    for (uint32_t k = 0; k < kRows; ++k, z += a.ldz)
+      if (kFull || k < n) *z = Elem<D>::round(v[k]);
+  }
+  activate<kRows>(v, a.act);
+  if (on) {
+#pragma unroll
+    for (uint32_t k = 0; k < kRows; ++k) v[k] += Elem<D>::widen(res[k]);
+  }
+  uint16_t* out = a.out + row * a.ldout + col;
+#pragma unroll
+  for (uint32_t k = 0; k < kRows; ++k, out += a.ldout)
+    if (kFull || k < n) *out = Elem<D>::round(v[k]);
+}
+
 template <int D, uint32_t kRows>
 __device__ __forceinline__ void finish_staged(const GemmArgs& a, const float* staged, uint32_t row0, uint32_t col,
                                               uint32_t lane) {
@@ -496,30 +524,10 @@ __device__ __forceinline__ void finish_staged(const GemmArgs& a, const float* st
   const float bias = a.bias ? load_param(a.bias, a.wdtype, col) : 0.0f;
 #pragma unroll 1
   for (uint32_t r = 0; r < rows; r += kRows) {
-    const uint64_t row = row0 + r;
-    const uint32_t n = rows - r;
-    uint16_t res[kRows];
-    const uint16_t* p = a.residual + row * a.ldresidual + col;
-#pragma unroll
-    for (uint32_t k = 0; k < kRows; ++k) res[k] = load_ahead2(p + k * a.ldresidual, a.residual && k < n);
-    float v[kRows];
-#pragma unroll
-    for (uint32_t k = 0; k < kRows; ++k) v[k] = staged[(r + k) * 33 + lane] + bias;
-    if (a.z) {
-      uint16_t* z = a.z + row * a.ldz + col;
-#pragma unroll
-      for (uint32_t k = 0; k < kRows; ++k)
-        if (k < n) z[k * a.ldz] = Elem<D>::round(v[k]);
-    }
-    activate<kRows>(v, a.act);
-    if (a.residual) {
-#pragma unroll
-      for (uint32_t k = 0; k < kRows; ++k) v[k] += Elem<D>::widen(res[k]);
-    }
-    uint16_t* out = a.out + row * a.ldout + col;
-#pragma unroll
-    for (uint32_t k = 0; k < kRows; ++k)
-      if (k < n) out[k * a.ldout] = Elem<D>::round(v[k]);
+    if (rows - r >= kRows)
+      finish_rows<D, kRows, true>(a, staged + r * 33 + lane, row0 + r, kRows, col, bias);
+    else
+      finish_rows<D, kRows, false>(a, staged + r * 33 + lane, row0 + r, rows - r, col, bias);
   }
 }
 
