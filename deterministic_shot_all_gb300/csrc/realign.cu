@@ -5,8 +5,9 @@
 // access of a warp.  The destination's words are the source's, or (a row on an
 // odd element) joined from the halves of two neighbours, the second one from
 // the next lane: loads of single elements would bring 18 bytes a cycle into an
-// SM.  About 2.3 us and 2.9 TB/s read (16.8 MB: 8.0 us); 16 words to a lane in
-// flight and blocks of four warps: 4 words took 3 us more at 25 MB, 32 words 4.
+// SM.  17.9 MB take 6 us.  16 words to a lane in flight, blocks of four warps:
+// 8 words took 2 us more at 25 MB; blocks of eight warps 7 us less at 134 MB and
+// 0.6 us more at 1 MB.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -20,39 +21,55 @@ namespace {
 
 constexpr uint32_t kWarps = 4, kWords = 16, kChunk = 64 * kWords;  // kWords words to a lane; elements to a warp
 
+// A warp's chunk of a row, from element c0 on.  kInside: every word that it
+// looks at lies inside the row (with checks of each, issue slots bound the
+// kernel: the product of 128 rows with [2047, 4099] took 24.0 us, so 20.0).
+template <bool kInside>
+__device__ __forceinline__ void realign_chunk(const Realign& a, const uint16_t* src, uint16_t* to, int64_t c0, bool odd,
+                                              uint32_t lane) {
+  const int64_t rest = a.cols - c0;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(src - odd) + lane;
+  // Word 32 i of the lane's: elements 2 (lane + 32 i) - odd and the next.
+  // Elements outside the row are not touched.
+  const auto load = [&](uint32_t i) -> uint32_t {
+    if (kInside) return words[32 * i];
+    if (64 * int64_t(i) > rest) return 0;  // the whole warp
+    const int64_t c = 2 * int64_t(lane + 32 * i) - odd;
+    if (c + c0 >= 0 && c + 1 < rest) return words[32 * i];
+    if (c + c0 >= 0 && c < rest) return src[c];
+    if (c + c0 == -1) return uint32_t(src[0]) << 16;
+    return 0;
+  };
+  uint32_t w[kWords + 1];
+#pragma unroll
+  for (uint32_t i = 0; i < kWords; ++i) w[i] = load(i);
+  w[kWords] = odd && lane == 0 ? load(kWords) : 0;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(to) + lane;
+  if (odd) {
+#pragma unroll
+    for (uint32_t i = 0; i < kWords; ++i) {
+      const uint32_t up = __shfl_down_sync(0xFFFFFFFFu, w[i], 1), wrap = __shfl_sync(0xFFFFFFFFu, w[i + 1], 0);
+      w[i] = __funnelshift_r(w[i], lane == 31 ? wrap : up, 16);
+    }
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < kWords; ++i)
+    if (kInside || 2 * int64_t(lane + 32 * i) < rest) dst[32 * i] = w[i];  // a last odd column's neighbour is padding
+}
+
 __global__ void __launch_bounds__(32 * kWarps) realign_kernel(const __grid_constant__ RealignPair pair) {
   dependent_launch_prologue();
   const Realign& a = pair.m[blockIdx.z];
   const uint32_t lane = threadIdx.x & 31;
-  // An element's index in its row; signed, as the word before the first is looked at.
-  for (int64_t chunk = blockIdx.x; chunk * int64_t(kChunk) < a.cols; chunk += gridDim.x)
+  for (int64_t c0 = int64_t(blockIdx.x) * kChunk; c0 < a.cols; c0 += int64_t(gridDim.x) * kChunk)
     for (uint64_t row = blockIdx.y * kWarps + threadIdx.x / 32; row < a.rows; row += uint64_t(gridDim.y) * kWarps) {
-      const uint16_t* src = a.src + row * a.ld;
-      const int64_t cols = a.cols, c0 = chunk * int64_t(kChunk);
-      const bool odd = reinterpret_cast<uintptr_t>(src + c0) & 2;
-      // Word k of the chunk: elements c0 + 2 k - odd and the next.  Elements
-      // outside the row are not touched.
-      const auto load = [&](uint32_t k) -> uint32_t {
-        const int64_t c = c0 + 2 * int64_t(k) - odd;
-        if (c >= 0 && c + 1 < cols) return *reinterpret_cast<const uint32_t*>(src + c);
-        if (c >= 0 && c < cols) return src[c];
-        if (c == -1) return uint32_t(src[0]) << 16;
-        return 0;
-      };
-      uint32_t w[kWords + 1];
-#pragma unroll
-      for (uint32_t i = 0; i < kWords; ++i) w[i] = load(lane + 32 * i);
-      w[kWords] = odd && lane == 0 ? load(32 * kWords) : 0;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(a.dst + row * a.ld_dst + c0);
-#pragma unroll
-      for (uint32_t i = 0; i < kWords; ++i) {
-        if (odd) {
-          const uint32_t up = __shfl_down_sync(0xFFFFFFFFu, w[i], 1), wrap = __shfl_sync(0xFFFFFFFFu, w[i + 1], 0);
-          w[i] = __funnelshift_r(w[i], lane == 31 ? wrap : up, 16);
-        }
-        const int64_t c = c0 + 2 * (lane + 32 * int64_t(i));
-        if (c < cols) dst[lane + 32 * i] = w[i];  // a last odd column's neighbour is padding
-      }
+      const uint16_t* src = a.src + row * a.ld + c0;
+      uint16_t* to = a.dst + row * a.ld_dst + c0;
+      const bool odd = reinterpret_cast<uintptr_t>(src) & 2;
+      if ((c0 > 0 || !odd) && a.cols - c0 >= int64_t(kChunk) + odd)
+        realign_chunk<true>(a, src, to, c0, odd, lane);
+      else
+        realign_chunk<false>(a, src, to, c0, odd, lane);
     }
 }
 
