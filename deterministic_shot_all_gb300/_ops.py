@@ -58,6 +58,7 @@ SIGNATURES = {
         ("linear_bwd", arx_linear_bwd_args))},
     **{f"arx_{op}_workspace_bytes": ([_u64, _u64], ctypes.c_size_t)
        for op in ("layer_norm_bwd", "dropout_add_bwd", "linear_bwd")},
+    "arx_stream_capturing": ([_vp], ctypes.c_int),
     **{f"arx_{op}_copies_bytes": ([ctypes.POINTER(t)], ctypes.c_size_t) for op, t in (
         ("linear", arx_linear_args), ("linear_bwd", arx_linear_bwd_args))},
 }
@@ -81,6 +82,16 @@ def _dtype(t, name, allowed):
     return code
 
 
+def _buffer(n, device, stream):
+    """n bytes of the stream's own memory (what was freed on it is not in use by another), or
+    of the graph's while torch captures the stream: they live as long as the graph."""
+    import torch
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=f"cuda:{device}")
+    with torch.cuda.stream(torch.cuda.ExternalStream(_core()._stream(stream))):
+        return torch.empty(n, dtype=torch.uint8, device=f"cuda:{device}")
+
+
 class _Marshal:
     """Fills an argument struct from tensors, checking each against the others."""
 
@@ -89,6 +100,7 @@ class _Marshal:
         self.refs = []
         self.dtype = first.dtype
         self.device = None  # the current device, looked up once a tensor is on a GPU
+        self.own_copies = 0  # bytes of a copies buffer that the caller does not hold
         if types is not None:
             args.dtype = _dtype(first, name, types)
         self.wdtype = None
@@ -221,12 +233,8 @@ class _Marshal:
             n = query(ctypes.byref(self.a)) if off & 15 else 0
             if n == 0:
                 return
-            import torch
-            if stream is None:
-                t = torch.empty(n, dtype=torch.uint8, device=f"cuda:{self.device}")
-            else:  # the stream's own memory: what was freed on it is not in use by another
-                with torch.cuda.stream(torch.cuda.ExternalStream(_core()._stream(stream))):
-                    t = torch.empty(n, dtype=torch.uint8, device=f"cuda:{self.device}")
+            self.own_copies = n
+            t = _buffer(n, self.device, stream)
         elif not t.is_contiguous():
             raise ValueError("copies: must be contiguous")
         self._on_device(t, "copies")
@@ -237,7 +245,7 @@ class _Marshal:
     def done(self):
         if hasattr(self.a, "wdtype"):
             self.a.wdtype = self.a.dtype if self.wdtype in (None, self.dtype) else ARX_F32
-        return self.a, self.refs
+        return self
 
 
 _ROW_TYPES = (ARX_BF16, ARX_F16, ARX_F32)
@@ -362,13 +370,23 @@ class _Plan:
 
     def __init__(self, *args, stream=None, **kwargs):
         core = _core()
-        self._args, self._refs = type(self)._marshal(*args, stream=stream, **kwargs)
+        m = type(self)._marshal(*args, stream=stream, **kwargs)
+        self._args, self._refs = m.a, m.refs
         self._ref = ctypes.byref(self._args)
         self._stream = core._stream(stream)
         self._fn = getattr(core.lib, self._name)
+        self._own_copies, self._device = m.own_copies, m.device
 
     def __call__(self) -> None:
-        st = self._fn(self._ref, self._stream)
+        ref = self._ref
+        # The plan's own copies end with the plan, a graph's nodes with the graph: a captured
+        # call gets copies of the graph's.
+        if self._own_copies and _core().lib.arx_stream_capturing(self._stream):
+            t = _buffer(self._own_copies, self._device, self._stream)
+            a = type(self._args).from_buffer_copy(self._args)
+            a.copies = t.data_ptr()
+            ref = ctypes.byref(a)
+        st = self._fn(ref, self._stream)
         if st:
             _core()._check(st)
 
@@ -377,9 +395,9 @@ def _function(name, marshal, doc):
     """The call and its plan; ``marshal`` also gets the stream, for buffers that it allocates."""
     def call(*args, stream=None, check=True, **kwargs):
         core = _core()
-        a, refs = marshal(*args, stream=stream, **kwargs)  # refs: held until the call is enqueued
-        st = getattr(core.lib, name)(ctypes.byref(a), core._stream(stream))
-        del refs
+        m = marshal(*args, stream=stream, **kwargs)  # holds the tensors until the call is enqueued
+        st = getattr(core.lib, name)(ctypes.byref(m.a), core._stream(stream))
+        del m
         if check:
             core._check(st)
         return st
@@ -441,8 +459,12 @@ Enqueue out = act(x w^T + bias) + residual on the tensor cores.
 
     bf16 or fp16; x [M, K], w [N, K]; bias of the same type or fp32.  ``z`` receives
     x w^T + bias for the backward pass.  ``out`` may be ``residual``.  ``copies``: a buffer of
-    ``arx_linear_copies_bytes`` bytes for operands whose rows are off 16 bytes; None: one is
-    allocated on the stream where the call is faster with it (a plan keeps it); False: none.
+    ``arx_linear_copies_bytes`` bytes for operands whose rows are off 16 bytes, which calls
+    that run in turn may share; None: one is allocated on the stream where the call is faster
+    with it; False: none.  With None a plan keeps a buffer of its own for eager calls, of the
+    operands' size (25 MB for [1003, 4100] x [2044, 4100] of 16 bits), and a call that torch
+    captures into a graph takes one of the graph's memory, so that neither has to outlive the
+    other.  Whoever captures by other means gives ``copies`` and keeps it as long as the graph.
     """)
 arx_linear_bwd, arx_linear_bwd_plan = _function("arx_linear_bwd", _linear_bwd, """\
 Enqueue dz = dout * act'(z), dx = dz w, dw = dz^T x, dbias = sum over rows of dz.
@@ -467,15 +489,21 @@ def arx_linear_bwd_workspace_bytes(M: int, N: int) -> int:
     return int(_core().lib.arx_linear_bwd_workspace_bytes(M, N))
 
 
+def arx_stream_capturing(stream=None) -> bool:
+    """Is the stream being captured into a graph?"""
+    core = _core()
+    return bool(core.lib.arx_stream_capturing(core._stream(stream)))
+
+
 def arx_linear_copies_bytes(x, w) -> int:
     """Bytes of ``copies`` for ``arx_linear`` of these operands; 0: it is faster without."""
-    a, _ = _linear(x, w, None, copies=False)
+    a = _linear(x, w, None, copies=False).a
     return int(_core().lib.arx_linear_copies_bytes(ctypes.byref(a)))
 
 
 def arx_linear_bwd_copies_bytes(dout, x=None, w=None, dx=None, dw=None, act=ARX_ACT_NONE, workspace=None) -> int:
     """Bytes of ``copies`` for ``arx_linear_bwd`` with these arguments."""
-    a, _ = _linear_bwd(dout, x, w, dx=dx, dw=dw, act=act, workspace=workspace, copies=False)
+    a = _linear_bwd(dout, x, w, dx=dx, dw=dw, act=act, workspace=workspace, copies=False).a
     return int(_core().lib.arx_linear_bwd_copies_bytes(ctypes.byref(a)))
 
 
@@ -486,5 +514,5 @@ __all__ = [
                                      "reduce_layer_norm", "linear", "linear_bwd")
       for suffix in ("", "_plan", "_args")),
     "arx_layer_norm_bwd_workspace_bytes", "arx_dropout_add_bwd_workspace_bytes", "arx_linear_bwd_workspace_bytes",
-    "arx_linear_copies_bytes", "arx_linear_bwd_copies_bytes",
+    "arx_linear_copies_bytes", "arx_linear_bwd_copies_bytes", "arx_stream_capturing",
 ]

@@ -315,6 +315,15 @@ arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stre
   return launched(arx::launch_reduce_layer_norm(*a, v, static_cast<cudaStream_t>(stream)), "arx_reduce_layer_norm");
 }
 
+int arx_stream_capturing(void* stream) {
+  cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &s) != cudaSuccess) {
+    (void)cudaGetLastError();  // the default stream beside a capture that waits for it, or no device
+    return 0;
+  }
+  return s != cudaStreamCaptureStatusNone;
+}
+
 size_t arx_linear_copies_bytes(const arx_linear_args* a) {
   if (!a || a->M > kMaxDim || a->N > kMaxDim || a->K > kMaxDim) return 0;
   return arx::gemm_copies_bytes(forward_product(*a));

@@ -748,6 +748,12 @@ typedef struct arx_linear_args {
   int32_t reserved;
 } arx_linear_args;
 
+/* 1 while `stream` is being captured into a graph, else 0.  Buffers given to a
+ * captured call are the graph's as long as it is replayed: a caller that keeps
+ * one between calls (copies, a workspace) gives a captured call another, which
+ * lives as long as the graph. */
+int arx_stream_capturing(void* stream);
+
 size_t arx_linear_copies_bytes(const arx_linear_args* a);
 arx_status arx_linear(const arx_linear_args* a, void* stream);
 
