@@ -45,10 +45,10 @@ arx_reduce_layer_norm_args = _struct(
     (_f64, "p"), (_f32, "eps"), (_i32, "W"))
 arx_linear_args = _struct(
     "arx_linear_args", (_vp, "x w bias residual out z status copies"), (_u64, "copies_bytes M N K ldx ldw ldresidual ldout ldz"),
-    (_i32, "act dtype wdtype reserved"))
+    (_i32, "act dtype wdtype wait_us"))
 arx_linear_bwd_args = _struct(
     "arx_linear_bwd_args", (_vp, "dout z x w dx dw dbias workspace"), (_u64, "workspace_bytes"), (_vp, "status copies"),
-    (_u64, "copies_bytes M N K lddout ldz ldx ldw lddx lddw"), (_i32, "act dtype wdtype reserved"))
+    (_u64, "copies_bytes M N K lddout ldz ldx ldw lddx lddw"), (_i32, "act dtype wdtype wait_us"))
 
 SIGNATURES = {
     **{f"arx_{op}": ([ctypes.POINTER(t), _vp], ctypes.c_int) for op, t in (
@@ -331,8 +331,9 @@ def _reduce_layer_norm(slots, h, y, bias=None, residual=None, weight=None, norm_
     return m.done()
 
 
-def _linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, status=None, copies=None, stream=None):
-    m = _Marshal(arx_linear_args(act=act), x, "x", _PRODUCT_TYPES)
+def _linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, status=None, copies=None, wait_us=0,
+            stream=None):
+    m = _Marshal(arx_linear_args(act=act, wait_us=wait_us), x, "x", _PRODUCT_TYPES)
     M, K = m.matrix(x, "x")
     N, _ = m.matrix(w, "w", None, K)
     m.matrix(residual, "residual", M, N)
@@ -346,8 +347,8 @@ def _linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, statu
 
 
 def _linear_bwd(dout, x, w, dx=None, dw=None, dbias=None, z=None, act=ARX_ACT_NONE, workspace=None, status=None,
-                copies=None, stream=None):
-    m = _Marshal(arx_linear_bwd_args(act=act), dout, "dout", _PRODUCT_TYPES)
+                copies=None, wait_us=0, stream=None):
+    m = _Marshal(arx_linear_bwd_args(act=act, wait_us=wait_us), dout, "dout", _PRODUCT_TYPES)
     M, N = m.matrix(dout, "dout")
     K = next((t.shape[-1] for t in (x, w) if t is not None), 0)
     m.matrix(z, "z", M, N)
@@ -455,7 +456,7 @@ arx_linear, arx_linear_plan = _function("arx_linear", _linear, """\
 Enqueue out = act(x w^T + bias) + residual on the tensor cores.
 
     ``arx_linear(x, w, out, bias=None, residual=None, z=None, act=ARX_ACT_NONE, status=None, copies=None,
-    stream=None, check=True)``
+    wait_us=0, stream=None, check=True)``
 
     bf16 or fp16; x [M, K], w [N, K]; bias of the same type or fp32.  ``z`` receives
     x w^T + bias for the backward pass.  ``out`` may be ``residual``.  ``copies``: a buffer of
@@ -470,10 +471,10 @@ arx_linear_bwd, arx_linear_bwd_plan = _function("arx_linear_bwd", _linear_bwd, "
 Enqueue dz = dout * act'(z), dx = dz w, dw = dz^T x, dbias = sum over rows of dz.
 
     ``arx_linear_bwd(dout, x, w, dx=None, dw=None, dbias=None, z=None, act=ARX_ACT_NONE, workspace=None,
-    status=None, copies=None, stream=None, check=True)``
+    status=None, copies=None, wait_us=0, stream=None, check=True)``
 
     ``workspace`` of ``arx_linear_bwd_workspace_bytes(M, N)`` bytes, unless there is no
-    activation and no dbias.  ``copies`` as in ``arx_linear``.
+    activation and no dbias.  ``copies``, ``status`` and ``wait_us`` as in ``arx_linear``.
     """)
 
 

@@ -17,7 +17,8 @@
 // where the copy engine brings 50.
 //
 // Every wait on a barrier is bounded (tensor_core.cuh); a block whose wait ran
-// out sets the call's status word, waits for what it has in flight, and ends.
+// out sets the call's status word, waits for what it has in flight (drain_block),
+// and ends.
 //
 // Three forms:
 //  vector one or two rows (decode): dot products on the CUDA cores, see
@@ -78,6 +79,7 @@ struct GemmArgs {
   const uint16_t* residual;
   uint64_t ldout, ldz, ldresidual;
   uint32_t* status;
+  uint64_t wait_ns;    // limit of a wait
   int act, wdtype;
   uint32_t bn, bq;     // rows of Q under one accumulator, and a block's share of them in a stage
   uint32_t stages, stage_bytes;
@@ -91,14 +93,17 @@ struct GemmArgs {
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+  uint32_t fills[1 + kLoaders / 32];  // of the copying thread and of each loading warp, once its role ends
   uint32_t tmem;
   volatile uint32_t abort;
 };
 
-// Position in the ring of stages: slot and the parity its next wait expects.
+// Position in the ring of stages: slot and the parity its next wait expects,
+// and the stages passed.
 struct Ring {
-  uint32_t slot = 0, phase = 0;
+  uint32_t slot = 0, phase = 0, passed = 0;
   __device__ __forceinline__ void next(uint32_t stages) {
+    ++passed;
     if (++slot == stages) slot = 0, phase ^= 1;
   }
 };
@@ -262,6 +267,11 @@ __device__ __forceinline__ void put(const Unit& t, const Place& c, uint8_t* dst)
 
 // ---- the roles, for one tile -------------------------------------------------------
 
+// Bytes that the copy engine brings to a block's stage for `subs` accumulators.
+__device__ __forceinline__ uint32_t copied_bytes(const GemmArgs& a, uint32_t subs) {
+  return (a.p_copy ? kPBytes : 0) + (a.q_copy ? subs * a.bq * 128 : 0);
+}
+
 // One thread: the operands that the copy engine can address.  In a pair each
 // block fills its own half of the stage; both halves count on the first
 // block's barrier.  Returns false after a wait ran out.
@@ -269,9 +279,9 @@ template <bool kPair, uint32_t kSubs>
 __device__ __forceinline__ bool copy_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
                                           uint8_t* stages, Ring& ring, uint32_t p0, uint32_t q0, uint32_t first,
                                           uint32_t last, uint32_t rank) {
-  const uint32_t bytes = (a.p_copy ? kPBytes : 0) + (a.q_copy ? kSubs * a.bq * 128 : 0);
+  const uint32_t bytes = copied_bytes(a, kSubs);
   for (uint32_t i = first; i < last; ++i) {
-    if (!mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort)) return false;
+    if (!mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort, a.wait_ns)) return false;
     uint8_t* dst = stages + ring.slot * a.stage_bytes;
     uint32_t bar = addr_of(&s.full[ring.slot]);
     if (!kPair || rank == 0) mbar_arrive_expect(bar, kPair ? 2 * bytes : bytes);
@@ -316,7 +326,7 @@ __device__ __forceinline__ bool load_tile(const GemmArgs& a, Shared& s, uint8_t*
     for (int b = 0; b < kBuffers; ++b) {
       if (i + b >= last) break;
       if (i + b + kBuffers - 1 < last) fetch_stage(t[(b + kBuffers - 1) % kBuffers], i + b + kBuffers - 1);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort))) return false;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort, a.wait_ns))) return false;
       uint8_t* dst = stages + ring.slot * a.stage_bytes;
 #pragma unroll
       for (int j = 0; j < kUnits; ++j) put<kWord>(t[b][j], c[j], j < 2 && p_first ? dst : dst + kPBytes);
@@ -343,7 +353,7 @@ __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint
   // MN-major tile; in the descriptors' units of 16 bytes.
   const uint32_t adv_p = a.p_mn ? 128 : 2, adv_q = a.q_mn ? 128 : 2;
   for (uint32_t i = first; i < last; ++i) {
-    if (!mbar_wait(addr_of(&s.full[ring.slot]), ring.phase, &s.abort)) return false;
+    if (!mbar_wait(addr_of(&s.full[ring.slot]), ring.phase, &s.abort, a.wait_ns)) return false;
     tmem_fence_after();
     const uint32_t base = stages + ring.slot * a.stage_bytes;
     const uint64_t dp = operand_descriptor(base, kStep * 128), dq = operand_descriptor(base + kPBytes, kStep * 128);
@@ -569,15 +579,71 @@ __device__ __forceinline__ void setup(const GemmArgs& a, const CUtensorMap* mp, 
   tmem_fence_after();
 }
 
-// Every thread, after its role; kCluster: the cluster's blocks read or signal
-// each other's memory, so none leaves before all are done.  When a wait ran
-// out in any of them, the copies and the matrix instructions still in flight
-// are waited for, again with a bound, before the memory is given up.  `ring`,
-// `issued`: the copying thread's next stage and an upper bound of the stages
-// it filled.
-template <bool kPair>
+// A writer's fills, at the end of its role (see drain_block).
+template <bool kTma>
+__device__ __forceinline__ void note_fills(Shared& s, const Ring& ring, bool copies, uint32_t warp, uint32_t lane) {
+  if (copies)
+    s.fills[0] = ring.passed;
+  else if (!kTma && lane == 0)
+    s.fills[1 + warp - kFirstLoader<kTma> / 32] = ring.passed;
+}
+
+// After a wait ran out and every role (of a pair: of both blocks) has ended,
+// nothing new is issued, but copies and matrix instructions may be in flight:
+// they are waited for, with a bound, before memory is given up.  Of a pair, the
+// first block does it, on whose barriers both blocks' copies count.
+//
+// One of a stage's writers -- the copying thread, in a pair the other block's
+// too, the loading warps -- may have filled it where another gave up before, so
+// that the stage's phase would never complete.  The writers' fills say which:
+// what the missing ones would have announced and arrived with is made up for,
+// and the phase completes exactly when the copies that were issued have landed.
+// A writer fills a stage once its fill before, `stages` ago, was consumed: only
+// the last `stages` of the writer that came furthest can be open.
+// bytes_of(f): what the copy engine brings to a block with fill f.
+template <bool kTma, bool kPair, typename Bytes>
+__device__ __forceinline__ void drain_block(const GemmArgs& a, Shared& s, uint32_t warp, uint32_t lane, Bytes bytes_of) {
+  constexpr uint32_t kBlocks = kPair ? 2 : 1, kWriters = kTma ? 1 : 1 + kLoaders / 32;
+  const uint32_t copies = a.p_copy | a.q_copy;
+  volatile uint32_t gave_up = 0;
+  if (threadIdx.x == 0) {
+    const auto fills = [&](uint32_t block, uint32_t writer) {
+      const uint32_t at = addr_of(&s.fills[writer]);
+      return ld_cluster_u32(cluster_peer_address(at, kPair ? block : cluster_ctarank()));
+    };
+    uint32_t most = 0;
+    for (uint32_t b = 0; b < kBlocks; ++b)
+      for (uint32_t w = copies ? 0 : 1; w < kWriters; ++w) most = fills(b, w) > most ? fills(b, w) : most;
+    for (uint32_t f = most > a.stages ? most - a.stages : 0; f < most; ++f) {
+      const uint32_t bar = addr_of(&s.full[f % a.stages]);
+      if (copies) {
+        const bool own = fills(0, 0) > f, peer = kPair && fills(1, 0) > f;
+        const uint32_t bytes = bytes_of(f);
+        if (own) {
+          if (kPair && !peer) mbar_complete_tx(bar, bytes);  // announced for both
+        } else if (peer) {
+          mbar_arrive_expect(bar, bytes);
+        } else {
+          mbar_arrive(bar);
+        }
+      }
+      for (uint32_t b = 0; b < kBlocks; ++b)
+        for (uint32_t w = 1; w < kWriters; ++w)
+          if (fills(b, w) <= f) mbar_arrive(bar);
+      mbar_wait(bar, f / a.stages & 1, &gave_up, kWaitNs);
+    }
+  }
+  if (warp == 1 && lane == 0) {
+    mma_commit_own<kPair>(addr_of(&s.drain));
+    mbar_wait(addr_of(&s.drain), 0, &gave_up, kWaitNs);
+  }
+}
+
+// Every thread, after its role.  A cluster's blocks read or signal each
+// other's memory, so none leaves before all are done.
+template <bool kTma, bool kPair, typename Bytes>
 __device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint32_t warp, uint32_t lane, uint32_t rank,
-                                             Ring ring, uint32_t issued) {
+                                             Bytes bytes_of) {
   tmem_fence_before();
   __syncthreads();
   cluster_arrive_release();
@@ -586,21 +652,10 @@ __device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint3
   uint32_t gave_up = s.abort;
   if (kPair) gave_up |= ld_cluster_u32(cluster_peer_address(addr_of(const_cast<uint32_t*>(&s.abort)), rank ^ 1));
   if (gave_up) {
-    volatile uint32_t own = 0;
-    if ((a.p_copy | a.q_copy) && threadIdx.x == 0 && (!kPair || rank == 0)) {
-      for (uint32_t i = 0; i < issued && i < a.stages; ++i) {
-        if (ring.slot == 0) ring.slot = a.stages, ring.phase ^= 1;
-        --ring.slot;
-        mbar_wait(addr_of(&s.full[ring.slot]), ring.phase, &own);
-      }
-    }
-    if (warp == 1 && lane == 0 && (!kPair || rank == 0)) {
-      mma_commit<kPair>(addr_of(&s.drain));
-      mbar_wait(addr_of(&s.drain), 0, &own);
-    }
+    if (!kPair || rank == 0) drain_block<kTma, kPair>(a, s, warp, lane, bytes_of);
     if (threadIdx.x == 0 && a.status) *a.status = uint32_t(ARX_ETIMEOUT) | (12u << 8);
   }
-  if (kPair) {  // after the peer's abort word was read, and any drain
+  if (kPair) {  // after the peer's words were read, and any drain
     __syncwarp();
     cluster_arrive_release();
     cluster_wait();
@@ -695,13 +750,11 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
   const uint32_t pieces = a.pieces, first_piece = blockIdx.x / 2, step = gridDim.x / 2;
 
   Ring ring;
-  uint32_t issued = 0;
   const bool copies = threadIdx.x == 0 && (a.p_copy | a.q_copy), loads = !kTma && threadIdx.x >= kFirstLoader<kTma>;
   if (copies || loads) {
     for (uint32_t t = first_piece; t < pieces; t += step) {
       const Piece w = piece_at<kSubs>(a, t);
       const uint32_t p0 = (2 * w.tp + rank) * kLanes, q0 = w.q0 + rank * a.bq;
-      issued = a.stages;
       bool ok = true;
       if (copies && kSubs == 2 && w.subs == 2)
         ok = copy_tile<true, kSubs>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
@@ -711,12 +764,13 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
         ok = load_tile<kWord, kBoth, true>(a, s, stages, ring, p0, q0, 0, a.steps, threadIdx.x - kFirstLoader<kTma>);
       if (!ok) break;
     }
+    note_fills<kTma>(s, ring, copies, warp, lane);
   } else if (warp == 1 && lane == 0 && rank == 0 && a.steps > 0) {
     uint32_t n = 0;
     for (uint32_t t = first_piece; t < pieces; t += step, ++n) {
       // One accumulator to a tile: two tiles' alternate.  Two: the tile has both.
       const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
-      if (!mbar_wait(addr_of(&s.acc_empty[b]), (use & 1) ^ 1, &s.abort)) break;
+      if (!mbar_wait(addr_of(&s.acc_empty[b]), (use & 1) ^ 1, &s.abort, a.wait_ns)) break;
       tmem_fence_after();
       const uint32_t subs = piece_at<kSubs>(a, t).subs;
       if (!(kSubs == 2 && subs == 2 ? multiply_tile<true, kSubs>(a, s, addr_of(stages), ring, s.tmem, 0, a.steps)
@@ -747,7 +801,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
       Ahead ahead;
       if (kTma && a.octets) ask(a, ahead, row0 + lane, column(0), runs > 0, lane);
       if (a.steps > 0) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.abort))) break;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.abort, a.wait_ns))) break;
         tmem_fence_after();
       }
       for (uint32_t i = 0; i < runs; ++i) {
@@ -788,7 +842,9 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     if (kTma && lane == 0) bulk_wait_all();
   }
   __syncwarp();
-  finish_block<true>(a, s, warp, lane, rank, ring, issued);
+  finish_block<kTma, true>(a, s, warp, lane, rank, [&](uint32_t f) {
+    return copied_bytes(a, piece_at<kSubs>(a, first_piece + f / a.steps * step).subs);
+  });
 }
 
 // One tile per cluster; block r of the cluster takes the r-th share of the
@@ -816,9 +872,11 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
   const bool copies = threadIdx.x == 0 && (a.p_copy | a.q_copy), loads = !kTma && threadIdx.x >= kFirstLoader<kTma>;
   if (copies) {
     copy_tile<false, 1>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, 0);
+    note_fills<kTma>(s, ring, copies, warp, lane);
   } else if (loads) {
     if constexpr (!kTma)
       load_tile<kWord, kBoth, false>(a, s, stages, ring, p0, q0, first, last, threadIdx.x - kFirstLoader<kTma>);
+    note_fills<kTma>(s, ring, copies, warp, lane);
   } else if (warp == 1 && lane == 0 && first < last) {
     if (multiply_tile<false, 1>(a, s, addr_of(stages), ring, s.tmem, first, last))
       mma_commit<false>(addr_of(&s.acc_full[0]));
@@ -830,7 +888,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
         prefetch_row(a.residual + (q0 + i) * a.ldresidual, p0, p0 + kLanes < a.P ? p0 + kLanes : a.P);
     bool ok = true;
     if (first < last) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[0]), 0, &s.abort));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[0]), 0, &s.abort, a.wait_ns));
       tmem_fence_after();
     }
     if (ok)
@@ -870,7 +928,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
       if (r < a.split) v[0] += in[r].x, v[1] += in[r].y, v[2] += in[r].z, v[3] += in[r].w;
     finish4<D>(a, v, res, row, j);
   }
-  finish_block<false>(a, s, warp, lane, rank, ring, last - first);
+  finish_block<kTma, false>(a, s, warp, lane, rank, [&](uint32_t) { return copied_bytes(a, 1); });
 }
 
 // ---- one or two rows --------------------------------------------------------------------
@@ -1222,6 +1280,7 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   a.residual = static_cast<const uint16_t*>(c.residual);
   a.ldout = c.ldout, a.ldz = c.ldz, a.ldresidual = c.ldresidual;
   a.status = c.status;
+  a.wait_ns = c.wait_ns;
   a.act = c.act, a.wdtype = c.wdtype;
   a.K = uint32_t(c.k);
   a.steps = ceil_div(c.k, kStep);

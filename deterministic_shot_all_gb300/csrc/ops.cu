@@ -13,6 +13,7 @@ namespace {
 
 using arx::report;
 
+constexpr int32_t kMostWaitUs = 2000000;  // of a wait in the product: the default, and the most
 constexpr uint64_t kMaxDim = (uint64_t(1) << 31) - 1;
 
 arx_status ok() { return arx::succeed(); }
@@ -111,6 +112,10 @@ arx_status check_dropout(double p, const uint64_t* rng) {
   return ARX_OK;
 }
 
+arx_status check_wait(int32_t us) {
+  return us >= 0 && us <= kMostWaitUs ? ARX_OK : report(ARX_EINVAL, "wait_us=%d outside 0..%d", us, kMostWaitUs);
+}
+
 arx_status check_eps(float eps) {
   return eps >= 0.0f ? ARX_OK : report(ARX_EINVAL, "eps=%g is negative or NaN", double(eps));
 }
@@ -142,24 +147,28 @@ arx_status check_copies(const void* p, uint64_t have, uint64_t need) {
 
 // The products of a layer, without their outputs: sizes, operands, types.
 arx::GemmCall product(const void* p, uint64_t ldp, bool p_mn, const void* q, uint64_t ldq, bool q_mn, uint64_t rows,
-                      uint64_t cols, uint64_t k, int dtype, int wdtype, uint32_t* status) {
+                      uint64_t cols, uint64_t k, int dtype, int wdtype, uint32_t* status, int32_t wait_us) {
   arx::GemmCall c{};
   c.p = p, c.ldp = (p_mn ? k : rows) <= 1 ? (p_mn ? rows : k) : ldp, c.p_mn = p_mn;
   c.q = q, c.ldq = (q_mn ? k : cols) <= 1 ? (q_mn ? cols : k) : ldq, c.q_mn = q_mn;
   c.rows = rows, c.cols = cols, c.k = k;
   c.act = ARX_ACT_NONE, c.dtype = dtype, c.wdtype = wdtype, c.status = status;
+  c.wait_ns = uint64_t(wait_us ? wait_us : kMostWaitUs) * 1000;
   return c;
 }
 arx::GemmCall forward_product(const arx_linear_args& a) {
-  return product(a.x, a.ldx, false, a.w, a.ldw, false, a.M, a.N, a.K, a.dtype, a.wdtype, a.status);
+  return product(a.x, a.ldx, false, a.w, a.ldw, false, a.M, a.N, a.K, a.dtype, a.wdtype, a.status,
+                 a.wait_us);
 }
 // dx = dz w: w's rows are the contraction.
 arx::GemmCall dx_product(const arx_linear_bwd_args& a, const void* dz, uint64_t lddz) {
-  return product(dz, lddz, false, a.w, a.ldw, true, a.M, a.K, a.N, a.dtype, a.wdtype, a.status);
+  return product(dz, lddz, false, a.w, a.ldw, true, a.M, a.K, a.N, a.dtype, a.wdtype, a.status,
+                 a.wait_us);
 }
 // dw = dz^T x: the rows of both are.
 arx::GemmCall dw_product(const arx_linear_bwd_args& a, const void* dz, uint64_t lddz) {
-  return product(dz, lddz, true, a.x, a.ldx, true, a.N, a.K, a.M, a.dtype, a.wdtype, a.status);
+  return product(dz, lddz, true, a.x, a.ldx, true, a.N, a.K, a.M, a.dtype, a.wdtype, a.status,
+                 a.wait_us);
 }
 
 // Where the products of a backward pass find dz: in the workspace (rows of N
@@ -334,6 +343,7 @@ arx_status arx_linear(const arx_linear_args* a, void* stream) {
   ARX_TRY(check_types(a->dtype, a->wdtype, false));
   ARX_TRY(check_dims(a->M, a->N, a->K));
   if (a->act < ARX_ACT_NONE || a->act > ARX_ACT_SILU) return report(ARX_EINVAL, "unknown activation %d", a->act);
+  ARX_TRY(check_wait(a->wait_us));
   if (a->M == 0 || a->N == 0) return ok();
   arx::GemmCall c = forward_product(*a);
   const size_t copies = a->copies ? arx::gemm_copies_bytes(c) : 0;
@@ -374,6 +384,7 @@ arx_status arx_linear_bwd(const arx_linear_bwd_args* a, void* stream) {
   ARX_TRY(check_types(a->dtype, a->wdtype, false));
   ARX_TRY(check_dims(a->M, a->N, a->K));
   if (a->act < ARX_ACT_NONE || a->act > ARX_ACT_SILU) return report(ARX_EINVAL, "unknown activation %d", a->act);
+  ARX_TRY(check_wait(a->wait_us));
   if (!a->dx && !a->dw && !a->dbias) return ok();
   const bool act = a->act != ARX_ACT_NONE, products = a->dx || a->dw;
   const Mat in[] = {mat("dout", a->dout, a->M, a->N, a->lddout, a->dtype),

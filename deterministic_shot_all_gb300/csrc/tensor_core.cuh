@@ -37,17 +37,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bound of every wait: two seconds of the global timer, or the poll count in
-// case the timer stood still.  A wait that runs out raises the block's abort
-// flag, which ends its other waits too.
+// Bound of every wait: `limit` nanoseconds of the global timer (two seconds
+// unless a call says less), or the poll count in case the timer stood still.
+// A wait that runs out raises the block's abort flag, which ends its other
+// waits too.
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kWaitPolls = 1u << 26;
 
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort, uint64_t limit) {
   const uint64_t t0 = global_timer_ns();
   for (uint32_t i = 1; i < kWaitPolls; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0 && (*abort || global_timer_ns() - t0 > kWaitNs)) break;
+    if ((i & 63u) == 0 && (*abort || global_timer_ns() - t0 > limit)) break;
   }
   *abort = 1;
   return false;
@@ -55,9 +56,14 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volat
 
 // True once the barrier's phase `parity` has completed, false when the block
 // gave up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, uint64_t limit) {
   if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, abort);
+  return mbar_wait_slow(bar, parity, abort, limit);
+}
+
+// Counts `bytes` of a phase as arrived.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
 }
 
 // ---- tiled copies (TMA) -----------------------------------------------------------
@@ -221,6 +227,15 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         :: "r"(bar), "h"(uint16_t(3)) : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+// The same on this block's `bar` alone.
+template <bool kPair>
+__device__ __forceinline__ void mma_commit_own(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+  else
+    mma_commit<false>(bar);
 }
 
 // Instruction descriptor: fp32 accumulators, both operands bf16 or both fp16.

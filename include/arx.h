@@ -720,6 +720,7 @@ arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stre
  *         device error word (ARX_ETIMEOUT in the low byte) if a wait of the
  *         kernel for its own copies or products ran out; the outputs are then
  *         unspecified.  No input causes it.
+ *   wait_us  limit of such a wait in microseconds, up to 2,000,000; 0 is that
  *   copies  arx_linear_copies_bytes(a) bytes on 16 bytes, or NULL.  The copy
  *         engine takes rows whose address and leading dimension are multiples of
  *         16 bytes.  An operand of other rows is loaded by threads, at a lower
@@ -745,7 +746,7 @@ typedef struct arx_linear_args {
   uint64_t copies_bytes;
   uint64_t M, N, K, ldx, ldw, ldresidual, ldout, ldz;
   int32_t act, dtype, wdtype;
-  int32_t reserved;
+  int32_t wait_us;
 } arx_linear_args;
 
 /* 1 while `stream` is being captured into a graph, else 0.  Buffers given to a
@@ -769,7 +770,8 @@ arx_status arx_linear(const arx_linear_args* a, void* stream);
  *           may be NULL when act is ARX_ACT_NONE and dbias is NULL (given all
  *           the same, a dout whose rows are not on 16 bytes is copied to it)
  *   copies  as in the forward, arx_linear_bwd_copies_bytes(a) bytes: of w, then
- *           of x.  Asked for with the workspace already in `a`. */
+ *           of x.  Asked for with the workspace already in `a`.
+ *   status, wait_us  as in the forward */
 typedef struct arx_linear_bwd_args {
   const void* dout;
   const void* z;
@@ -785,7 +787,7 @@ typedef struct arx_linear_bwd_args {
   uint64_t copies_bytes;
   uint64_t M, N, K, lddout, ldz, ldx, ldw, lddx, lddw;
   int32_t act, dtype, wdtype;
-  int32_t reserved;
+  int32_t wait_us;
 } arx_linear_bwd_args;
 
 size_t arx_linear_bwd_workspace_bytes(uint64_t M, uint64_t N);
