@@ -18,7 +18,7 @@
 //
 // Every wait on a barrier is bounded (tensor_core.cuh); a block whose wait ran
 // out sets the call's status word, waits for what it has in flight (drain_block),
-// and ends.
+// leaves NaN in the outputs that it did not finish, and ends.
 //
 // Three forms:
 //  vector one or two rows (decode): dot products on the CUDA cores, see
@@ -639,8 +639,20 @@ __device__ __forceinline__ void drain_block(const GemmArgs& a, Shared& s, uint32
   }
 }
 
+constexpr uint16_t kNan16 = 0x7FFF;  // in bf16 and in fp16
+
+// 32 rows by n columns of the outputs, by a warp.
+__device__ __noinline__ void fill_nan(const GemmArgs& a, uint32_t row0, uint32_t col0, uint32_t n, uint32_t lane) {
+  for (uint32_t row = row0; row < row0 + 32 && row < a.P; ++row)
+    for (uint32_t c = col0 + lane; c < col0 + n && c < a.Q; c += 32) {
+      a.out[row * a.ldout + c] = kNan16;
+      if (a.z) a.z[row * a.ldz + c] = kNan16;
+    }
+}
+
 // Every thread, after its role.  A cluster's blocks read or signal each
-// other's memory, so none leaves before all are done.
+// other's memory, so none leaves before all are done.  (A block of the split
+// form drains before it joins the others.)
 template <bool kTma, bool kPair, typename Bytes>
 __device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint32_t warp, uint32_t lane, uint32_t rank,
                                              Bytes bytes_of) {
@@ -652,7 +664,7 @@ __device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint3
   uint32_t gave_up = s.abort;
   if (kPair) gave_up |= ld_cluster_u32(cluster_peer_address(addr_of(const_cast<uint32_t*>(&s.abort)), rank ^ 1));
   if (gave_up) {
-    if (!kPair || rank == 0) drain_block<kTma, kPair>(a, s, warp, lane, bytes_of);
+    if (kPair && rank == 0) drain_block<kTma, true>(a, s, warp, lane, bytes_of);
     if (threadIdx.x == 0 && a.status) *a.status = uint32_t(ARX_ETIMEOUT) | (12u << 8);
   }
   if (kPair) {  // after the peer's words were read, and any drain
@@ -782,8 +794,8 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     const uint32_t quarter = warp & 3;  // the accumulator lanes this warp may read
     float* staged = reinterpret_cast<float*>(stages + a.stages * a.stage_bytes) + (warp - 2) * 32 * 33;
     Boxes boxes{addr_of(stages + a.stages * a.stage_bytes) + (warp - 2) * 4096, 0};
-    uint32_t n = 0;
-    for (uint32_t t = first_piece; t < pieces; t += step, ++n) {
+    uint32_t n = 0, t = first_piece;
+    for (; t < pieces; t += step, ++n) {
       const Piece w = piece_at<kSubs>(a, t);
       const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
       const uint32_t row0 = (2 * w.tp + rank) * kLanes + quarter * 32;
@@ -838,6 +850,12 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_peer_address(addr_of(&s.acc_empty[b]), 0));
+    }
+    for (; t < pieces; t += step) {  // after a wait ran out
+      const Piece w = piece_at<kSubs>(a, t);
+      const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
+      for (uint32_t j = 0; j < w.subs; ++j)
+        fill_nan(a, (2 * w.tp + rank) * kLanes + quarter * 32, w.q0 + j * a.bn + c0, half, lane);
     }
     if (kTma && lane == 0) bulk_wait_all();
   }
@@ -904,6 +922,13 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
       }
   }
   __syncthreads();
+  const auto bytes_of = [&](uint32_t) { return copied_bytes(a, 1); };
+  if (s.abort) {  // its part of every sum is NaN, once nothing lands on it any more
+    drain_block<kTma, false>(a, s, warp, lane, bytes_of);
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < a.bn * kLanes; i += kGemmThreads<kTma>) part[i] = __int_as_float(0x7FFFFFFF);
+    __syncthreads();
+  }
   cluster_arrive_release();
   cluster_wait();
 
@@ -928,7 +953,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
       if (r < a.split) v[0] += in[r].x, v[1] += in[r].y, v[2] += in[r].z, v[3] += in[r].w;
     finish4<D>(a, v, res, row, j);
   }
-  finish_block<kTma, false>(a, s, warp, lane, rank, [&](uint32_t) { return copied_bytes(a, 1); });
+  finish_block<kTma, false>(a, s, warp, lane, rank, bytes_of);
 }
 
 // ---- one or two rows --------------------------------------------------------------------

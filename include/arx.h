@@ -718,8 +718,9 @@ arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stre
  *         silu (z / (1 + exp(-z)))
  *   status  optional DEVICE uint32, zero before the call: set to a nonzero
  *         device error word (ARX_ETIMEOUT in the low byte) if a wait of the
- *         kernel for its own copies or products ran out; the outputs are then
- *         unspecified.  No input causes it.
+ *         kernel for its own copies or products ran out.  Elements of the
+ *         outputs that were not finished are then NaN, with or without a status
+ *         word.  No input causes it.
  *   wait_us  limit of such a wait in microseconds, up to 2,000,000; 0 is that
  *   copies  arx_linear_copies_bytes(a) bytes on 16 bytes, or NULL.  The copy
  *         engine takes rows whose address and leading dimension are multiples of

@@ -138,3 +138,32 @@ def test_a_wait_that_runs_out_ends_with_a_status(arx, form):
         torch.cuda.synchronize()
         assert int(status) == 0
         assert bool((out == float(K)).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_what_was_not_finished_is_nan(arx, form, act):
+    # Without a status word: no element keeps what was there before.
+    M, N, K, xlead, wlead = FORMS[form]
+    x, w = _ones(M, K, xlead), _ones(N, K, wlead)
+    out, z = (torch.full((M, N), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    residual = torch.zeros_like(out)
+    arx.arx_linear(x, w, out, residual=residual, z=z, act=getattr(arx, "ARX_ACT_" + act.upper()), copies=False, wait_us=1000)
+    torch.cuda.synchronize()
+    for t in (out, z):
+        nan = torch.isnan(t)
+        assert bool(nan.any()) and bool((t[~nan] == float(K)).all())
+
+
+@pytest.mark.gpu
+def test_gradients_that_were_not_finished_are_nan(arx):
+    M, N, K = 1 << 19, 512, 1024
+    x, d = _ones(M, K), _ones(M, N)
+    dw = torch.full((N, K), 3.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    arx.arx_linear_bwd(d, x, None, dw=dw, status=status, wait_us=100)
+    torch.cuda.synchronize()
+    nan = torch.isnan(dw)
+    assert int(status) & 0xFF == arx.ARX_ETIMEOUT
+    assert bool(nan.any()) and bool((dw[~nan] == float(M)).all())
