@@ -37,18 +37,36 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bound of every wait: `limit` nanoseconds of the global timer (two seconds
-// unless a call says less), or the poll count in case the timer stood still.
-// A wait that runs out raises the block's abort flag, which ends its other
-// waits too.
+// The same, suspended for `ns` at most.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+               " selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok) : "r"(bar), "r"(parity), "r"(ns) : "memory");
+  return ok != 0;
+}
+
+// Bound of every wait: `limit` nanoseconds (two seconds unless a call says
+// less) of the global timer, as far as the block was running: what passes
+// between two looks at the timer, 16 polls of 20 us at most, counts as half a
+// millisecond at most, so that a block that is suspended in between (time
+// slices, a debugger) does not run out of time standing still (beside a busy
+// process waits of 2.4 ms ran out of 6 ms of the timer alone, none of 4.5 ms so).
+// Or the poll count, in case the timer stood still.  A wait that runs out raises the
+// block's abort flag, which ends its other waits too.
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kWaitPolls = 1u << 26;
+constexpr uint32_t kWaitPolls = 1u << 26, kPollsToLook = 16, kPollNs = 20000;
+constexpr uint64_t kLookNs = 500000;
 
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort, uint64_t limit) {
-  const uint64_t t0 = global_timer_ns();
+  uint64_t last = global_timer_ns(), waited = 0;
   for (uint32_t i = 1; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0 && (*abort || global_timer_ns() - t0 > limit)) break;
+    if (mbar_try_wait_for(bar, parity, kPollNs)) return true;
+    if (i % kPollsToLook) continue;
+    const uint64_t now = global_timer_ns(), passed = now - last;
+    last = now;
+    waited += passed < kLookNs ? passed : kLookNs;
+    if (*abort || waited > limit) break;
   }
   *abort = 1;
   return false;

@@ -721,7 +721,8 @@ arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stre
  *         kernel for its own copies or products ran out.  Elements of the
  *         outputs that were not finished are then NaN, with or without a status
  *         word.  No input causes it.
- *   wait_us  limit of such a wait in microseconds, up to 2,000,000; 0 is that
+ *   wait_us  limit of such a wait in microseconds of the block's own running time
+ *         (not of the time that it is suspended), up to 2,000,000; 0 is that
  *   copies  arx_linear_copies_bytes(a) bytes on 16 bytes, or NULL.  The copy
  *         engine takes rows whose address and leading dimension are multiples of
  *         16 bytes.  An operand of other rows is loaded by threads, at a lower

@@ -8,6 +8,8 @@ hangs: every wait has its limit, and the operands are ordinary ones.
 
 import ctypes
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -167,3 +169,37 @@ def test_gradients_that_were_not_finished_are_nan(arx):
     nan = torch.isnan(dw)
     assert int(status) & 0xFF == arx.ARX_ETIMEOUT
     assert bool(nan.any()) and bool((dw[~nan] == float(M)).all())
+
+
+NEIGHBOUR = """
+import select, sys, torch
+a = torch.randn(8192, 8192, device="cuda").bfloat16()
+b = torch.empty_like(a)
+torch.mm(a, a, out=b)
+torch.cuda.synchronize()
+print("ready", flush=True)
+while not select.select([sys.stdin], [], [], 0)[0]:  # until the test closes it
+    for _ in range(20):
+        torch.mm(a, a, out=b)
+    torch.cuda.synchronize()
+"""
+
+
+@pytest.mark.gpu
+def test_time_of_another_process_on_the_gpu_does_not_count(arx):
+    # A tile's products take 2.4 ms here; beside a busy process, whose time slices
+    # suspend the kernel, they take about four times that.
+    M, N, K = FORMS["two_accumulators"][:3]
+    x, w = _ones(M, K), _ones(N, K)
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with subprocess.Popen([sys.executable, "-c", NEIGHBOUR], stdin=subprocess.PIPE, stdout=subprocess.PIPE, text=True) as p:
+        try:
+            assert p.stdout.readline() == "ready\n"
+            for _ in range(20):
+                arx.arx_linear(x, w, out, status=status, wait_us=5000)
+                torch.cuda.synchronize()
+        finally:
+            p.stdin.close()
+    assert p.returncode == 0
+    assert int(status) == 0 and bool((out == float(K)).all())
