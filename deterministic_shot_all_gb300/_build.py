@@ -32,7 +32,7 @@ CHECK_LIB = os.path.join(PKG, "libarx_boundscheck.so")
 SOURCES = ["reduce.cu", "step.cu", "abi.cu", "step_noalloc.cu", "external.cu", "ops.cu", "norm.cu",
            "reduce_norm.cu", "dropout.cu", "linear.cu", "realign.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("arx_device.cuh", "arx_internal.h", "arx_rows.cuh", "norm.cuh",
-                                           "activation.cuh", "tensor_core.cuh", "ops_launch.h")] + [
+                                           "activation.cuh", "tensor_core.cuh", "ops_launch.h", "spans.h")] + [
     os.path.join(INCLUDE, "arx.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

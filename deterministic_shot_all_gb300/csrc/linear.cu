@@ -48,13 +48,13 @@
 #include "arx_internal.h"
 #include "arx_rows.cuh"
 #include "ops_launch.h"
+#include "spans.h"
 #include "tensor_core.cuh"
 
 namespace arx {
 namespace {
 
 constexpr uint32_t kLanes = 128;             // rows of P in a tile (accumulator lanes)
-constexpr uint32_t kStep = 64;               // contraction elements in a stage
 constexpr uint32_t kPBytes = kLanes * 128;   // P's part of a stage
 constexpr uint32_t kMaxStages = 12;
 // Shared memory of a block's stages.  One wide block, or two split blocks of
@@ -149,41 +149,17 @@ __device__ __forceinline__ void copy_operand(uint32_t dst, const CUtensorMap* ma
 // shifted by half a word, where it lies between words.  The addresses advance
 // by a constant from stage to stage, so that a unit costs about ten
 // instructions (with its address and bounds worked out anew it cost 70, which
-// took the issue slots: 1.3 us a stage of 32 KB).  The first and the last
-// stage of a contraction, and units that the matrix's edge cuts, take the
-// general path: nothing outside [lo, hi), the matrix's first and last byte,
-// is read.
-
-struct Operand {
-  const uint16_t* p;
-  uint64_t ld;
-  uint32_t nrows, ncols;  // as stored
-  uint32_t mn, row0;      // the tile's first matrix row
-  uintptr_t lo, hi;
-};
-
-__device__ __forceinline__ Operand operand(const uint16_t* p, uint64_t ld, uint32_t mn, uint32_t rows, uint32_t k,
-                                           uint32_t row0) {
-  Operand o{p, ld, mn ? k : rows, mn ? rows : k, mn, row0, 0, 0};
-  o.lo = reinterpret_cast<uintptr_t>(p);
-  o.hi = o.lo + ((o.nrows - 1) * ld + o.ncols) * 2;
-  return o;
-}
+// took the issue slots: 1.3 us a stage of 32 KB; spans.h has the arithmetic).
+// Five words reach two bytes to either side of a unit.  Units of the first and
+// the last stage of a contraction, which may stand at the matrix's ends, and
+// units that its edge cuts (`fast` is false) take the general path, element by
+// element: nothing before the matrix's first byte or past its last is read.
 
 // A unit on its way: four words, or, where its address lies between words,
 // five that are to be shifted by half a word.
 struct Unit {
   uint32_t w[5];
 };
-
-// Row and column of a unit in the matrix as stored, k0 the stage's first
-// contraction element.
-__device__ __forceinline__ uint32_t unit_row(const Operand& o, uint32_t id, uint32_t k0) {
-  return o.mn ? k0 + (id >> 3 & 63u) : o.row0 + (id >> 3);
-}
-__device__ __forceinline__ uint32_t unit_col(const Operand& o, uint32_t id, uint32_t k0) {
-  return (o.mn ? o.row0 + (id >> 9) * 64 : k0) + (id & 7u) * 8;
-}
 
 // General path: element by element.
 __device__ __noinline__ Unit unit_edge(const uint16_t* p, int n) {
@@ -211,43 +187,13 @@ __device__ __forceinline__ void unit_fast(Unit& t, const uint8_t* p, bool shifte
   }
 }
 
-// One of a thread's places in the stages of a tile.
-struct Place {
-  const uint8_t* at;  // the unit's first word in the next stage to fetch
-  uint64_t step;      // from stage to stage
-  uint32_t id;
-  bool on, fast, shifted;
-};
-
-// Threads beyond the operand's units fetch another's once more and store
-// nothing: a load under a condition of its own is waited for where the
-// condition ends, and the stages in flight with it (64 us became 127).
-template <int kWord>
-__device__ __forceinline__ Place place(const Operand& o, uint32_t id, uint32_t units, uint32_t first) {
-  Place c;
-  c.on = id < units;
-  c.id = c.on ? id : id % units;
-  const uint32_t row = unit_row(o, c.id, first * kStep), col = unit_col(o, c.id, first * kStep);
-  // Past the matrix's last row (MN-major: column) a unit feeds results that
-  // are not stored: whole ones read another row instead, cut ones take the
-  // general path.
-  const uint32_t safe = o.mn ? row : (row < o.nrows ? row : 0);
-  c.fast = o.mn ? col + 8 <= o.ncols : true;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(o.p + safe * o.ld + col);
-  c.shifted = kWord == 2 && (a & 2) != 0;
-  c.at = reinterpret_cast<const uint8_t*>(kWord == 2 ? a & ~uintptr_t(3) : a);
-  c.step = o.mn ? kStep * o.ld * 2 : kStep * 2;
-  return c;
-}
-
 template <int kWord>
 __device__ __forceinline__ void fetch(Unit& t, Place& c, const Operand& o, uint32_t stage, bool edge) {
   if (!edge && c.fast) {
     unit_fast<kWord>(t, c.at, c.shifted);
   } else {
     const uint32_t row = unit_row(o, c.id, stage * kStep), col = unit_col(o, c.id, stage * kStep);
-    const int n = row < o.nrows ? int(o.ncols) - int(col) : 0;
-    t = unit_edge(o.p + row * o.ld + col, n);
+    t = unit_edge(o.p + row * o.ld + col, unit_elements(o, row, col));
   }
   c.at += c.step;
 }

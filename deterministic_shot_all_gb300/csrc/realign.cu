@@ -15,11 +15,12 @@
 #include "arx_device.cuh"
 #include "arx_rows.cuh"
 #include "ops_launch.h"
+#include "spans.h"
 
 namespace arx {
 namespace {
 
-constexpr uint32_t kWarps = 4, kWords = 16, kChunk = 64 * kWords;  // kWords words to a lane; elements to a warp
+constexpr uint32_t kWarps = 4, kWords = kRealignWords, kChunk = kRealignChunk;
 
 // A warp's chunk of a row, from element c0 on.  kInside: every word that it
 // looks at lies inside the row (with checks of each, issue slots bound the
@@ -33,12 +34,12 @@ __device__ __forceinline__ void realign_chunk(const Realign& a, const uint16_t* 
   // Elements outside the row are not touched.
   const auto load = [&](uint32_t i) -> uint32_t {
     if (kInside) return words[32 * i];
-    if (64 * int64_t(i) > rest) return 0;  // the whole warp
-    const int64_t c = 2 * int64_t(lane + 32 * i) - odd;
-    if (c + c0 >= 0 && c + 1 < rest) return words[32 * i];
-    if (c + c0 >= 0 && c < rest) return src[c];
-    if (c + c0 == -1) return uint32_t(src[0]) << 16;
-    return 0;
+    switch (realign_load(c0, rest, lane, i, odd)) {
+      case kBoth: return words[32 * i];
+      case kLower: return src[2 * int64_t(lane + 32 * i) - odd];
+      case kUpper: return uint32_t(src[0]) << 16;
+      default: return 0;
+    }
   };
   uint32_t w[kWords + 1];
 #pragma unroll
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(32 * kWarps) realign_kernel(const __grid_const
       const uint16_t* src = a.src + row * a.ld + c0;
       uint16_t* to = a.dst + row * a.ld_dst + c0;
       const bool odd = reinterpret_cast<uintptr_t>(src) & 2;
-      if ((c0 > 0 || !odd) && a.cols - c0 >= int64_t(kChunk) + odd)
+      if (realign_inside(c0, a.cols, odd))
         realign_chunk<true>(a, src, to, c0, odd, lane);
       else
         realign_chunk<false>(a, src, to, c0, odd, lane);
