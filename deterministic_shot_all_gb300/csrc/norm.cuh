@@ -26,14 +26,15 @@ __device__ __forceinline__ uint32_t row_col(int i) {
 // t, t + T, ...; nothing outside [lo, hi) is read.
 template <int T>
 __device__ __forceinline__ void copy_row(uint8_t* dst, uintptr_t at, uint32_t bytes, uintptr_t lo, uintptr_t hi) {
+  const uintptr_t first = first_unit(at);
   const uint32_t units = row_units(at, bytes);
   for (uint32_t u = threadIdx.x % T; u < units; u += T) {
-    const RowUnit w = row_unit(at, u, lo, hi);
-    if (w.at >= lo) {
-      cp_async16(shared_address(dst + 16 * u), reinterpret_cast<const void*>(w.at), uint32_t(w.to - w.at));
+    const uintptr_t src = first + 16 * u;
+    if (src >= lo) {
+      cp_async16(shared_address(dst + 16 * u), reinterpret_cast<const void*>(src), unit_bytes(src, hi));
     } else {  // the matrix begins inside the unit
-      for (uintptr_t i = w.from; i < w.to; i += 2)
-        *reinterpret_cast<uint16_t*>(dst + 16 * u + (i - w.at)) = *reinterpret_cast<const uint16_t*>(i);
+      for (uintptr_t i = lo; i < src + 16 && i < hi; i += 2)
+        *reinterpret_cast<uint16_t*>(dst + 16 * u + (i - src)) = *reinterpret_cast<const uint16_t*>(i);
     }
   }
 }

@@ -34,12 +34,12 @@ __device__ __forceinline__ void realign_chunk(const Realign& a, const uint16_t* 
   // Elements outside the row are not touched.
   const auto load = [&](uint32_t i) -> uint32_t {
     if (kInside) return words[32 * i];
-    switch (realign_load(c0, rest, lane, i, odd)) {
-      case kBoth: return words[32 * i];
-      case kLower: return src[2 * int64_t(lane + 32 * i) - odd];
-      case kUpper: return uint32_t(src[0]) << 16;
-      default: return 0;
-    }
+    if (64 * int64_t(i) > rest) return 0;  // the whole warp
+    const int64_t c = realign_element(lane, i, odd);
+    if (realign_both(c, c0, rest)) return words[32 * i];
+    if (realign_lower(c, c0, rest)) return src[c];
+    if (realign_upper(c, c0)) return uint32_t(src[0]) << 16;
+    return 0;
   };
   uint32_t w[kWords + 1];
 #pragma unroll

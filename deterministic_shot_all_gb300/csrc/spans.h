@@ -16,17 +16,13 @@ namespace arx {
 
 // ---- a row as the aligned 16-byte units that cover it (norm.cuh) ------------------------
 
-// Units of a row of `bytes` bytes at address `row`.
-ARX_HD uint32_t row_units(uintptr_t row, uint32_t bytes) { return uint32_t(((row & 15) + bytes + 15) >> 4); }
+// The first unit of a row of `bytes` bytes at address `row`, and how many cover it.
+ARX_HD uintptr_t first_unit(uintptr_t row) { return row & ~uintptr_t(15); }
+ARX_HD uint32_t row_units(uintptr_t row, uint32_t bytes) { return uint32_t((row + bytes - first_unit(row) + 15) >> 4); }
 
-// Unit u: its address, and its bytes [from, to) inside the matrix [lo, hi).
-struct RowUnit {
-  uintptr_t at, from, to;
-};
-ARX_HD RowUnit row_unit(uintptr_t row, uint32_t u, uintptr_t lo, uintptr_t hi) {
-  const uintptr_t at = (row & ~uintptr_t(15)) + 16 * u;
-  return RowUnit{at, at < lo ? lo : at, at + 16 <= hi ? at + 16 : hi};
-}
+// Bytes of the unit at address `at` before the matrix's end `hi`.  (Those of a
+// unit that begins before the matrix, at < lo, are [lo, at + unit_bytes).)
+ARX_HD uint32_t unit_bytes(uintptr_t at, uintptr_t hi) { return at + 16 <= hi ? 16 : uint32_t(hi - at); }
 
 // ---- units of 8 elements of a product's operand, loaded by threads (linear.cu) --------------
 
@@ -99,15 +95,12 @@ ARX_HD bool realign_inside(int64_t c0, int64_t cols, bool odd) {
   return (c0 > 0 || !odd) && cols - c0 >= int64_t(kRealignChunk) + odd;
 }
 
-// Where it does not: what word 32 i of a lane's, elements c = 2 (lane + 32 i) -
-// odd and c + 1 of the chunk's `rest` elements, takes from the row.
-enum RealignLoad { kNothing, kBoth, kLower, kUpper };
-ARX_HD RealignLoad realign_load(int64_t c0, int64_t rest, uint32_t lane, uint32_t i, bool odd) {
-  if (64 * int64_t(i) > rest) return kNothing;  // the whole warp
-  const int64_t c = 2 * int64_t(lane + 32 * i) - odd;
-  if (c + c0 >= 0 && c + 1 < rest) return kBoth;
-  if (c + c0 >= 0 && c < rest) return kLower;
-  return c + c0 == -1 ? kUpper : kNothing;
-}
+// Where it does not: word 32 i of a lane's holds elements c and c + 1 of the
+// chunk's `rest` elements.  It is read whole, or its lower half, or, before the
+// row's first word, the upper one, or nothing of it.
+ARX_HD int64_t realign_element(uint32_t lane, uint32_t i, bool odd) { return 2 * int64_t(lane + 32 * i) - odd; }
+ARX_HD bool realign_both(int64_t c, int64_t c0, int64_t rest) { return c + c0 >= 0 && c + 1 < rest; }
+ARX_HD bool realign_lower(int64_t c, int64_t c0, int64_t rest) { return c + c0 >= 0 && c < rest; }
+ARX_HD bool realign_upper(int64_t c, int64_t c0) { return c + c0 == -1; }
 
 }  // namespace arx

@@ -39,12 +39,12 @@ static bool rows_as_units() {
               const uint32_t units = row_units(row, cols * size);
               std::vector<int> have(slot, 0);
               for (uint32_t u = 0; u < units; ++u) {
-                const RowUnit w = row_unit(row, u, lo, hi);
-                CHECK(w.at % 16 == 0 && w.from >= w.at && w.to <= w.at + 16 && w.from < w.to, "row %u unit %u", r, u);
-                CHECK(w.from >= lo && w.to <= hi, "row %u unit %u of %u", r, u, cols);
+                const uintptr_t at = first_unit(row) + 16 * u, from = at < lo ? lo : at, to = at + unit_bytes(at, hi);
+                CHECK(at % 16 == 0 && at + 16 > lo && at < hi && from < to && to <= at + 16, "row %u unit %u", r, u);
+                CHECK(to <= hi, "row %u unit %u of %u", r, u, cols);
                 CHECK(16 * u + 16 <= slot, "row %u unit %u", r, u);
-                if (w.from != w.at) CHECK((w.to - w.from) % 2 == 0 && w.from % 2 == 0, "element by element");
-                for (uintptr_t b = w.from; b < w.to; ++b) have[16 * u + (b - w.at)] = 1;
+                if (at < lo) CHECK((to - from) % 2 == 0 && from % 2 == 0, "element by element");
+                for (uintptr_t b = from; b < to; ++b) have[16 * u + (b - at)] = 1;
               }
               for (uint32_t b = 0; b < cols * size; ++b) CHECK(have[(row & 15) + b], "row %u byte %u of %u", r, b, cols);
             }
@@ -106,15 +106,17 @@ static bool realigned_rows() {
           for (uint32_t lane = 0; lane < 32; ++lane) {
             if (i == kRealignWords && !(odd && lane == 0)) continue;
             const int64_t c = c0 + 2 * int64_t(lane + 32 * i) - odd;
-            const RealignLoad l = inside ? kBoth : realign_load(c0, rest, lane, i, odd);
+            const int64_t in = realign_element(lane, i, odd);
             const uint32_t at = 32 * i + lane;
-            if (l == kBoth) {
+            CHECK(in == c - c0, "lane %u word %u", lane, i);
+            if (!inside && 64 * int64_t(i) > rest) continue;
+            if (inside || realign_both(in, c0, rest)) {
               CHECK(c >= 0 && c + 1 < cols, "cols %ld c0 %ld lane %u word %u", long(cols), long(c0), lane, i);
               lo[at] = c, hi[at] = c + 1;
-            } else if (l == kLower) {
+            } else if (realign_lower(in, c0, rest)) {
               CHECK(c >= 0 && c < cols, "cols %ld c0 %ld lane %u word %u", long(cols), long(c0), lane, i);
               lo[at] = c;
-            } else if (l == kUpper) {
+            } else if (realign_upper(in, c0)) {
               CHECK(c == -1, "cols %ld", long(cols));
               hi[at] = 0;
             }

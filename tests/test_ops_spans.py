@@ -27,9 +27,11 @@ def test_reads_stay_inside(tmp_path):
 
 
 @pytest.mark.parametrize("right,wrong", [
-    ("return uint32_t(((row & 15) + bytes + 15) >> 4);", "return uint32_t(((row & 15) + bytes + 31) >> 4);"),  # a unit too many
-    ("at < lo ? lo : at,", "at,"),                                                                          # before the matrix
-    ("at + 16 <= hi ? at + 16 : hi", "at + 16"),                                                           # past its end
+    ("return uint32_t((row + bytes - first_unit(row) + 15) >> 4);",
+     "return uint32_t((row + bytes - first_unit(row) + 31) >> 4);"),                # a unit too many
+    ("at + 16 <= hi ? 16 : uint32_t(hi - at)", "16"),                              # past the matrix's end
+    ("at + 16 <= hi ? 16 : uint32_t(hi - at)", "at + 16 <= hi ? 16 : uint32_t(hi - at) - 1"),
+    ("return row & ~uintptr_t(15);", "return row & ~uintptr_t(31);"),              # before its begin
     ("c.fast = o.mn ? col + 8 <= o.ncols : true;", "c.fast = true;"),
     ("row < o.nrows ? int(o.ncols)", "row <= o.nrows ? int(o.ncols)"),
     ("cols - c0 >= int64_t(kRealignChunk) + odd", "cols - c0 >= int64_t(kRealignChunk)"),
