@@ -373,29 +373,66 @@ cudaError_t fwd_ring(const arx_layer_norm_args& a, cudaStream_t st) {
                    1.0f / float(a.cols));
 }
 
-// The ring once its blocks have two rows each; below, one block to a row, with
-// more threads the fewer columns each has the sooner it ends.
+// Does a forward pass go through the ring?  One block to a row, with more
+// threads the fewer columns each has the sooner it ends, is the other form, and
+// the better one up to four rows to an SM.  Above, the ring gains as it holds
+// the parameters (the more their bytes beside the rows') and by the rows in
+// flight; its few blocks cost where rows are short and many, or read element
+// by element.  Measured, time of the ring by that of the other form, 609 to
+// 16,384 rows (16-bit rows with 32-bit parameters; with 16-bit ones; 32-bit rows):
+//   up to 256 columns   to 2,000 rows .61 to 1.0; 1.0 to 1.2; .64 to 1.0
+//                       from 3,000    1.1 to 1.7; 1.25 to 1.7; 1.1 to 1.6
+//   512  aligned        .74 to 1.0; .88 to 1.1; .75 to 1.2
+//        off 16 bytes   .56 to 1.2; 1.1 to 2.1, from 8,192 rows .6 to .85; .6 to 1.2
+//   1024 aligned        to 2,000 rows .8 to 1.3; .9 to 1.3; 1.1 to 1.4
+//                       from 3,000    .7 to .9; .7 to 1.0; 1.1 to 1.2
+//        off 16 bytes   .9 to 1.3; 1.1 to 1.85; 1.0 to 1.3
+//   2048 aligned        .7 to .95; .75 to 1.1; .9 to 1.2
+//        off 16 bytes   .9 to 1.2; 1.0 to 1.8; .95 to 1.3
+//   4096 aligned        .6 to .95; .65 to 1.0; .85 to 1.05
+//        off 16 bytes   .85 to 1.1; 1.1 to 1.5, from 4,000 rows .9 to 1.0; .85 to 1.1
+//   above               .3 to .6; .3 to .9; .55 to .8
+// In the ring 320 threads to rows of up to 5120 columns, against 512: .55 to .9
+// of the time, 32-bit rows of whole units 1.0 to 1.1 at 5120 columns, .85 at 4200.
+template <int D>
+bool through_ring(const arx_layer_norm_args& a, bool vec) {
+  const uint64_t n = a.cols;
+  if (a.rows <= 4 * kSms) return false;
+  const bool wide = (a.weight || a.bias) && a.wdtype == ARX_F32, more = a.rows > 16 * kSms;
+  if (n <= 256) return wide && !more;
+  if (n <= 512) return vec || wide || a.rows > 48 * kSms;
+  if (n <= 1024) return vec && D != ARX_F32 && more;
+  if (n <= 2048) return vec && D != ARX_F32;
+  if (n <= 4096) return vec || wide || more;
+  return true;
+}
+
 template <int D>
 cudaError_t fwd_any(const arx_layer_norm_args& a, bool vec, cudaStream_t st) {
   const uint64_t n = a.cols;
-  const bool many = a.rows > 4 * kSms;
+  const bool ring = through_ring<D>(a, vec);
+  constexpr bool kHalf = D != ARX_F32;
   if (vec) {
-    if (n <= 256) return many ? fwd_ring<D, 32, 8, 1, 8>(a, st) : fwd<D, 32, 4, 1, 8>(a, st);
-    if (n <= 512) return many ? fwd_ring<D, 32, 8, 2, 8>(a, st) : fwd<D, 32, 4, 2, 8>(a, st);
-    if (n <= 1024) return many ? fwd_ring<D, 64, 4, 2, 8>(a, st) : fwd<D, 128, 1, 1, 8>(a, st);
-    if (n <= 2048) return many ? fwd_ring<D, 128, 2, 2, 8>(a, st) : fwd<D, 256, 1, 1, 8>(a, st);
-    if (n <= 4096) return many ? fwd_ring<D, 256, 1, 2, 8>(a, st) : fwd<D, 512, 1, 1, 8>(a, st);
-    if (n <= 5120 && many) return fwd_ring<D, 320, 1, 2, 8>(a, st);
-    if (n <= 8192) return many ? fwd_ring<D, 512, 1, 2, 8>(a, st) : fwd<D, 1024, 1, 1, 8>(a, st);
+    if (n <= 256) return ring ? fwd_ring<D, 32, 8, 1, 8>(a, st) : fwd<D, 32, 4, 1, 8>(a, st);
+    if (n <= 512) return ring ? fwd_ring<D, 32, 8, 2, 8>(a, st) : fwd<D, 32, 4, 2, 8>(a, st);
+    if constexpr (kHalf) {
+      if (n <= 1024 && ring) return fwd_ring<D, 64, 4, 2, 8>(a, st);
+      if (n <= 2048 && ring) return fwd_ring<D, 128, 2, 2, 8>(a, st);
+    }
+    if (n <= 1024) return fwd<D, 128, 1, 1, 8>(a, st);
+    if (n <= 2048) return fwd<D, 256, 1, 1, 8>(a, st);
+    if (n <= 4096) return ring ? fwd_ring<D, 256, 1, 2, 8>(a, st) : fwd<D, 512, 1, 1, 8>(a, st);
+    if (n <= 5120 && ring) return fwd_ring<D, 320, 1, 2, 8>(a, st);
+    if (n <= 8192) return ring ? fwd_ring<D, 512, 1, 2, 8>(a, st) : fwd<D, 1024, 1, 1, 8>(a, st);
     if (n <= 16384) return fwd<D, 512, 1, 4, 8>(a, st);
   } else {
-    if (n <= 256) return many ? fwd_ring<D, 32, 8, 8, 1>(a, st) : fwd<D, 32, 4, 8, 1>(a, st);
-    if (n <= 512) return many ? fwd_ring<D, 32, 8, 16, 1>(a, st) : fwd<D, 128, 1, 8, 1>(a, st);
-    if (n <= 1024) return many ? fwd_ring<D, 64, 4, 16, 1>(a, st) : fwd<D, 128, 1, 8, 1>(a, st);
-    if (n <= 2048) return many ? fwd_ring<D, 128, 2, 16, 1>(a, st) : fwd<D, 256, 1, 8, 1>(a, st);
-    if (n <= 4096) return many ? fwd_ring<D, 256, 1, 16, 1>(a, st) : fwd<D, 512, 1, 8, 1>(a, st);
-    if (n <= 5120 && many) return fwd_ring<D, 320, 1, 16, 1>(a, st);
-    if (n <= 8192) return many ? fwd_ring<D, 512, 1, 16, 1>(a, st) : fwd<D, 1024, 1, 8, 1>(a, st);
+    if (n <= 256) return ring ? fwd_ring<D, 32, 8, 8, 1>(a, st) : fwd<D, 32, 4, 8, 1>(a, st);
+    if (n <= 512) return ring ? fwd_ring<D, 32, 8, 16, 1>(a, st) : fwd<D, 128, 1, 8, 1>(a, st);
+    if (n <= 1024) return fwd<D, 128, 1, 8, 1>(a, st);
+    if (n <= 2048) return fwd<D, 256, 1, 8, 1>(a, st);
+    if (n <= 4096) return ring ? fwd_ring<D, 256, 1, 16, 1>(a, st) : fwd<D, 512, 1, 8, 1>(a, st);
+    if (n <= 5120 && ring) return fwd_ring<D, 320, 1, 16, 1>(a, st);
+    if (n <= 8192) return ring ? fwd_ring<D, 512, 1, 16, 1>(a, st) : fwd<D, 1024, 1, 8, 1>(a, st);
     if (n <= 16384) return fwd<D, 1024, 1, 16, 1>(a, st);
   }
   return launch_op(norm_fwd_long_kernel<D>, dim3(unsigned(a.rows)), 512, 0, st, a);
@@ -433,6 +470,10 @@ cudaError_t bwd(const arx_layer_norm_bwd_args& a, unsigned* parts, bool* done, c
                                     : bwd_ring<D, T, RPC, NV, V, 2>(a, parts, slot, 2 * row, st);
 }
 
+// 320 threads to rows of 4097 to 5120 columns off 16 bytes, whose columns are
+// read one by one (512 threads take up to 1.1 times as long); aligned ones gain
+// nothing by it ([8192, 5120] with dresidual, 512 threads and 320: bf16 68.0 us,
+// 67.8; fp32 105, 129).
 template <int D>
 cudaError_t bwd_any(const arx_layer_norm_bwd_args& a, bool vec, unsigned* parts, cudaStream_t st) {
   const uint64_t n = a.cols;

@@ -136,18 +136,36 @@ cudaError_t run(const ReduceNormArgs& a, cudaStream_t st) {
 template <int W>
 cudaError_t run_w(const ReduceNormArgs& a, bool vec, cudaStream_t st) {
   const size_t n = a.cols;
-  // Many rows: 32 columns to a thread, so that a row's sums and bookkeeping
-  // cost few instructions (W = 8 [8192, 4096] with dropout: 115 us at 128
-  // threads to a row, 134 at 512; W = 4 [1024, 8192]: 23.8 at 256, 25.9 at 1024).
-  // Few: 8 to a thread, for the least time of a row (W = 8 [32, 4096]: 2.9 us at
-  // 512 threads, 4.2 at 128).
-  const bool many = a.rows > 4 * 152;
+  // 32 columns to a thread, so that a row's sums and bookkeeping cost few
+  // instructions, or 8, for the least time of a row.  Measured, time of 32
+  // columns by that of 8:
+  //  above 4096 columns  1024 threads to a row fill an SM: from 153 rows on .45 to
+  //                      .98 (up to 5120 columns), .6 to 1.1 (8192); up to 152
+  //                      rows .85 to 1.2
+  //  2049 to 4096        W of 1 to 4 .8 to 1.25; above, from 2.5 million elements
+  //                      on .75 to 1.05, below to 1.2
+  //  513 to 2048         W of 1 to 6 .95 to 1.9; 7 and 8 from 2.5 million elements
+  //                      on .9 to 1.05, below to 1.8 (fewer warps)
+  //  257 to 512          up to 1,216 rows .95 to 1.4, above .75 to 1.15
+  // 640 threads to rows of up to 5120 columns, against 1024: aligned, up to 152
+  // rows, .65 to .9; off 16 bytes, whose elements are read one by one, .7 to .85
+  // from 153 rows on, .95 to 1.1 below.
+  const bool work = a.rows * n > uint64_t(4 * 152) * 4096;
   if (vec) {
     if (n <= 256) return run<W, 32, 4, 1, 8>(a, st);
-    if (n <= 1024) return many ? run<W, 32, 4, 4, 8>(a, st) : run<W, 128, 1, 1, 8>(a, st);
-    if (n <= 2048) return many ? run<W, 64, 1, 4, 8>(a, st) : run<W, 256, 1, 1, 8>(a, st);
-    if (n <= 4096) return many ? run<W, 128, 1, 4, 8>(a, st) : run<W, 512, 1, 1, 8>(a, st);
-    if (n <= 8192) return many ? run<W, 256, 1, 4, 8>(a, st) : run<W, 1024, 1, 1, 8>(a, st);
+    if (n <= 512 && a.rows > 8 * 152) return run<W, 32, 4, 4, 8>(a, st);
+    if constexpr (W > 6) {
+      if (n <= 1024 && work) return run<W, 32, 4, 4, 8>(a, st);
+      if (n <= 2048 && work) return run<W, 64, 1, 4, 8>(a, st);
+    }
+    if constexpr (W > 4)
+      if (n > 2048 && n <= 4096 && work) return run<W, 128, 1, 4, 8>(a, st);
+    if (n <= 1024) return run<W, 128, 1, 1, 8>(a, st);
+    if (n <= 2048) return run<W, 256, 1, 1, 8>(a, st);
+    if (n <= 4096) return run<W, 512, 1, 1, 8>(a, st);
+    if (n <= 8192 && a.rows > 152) return run<W, 256, 1, 4, 8>(a, st);
+    if (n <= 5120) return run<W, 640, 1, 1, 8>(a, st);
+    if (n <= 8192) return run<W, 1024, 1, 1, 8>(a, st);
     if (n <= 16384) return run<W, 512, 1, 4, 8>(a, st);
   } else {
     if (n <= 256) return run<W, 32, 4, 8, 1>(a, st);

@@ -21,8 +21,9 @@ from ops_gpu import TYPES, bits, make, rng, strided
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = TYPES
 
-# Rows: six turns and a part of one of 152 SMs' blocks (three of up to 256
-# threads to an SM, two above, one of 512), 8, 8, 4, 2, 1, 1, 1 rows to a block.
+# Rows: where the ring is the form, six turns and a part of one of 152 SMs' blocks
+# (three of up to 256 threads to an SM, two above, one of 512), 8, 8, 4, 2, 1, 1, 1
+# rows to a block.
 RING_ROWS = {256: 22003, 512: 22003, 1024: 11003, 2048: 5503, 4096: 2803, 5120: 1903, 8192: 1003}
 
 
@@ -46,10 +47,16 @@ def test_norm_forward_off_16_bytes(arx, cols, dtype, wdtype, pad, lead):
     norm._forward(arx, _ring_rows(cols), cols, dtype, wdtype, pad, lead)
 
 
-@pytest.mark.parametrize("rows", [608, 609, 610, 1216, 1217])
-@pytest.mark.parametrize("cols", [264, 257])
-def test_norm_forward_around_the_switch_of_forms(arx, rows, cols):
-    norm._forward(arx, rows, cols, BF16, F32)
+@pytest.mark.parametrize("rows", [608, 609, 1216, 2432, 2433])
+@pytest.mark.parametrize("cols", [256, 250, 264, 257, 1024, 3000, 2500])
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, F32), (BF16, BF16), (F32, F32)])
+def test_norm_forward_around_the_switch_of_forms(arx, rows, cols, dtype, wdtype):
+    norm._forward(arx, rows, cols, dtype, wdtype)
+
+
+@pytest.mark.parametrize("rows", [7296, 7297, 14999])
+def test_norm_forward_around_the_switch_off_16_bytes(arx, rows):
+    norm._forward(arx, rows, 300, F16, F16, pad=1)
 
 
 @pytest.mark.parametrize("cols,pad,lead", [(256, 0, 0), (257, 0, 0), (1024, 8, 0), (1001, 0, 1), (2047, 0, 0), (4096, 0, 0),
@@ -136,6 +143,15 @@ def test_reduce_norm_off_16_bytes(arx, cols):
 def test_reduce_norm_every_w(arx, W):
     for cols in (1000, 2000, 4000, 8000):
         reduce_norm._run(arx, W, 613, cols, p=0.1 if W % 2 else 0.0)
+
+
+# Rows and columns to either side of each switch of the launch rules.
+@pytest.mark.parametrize("W", [1, 4, 6, 7, 8])
+@pytest.mark.parametrize("rows,cols", [(1216, 512), (1217, 512), (1217, 264), (2432, 1024), (2433, 1024), (1216, 2048),
+                                       (1217, 2048), (608, 4096), (609, 4096), (152, 5120), (153, 5120), (152, 8192),
+                                       (153, 8192), (40, 4104), (40, 5128)])
+def test_reduce_norm_around_the_switches_of_forms(arx, W, rows, cols):
+    reduce_norm._run(arx, W, rows, cols, p=0.25 if W % 2 else 0.0)
 
 
 @pytest.mark.parametrize("alias", ["slot", "residual", "both"])
