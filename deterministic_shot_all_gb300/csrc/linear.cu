@@ -11,10 +11,10 @@
 // the accumulators and run the epilogue; operands pass through a ring of
 // stages guarded by mbarriers.  Operands that the copy engine cannot address
 // (rows off 16 bytes) are first copied to aligned rows (realign.cu) where the
-// caller gave a buffer and that is faster -- nearly always: [4000, 4100] x
-// [2044, 4100] 74 us against 221 -- or loaded by 512 more threads into the same
-// swizzled stages, beside four epilogue warps, 18 bytes a cycle into an SM
-// where the copy engine brings 50.
+// caller gave a buffer: [4000, 4100] x [2044, 4100] 68 us against 221.  Without
+// a buffer, and in the few calls that are estimated to be faster so, they are
+// loaded by 512 more threads into the same swizzled stages, beside four
+// epilogue warps, 18 bytes a cycle into an SM where the copy engine brings 50.
 //
 // Every wait on a barrier is bounded (tensor_core.cuh); a block whose wait ran
 // out sets the call's status word, waits for what it has in flight (drain_block),
@@ -30,14 +30,14 @@
 //         so a tile's epilogue runs under the next tile's products; or over
 //         tiles of 256 x 512 on both accumulators, which needs 48 bytes a cycle.
 //         8192^3 in bf16: 614 to 624 us, 1760 to 1790 TFLOP/s; bound by the clock
-//         that the card's power allows.  [1024, 8192] x [8192, 8192]: 79 us, and
-//         86 with bias, gelu and z, whose last stores nothing hides;
+//         that the card's power allows.  [1024, 8192] x [8192, 8192]: 79 to 83 us, and
+//         86 to 94 with bias, gelu and z, whose last stores nothing hides;
 //  split  for few tiles (decode, small matrices): the output's columns take
 //         the 128 accumulator lanes, its few rows the instruction's N, and a
 //         cluster of up to 8 blocks splits the contraction; the partials
 //         meet in distributed shared memory and are added in block order, the
 //         rank-order sum of a one-shot all-reduce.  Bound by reading the
-//         weights once (32 tokens of 8192 -> 8192: 25.6 us, 5.3 TB/s).
+//         weights once (32 tokens of 8192 -> 8192: 24.9 us, 5.4 TB/s).
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 

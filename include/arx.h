@@ -725,11 +725,13 @@ arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stre
  *         (not of the time that it is suspended), up to 2,000,000; 0 is that
  *   copies  arx_linear_copies_bytes(a) bytes on 16 bytes, or NULL.  The copy
  *         engine takes rows whose address and leading dimension are multiples of
- *         16 bytes.  An operand of other rows is loaded by threads, at a lower
- *         rate, or first copied here where that is estimated to be faster
- *         (arx_linear_copies_bytes is 0 where it is not).  It looks at sizes,
- *         alignment and types only.  The two ways may differ in the order of
- *         the sums. */
+ *         16 bytes.  An operand of other rows is first copied here, or, without
+ *         this buffer, loaded by threads at a lower rate.
+ *         (arx_linear_copies_bytes is 0 where every operand is on such rows, for
+ *         one or two rows of x with fewer than 2^23 weights, and in the few
+ *         cases where threads are estimated to be faster; it looks at sizes,
+ *         alignment and types only.)  The copies give the bits of aligned operands; the two
+ *         ways may differ in the order of the sums. */
 #define ARX_ACT_NONE 0
 #define ARX_ACT_RELU 1
 #define ARX_ACT_GELU 2
