@@ -79,7 +79,7 @@ struct GemmArgs {
   const uint16_t* residual;
   uint64_t ldout, ldz, ldresidual;
   uint32_t* status;
-  uint64_t wait_ns;    // limit of a wait
+  uint32_t wait_ns;    // limit of a wait
   int act, wdtype;
   uint32_t bn, bq;     // rows of Q under one accumulator, and a block's share of them in a stage
   uint32_t stages, stage_bytes;
@@ -95,15 +95,13 @@ struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   uint32_t fills[1 + kLoaders / 32];  // of the copying thread and of each loading warp, once its role ends
   uint32_t tmem;
-  volatile uint32_t abort;
+  volatile Waits waits;
 };
 
-// Position in the ring of stages: slot and the parity its next wait expects,
-// and the stages passed.
+// Position in the ring of stages: slot and the parity its next wait expects.
 struct Ring {
-  uint32_t slot = 0, phase = 0, passed = 0;
+  uint32_t slot = 0, phase = 0;
   __device__ __forceinline__ void next(uint32_t stages) {
-    ++passed;
     if (++slot == stages) slot = 0, phase ^= 1;
   }
 };
@@ -220,14 +218,15 @@ __device__ __forceinline__ uint32_t copied_bytes(const GemmArgs& a, uint32_t sub
 
 // One thread: the operands that the copy engine can address.  In a pair each
 // block fills its own half of the stage; both halves count on the first
-// block's barrier.  Returns false after a wait ran out.
+// block's barrier.  Returns the stages filled, fewer than last - first after a
+// wait ran out.
 template <bool kPair, uint32_t kSubs>
-__device__ __forceinline__ bool copy_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
+__device__ __forceinline__ uint32_t copy_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq, Shared& s,
                                           uint8_t* stages, Ring& ring, uint32_t p0, uint32_t q0, uint32_t first,
                                           uint32_t last, uint32_t rank) {
   const uint32_t bytes = copied_bytes(a, kSubs);
   for (uint32_t i = first; i < last; ++i) {
-    if (!mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort, a.wait_ns)) return false;
+    if (!mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.waits)) return i - first;
     uint8_t* dst = stages + ring.slot * a.stage_bytes;
     uint32_t bar = addr_of(&s.full[ring.slot]);
     if (!kPair || rank == 0) mbar_arrive_expect(bar, kPair ? 2 * bytes : bytes);
@@ -239,15 +238,15 @@ __device__ __forceinline__ bool copy_tile(const GemmArgs& a, const CUtensorMap* 
         copy_operand<kPair>(addr_of(dst) + kPBytes + j * a.bq * 128, mq, a.q_layout, q0 + j * a.bn, i * kStep, a.bq, bar);
     ring.next(a.stages);
   }
-  return true;
+  return last - first;
 }
 
 // kLoaders threads: the operands whose rows are off 16 bytes -- both, or the
 // one that the copy engine does not bring -- two units of each to a thread (bq
 // <= 128).  The words of the next stages (two; one of the five-word kind) are
-// in flight while a stage is stored.
+// in flight while a stage is stored.  Returns the stages filled, as copy_tile.
 template <int kWord, bool kBoth, bool kPair>
-__device__ __forceinline__ bool load_tile(const GemmArgs& a, Shared& s, uint8_t* stages, Ring& ring, uint32_t p0,
+__device__ __forceinline__ uint32_t load_tile(const GemmArgs& a, Shared& s, uint8_t* stages, Ring& ring, uint32_t p0,
                                           uint32_t q0, uint32_t first, uint32_t last, uint32_t tid) {
   constexpr int kBuffers = kWord == 2 ? 2 : 3, kUnits = kBoth ? 4 : 2;
   const bool p_first = kBoth || !a.p_copy;
@@ -272,7 +271,8 @@ __device__ __forceinline__ bool load_tile(const GemmArgs& a, Shared& s, uint8_t*
     for (int b = 0; b < kBuffers; ++b) {
       if (i + b >= last) break;
       if (i + b + kBuffers - 1 < last) fetch_stage(t[(b + kBuffers - 1) % kBuffers], i + b + kBuffers - 1);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.abort, a.wait_ns))) return false;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.empty[ring.slot]), ring.phase ^ 1, &s.waits)))
+        return i + b - first;
       uint8_t* dst = stages + ring.slot * a.stage_bytes;
 #pragma unroll
       for (int j = 0; j < kUnits; ++j) put<kWord>(t[b][j], c[j], j < 2 && p_first ? dst : dst + kPBytes);
@@ -288,7 +288,7 @@ __device__ __forceinline__ bool load_tile(const GemmArgs& a, Shared& s, uint8_t*
       ring.next(a.stages);
     }
   }
-  return true;
+  return last - first;
 }
 
 // One thread (of a pair's first block) issues the tile's products into `tmem`.
@@ -299,7 +299,7 @@ __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint
   // MN-major tile; in the descriptors' units of 16 bytes.
   const uint32_t adv_p = a.p_mn ? 128 : 2, adv_q = a.q_mn ? 128 : 2;
   for (uint32_t i = first; i < last; ++i) {
-    if (!mbar_wait(addr_of(&s.full[ring.slot]), ring.phase, &s.abort, a.wait_ns)) return false;
+    if (!mbar_wait(addr_of(&s.full[ring.slot]), ring.phase, &s.waits)) return false;
     tmem_fence_after();
     const uint32_t base = stages + ring.slot * a.stage_bytes;
     const uint64_t dp = operand_descriptor(base, kStep * 128), dq = operand_descriptor(base + kPBytes, kStep * 128);
@@ -510,7 +510,7 @@ __device__ __forceinline__ void setup(const GemmArgs& a, const CUtensorMap* mp, 
       mbar_init(addr_of(&s.acc_empty[i]), 2 * kEpilogueWarps<kTma>);  // of a pair
     }
     mbar_init(addr_of(&s.drain), 1);
-    s.abort = 0;
+    s.waits.limit_ns = a.wait_ns, s.waits.abort = 0;
     mbar_init_fence();
     if (a.p_copy) prefetch_tensor_map(mp);
     if (a.q_copy) prefetch_tensor_map(mq);
@@ -525,13 +525,42 @@ __device__ __forceinline__ void setup(const GemmArgs& a, const CUtensorMap* mp, 
   tmem_fence_after();
 }
 
+// Tile order: bands of 8 row tiles, down the band first, so that the blocks
+// at work at one time share operands in L2.
+__device__ __forceinline__ void tile_at(const GemmArgs& a, uint32_t t, uint32_t& tp, uint32_t& tq) {
+  const uint32_t band = 8u * a.tiles_q, b = t / band, in = t - b * band;
+  const uint32_t rows = a.tiles_p - 8u * b < 8u ? a.tiles_p - 8u * b : 8u;
+  tq = in / rows;
+  tp = 8u * b + (in - tq * rows);
+}
+
+// The kernel's work in order.  Two accumulators to a tile (kSubs == 2): where
+// the tiles past the last whole round of the grid would leave half of it or
+// more without one, each of them is two pieces of one accumulator.
+struct Piece {
+  uint32_t tp, q0, subs;
+};
+template <uint32_t kSubs>
+__device__ __forceinline__ Piece piece_at(const GemmArgs& a, uint32_t t) {
+  Piece w{0, 0, kSubs};
+  uint32_t tq, sub = 0;
+  if (kSubs == 2 && t >= a.whole) {
+    sub = (t - a.whole) & 1;
+    w.subs = 1;
+    t = a.whole + (t - a.whole) / 2;
+  }
+  tile_at(a, t, w.tp, tq);
+  w.q0 = (tq * kSubs + sub) * a.bn;
+  return w;
+}
+
 // A writer's fills, at the end of its role (see drain_block).
 template <bool kTma>
-__device__ __forceinline__ void note_fills(Shared& s, const Ring& ring, bool copies, uint32_t warp, uint32_t lane) {
+__device__ __forceinline__ void note_fills(Shared& s, uint32_t fills, bool copies, uint32_t warp, uint32_t lane) {
   if (copies)
-    s.fills[0] = ring.passed;
+    s.fills[0] = fills;
   else if (!kTma && lane == 0)
-    s.fills[1 + warp - kFirstLoader<kTma> / 32] = ring.passed;
+    s.fills[1 + warp - kFirstLoader<kTma> / 32] = fills;
 }
 
 // After a wait ran out and every role (of a pair: of both blocks) has ended,
@@ -546,12 +575,12 @@ __device__ __forceinline__ void note_fills(Shared& s, const Ring& ring, bool cop
 // and the phase completes exactly when the copies that were issued have landed.
 // A writer fills a stage once its fill before, `stages` ago, was consumed: only
 // the last `stages` of the writer that came furthest can be open.
-// bytes_of(f): what the copy engine brings to a block with fill f.
-template <bool kTma, bool kPair, typename Bytes>
-__device__ __forceinline__ void drain_block(const GemmArgs& a, Shared& s, uint32_t warp, uint32_t lane, Bytes bytes_of) {
+// (Not inlined: the loading threads have no registers to spare.)
+template <bool kTma, bool kPair, uint32_t kSubs>
+__device__ __noinline__ void drain_block(const GemmArgs& a, Shared& s) {
   constexpr uint32_t kBlocks = kPair ? 2 : 1, kWriters = kTma ? 1 : 1 + kLoaders / 32;
   const uint32_t copies = a.p_copy | a.q_copy;
-  volatile uint32_t gave_up = 0;
+  volatile Waits own{kWaitNs, 0};
   if (threadIdx.x == 0) {
     const auto fills = [&](uint32_t block, uint32_t writer) {
       const uint32_t at = addr_of(&s.fills[writer]);
@@ -563,9 +592,10 @@ __device__ __forceinline__ void drain_block(const GemmArgs& a, Shared& s, uint32
     for (uint32_t f = most > a.stages ? most - a.stages : 0; f < most; ++f) {
       const uint32_t bar = addr_of(&s.full[f % a.stages]);
       if (copies) {
-        const bool own = fills(0, 0) > f, peer = kPair && fills(1, 0) > f;
-        const uint32_t bytes = bytes_of(f);
-        if (own) {
+        const bool mine = fills(0, 0) > f, peer = kPair && fills(1, 0) > f;
+        const uint32_t piece = blockIdx.x / 2 + f / a.steps * (gridDim.x / 2);  // of a pair
+        const uint32_t bytes = copied_bytes(a, kSubs == 2 ? piece_at<kSubs>(a, piece).subs : 1);
+        if (mine) {
           if (kPair && !peer) mbar_complete_tx(bar, bytes);  // announced for both
         } else if (peer) {
           mbar_arrive_expect(bar, bytes);
@@ -576,12 +606,12 @@ __device__ __forceinline__ void drain_block(const GemmArgs& a, Shared& s, uint32
       for (uint32_t b = 0; b < kBlocks; ++b)
         for (uint32_t w = 1; w < kWriters; ++w)
           if (fills(b, w) <= f) mbar_arrive(bar);
-      mbar_wait(bar, f / a.stages & 1, &gave_up, kWaitNs);
+      mbar_wait(bar, f / a.stages & 1, &own);
     }
   }
-  if (warp == 1 && lane == 0) {
+  if (threadIdx.x == 32) {  // issued them
     mma_commit_own<kPair>(addr_of(&s.drain));
-    mbar_wait(addr_of(&s.drain), 0, &gave_up, kWaitNs);
+    mbar_wait(addr_of(&s.drain), 0, &own);
   }
 }
 
@@ -599,18 +629,17 @@ __device__ __noinline__ void fill_nan(const GemmArgs& a, uint32_t row0, uint32_t
 // Every thread, after its role.  A cluster's blocks read or signal each
 // other's memory, so none leaves before all are done.  (A block of the split
 // form drains before it joins the others.)
-template <bool kTma, bool kPair, typename Bytes>
-__device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint32_t warp, uint32_t lane, uint32_t rank,
-                                             Bytes bytes_of) {
+template <bool kTma, bool kPair, uint32_t kSubs>
+__device__ __forceinline__ void finish_block(const GemmArgs& a, Shared& s, uint32_t warp, uint32_t rank) {
   tmem_fence_before();
   __syncthreads();
   cluster_arrive_release();
   cluster_wait();
   tmem_fence_after();
-  uint32_t gave_up = s.abort;
-  if (kPair) gave_up |= ld_cluster_u32(cluster_peer_address(addr_of(const_cast<uint32_t*>(&s.abort)), rank ^ 1));
+  uint32_t gave_up = s.waits.abort;
+  if (kPair) gave_up |= ld_cluster_u32(cluster_peer_address(addr_of(const_cast<uint32_t*>(&s.waits.abort)), rank ^ 1));
   if (gave_up) {
-    if (kPair && rank == 0) drain_block<kTma, true>(a, s, warp, lane, bytes_of);
+    if (kPair && rank == 0) drain_block<kTma, true, kSubs>(a, s);
     if (threadIdx.x == 0 && a.status) *a.status = uint32_t(ARX_ETIMEOUT) | (12u << 8);
   }
   if (kPair) {  // after the peer's words were read, and any drain
@@ -663,35 +692,6 @@ __device__ __forceinline__ void finish4(const GemmArgs& a, float (&v)[4], uint2 
   store(a.out + row * a.ldout + col);
 }
 
-// Tile order: bands of 8 row tiles, down the band first, so that the blocks
-// at work at one time share operands in L2.
-__device__ __forceinline__ void tile_at(const GemmArgs& a, uint32_t t, uint32_t& tp, uint32_t& tq) {
-  const uint32_t band = 8u * a.tiles_q, b = t / band, in = t - b * band;
-  const uint32_t rows = a.tiles_p - 8u * b < 8u ? a.tiles_p - 8u * b : 8u;
-  tq = in / rows;
-  tp = 8u * b + (in - tq * rows);
-}
-
-// The kernel's work in order.  Two accumulators to a tile (kSubs == 2): where
-// the tiles past the last whole round of the grid would leave half of it or
-// more without one, each of them is two pieces of one accumulator.
-struct Piece {
-  uint32_t tp, q0, subs;
-};
-template <uint32_t kSubs>
-__device__ __forceinline__ Piece piece_at(const GemmArgs& a, uint32_t t) {
-  Piece w{0, 0, kSubs};
-  uint32_t tq, sub = 0;
-  if (kSubs == 2 && t >= a.whole) {
-    sub = (t - a.whole) & 1;
-    w.subs = 1;
-    t = a.whole + (t - a.whole) / 2;
-  }
-  tile_at(a, t, w.tp, tq);
-  w.q0 = (tq * kSubs + sub) * a.bn;
-  return w;
-}
-
 // kSubs: accumulators to a tile.
 template <int D, int kWord, bool kBoth, uint32_t kSubs>
 __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
@@ -710,25 +710,26 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
   Ring ring;
   const bool copies = threadIdx.x == 0 && (a.p_copy | a.q_copy), loads = !kTma && threadIdx.x >= kFirstLoader<kTma>;
   if (copies || loads) {
-    for (uint32_t t = first_piece; t < pieces; t += step) {
+    uint32_t t = first_piece, filled = 0;
+    for (; t < pieces; t += step) {
       const Piece w = piece_at<kSubs>(a, t);
       const uint32_t p0 = (2 * w.tp + rank) * kLanes, q0 = w.q0 + rank * a.bq;
-      bool ok = true;
+      filled = 0;
       if (copies && kSubs == 2 && w.subs == 2)
-        ok = copy_tile<true, kSubs>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
+        filled = copy_tile<true, kSubs>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
       else if (copies)
-        ok = copy_tile<true, 1>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
+        filled = copy_tile<true, 1>(a, &mp, &mq, s, stages, ring, p0, q0, 0, a.steps, rank);
       else if constexpr (!kTma)
-        ok = load_tile<kWord, kBoth, true>(a, s, stages, ring, p0, q0, 0, a.steps, threadIdx.x - kFirstLoader<kTma>);
-      if (!ok) break;
+        filled = load_tile<kWord, kBoth, true>(a, s, stages, ring, p0, q0, 0, a.steps, threadIdx.x - kFirstLoader<kTma>);
+      if (filled < a.steps) break;
     }
-    note_fills<kTma>(s, ring, copies, warp, lane);
+    note_fills<kTma>(s, (t - first_piece) / step * a.steps + (t < pieces ? filled : 0), copies, warp, lane);
   } else if (warp == 1 && lane == 0 && rank == 0 && a.steps > 0) {
     uint32_t n = 0;
     for (uint32_t t = first_piece; t < pieces; t += step, ++n) {
       // One accumulator to a tile: two tiles' alternate.  Two: the tile has both.
       const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
-      if (!mbar_wait(addr_of(&s.acc_empty[b]), (use & 1) ^ 1, &s.abort, a.wait_ns)) break;
+      if (!mbar_wait(addr_of(&s.acc_empty[b]), (use & 1) ^ 1, &s.waits)) break;
       tmem_fence_after();
       const uint32_t subs = piece_at<kSubs>(a, t).subs;
       if (!(kSubs == 2 && subs == 2 ? multiply_tile<true, kSubs>(a, s, addr_of(stages), ring, s.tmem, 0, a.steps)
@@ -759,7 +760,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
       Ahead ahead;
       if (kTma && a.octets) ask(a, ahead, row0 + lane, column(0), runs > 0, lane);
       if (a.steps > 0) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.abort, a.wait_ns))) break;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[b]), use & 1, &s.waits))) break;
         tmem_fence_after();
       }
       for (uint32_t i = 0; i < runs; ++i) {
@@ -806,9 +807,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     if (kTma && lane == 0) bulk_wait_all();
   }
   __syncwarp();
-  finish_block<kTma, true>(a, s, warp, lane, rank, [&](uint32_t f) {
-    return copied_bytes(a, piece_at<kSubs>(a, first_piece + f / a.steps * step).subs);
-  });
+  finish_block<kTma, true, kSubs>(a, s, warp, rank);
 }
 
 // One tile per cluster; block r of the cluster takes the r-th share of the
@@ -835,12 +834,12 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
   Ring ring;
   const bool copies = threadIdx.x == 0 && (a.p_copy | a.q_copy), loads = !kTma && threadIdx.x >= kFirstLoader<kTma>;
   if (copies) {
-    copy_tile<false, 1>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, 0);
-    note_fills<kTma>(s, ring, copies, warp, lane);
+    note_fills<kTma>(s, copy_tile<false, 1>(a, &mp, &mq, s, stages, ring, p0, q0, first, last, 0), true, warp, lane);
   } else if (loads) {
-    if constexpr (!kTma)
-      load_tile<kWord, kBoth, false>(a, s, stages, ring, p0, q0, first, last, threadIdx.x - kFirstLoader<kTma>);
-    note_fills<kTma>(s, ring, copies, warp, lane);
+    if constexpr (!kTma) {
+      const uint32_t tid = threadIdx.x - kFirstLoader<kTma>;
+      note_fills<kTma>(s, load_tile<kWord, kBoth, false>(a, s, stages, ring, p0, q0, first, last, tid), false, warp, lane);
+    }
   } else if (warp == 1 && lane == 0 && first < last) {
     if (multiply_tile<false, 1>(a, s, addr_of(stages), ring, s.tmem, first, last))
       mma_commit<false>(addr_of(&s.acc_full[0]));
@@ -852,7 +851,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
         prefetch_row(a.residual + (q0 + i) * a.ldresidual, p0, p0 + kLanes < a.P ? p0 + kLanes : a.P);
     bool ok = true;
     if (first < last) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[0]), 0, &s.abort, a.wait_ns));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(addr_of(&s.acc_full[0]), 0, &s.waits));
       tmem_fence_after();
     }
     if (ok)
@@ -868,9 +867,8 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
       }
   }
   __syncthreads();
-  const auto bytes_of = [&](uint32_t) { return copied_bytes(a, 1); };
-  if (s.abort) {  // its part of every sum is NaN, once nothing lands on it any more
-    drain_block<kTma, false>(a, s, warp, lane, bytes_of);
+  if (s.waits.abort) {  // its part of every sum is NaN, once nothing lands on it any more
+    drain_block<kTma, false, 1>(a, s);
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < a.bn * kLanes; i += kGemmThreads<kTma>) part[i] = __int_as_float(0x7FFFFFFF);
     __syncthreads();
@@ -899,7 +897,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
       if (r < a.split) v[0] += in[r].x, v[1] += in[r].y, v[2] += in[r].z, v[3] += in[r].w;
     finish4<D>(a, v, res, row, j);
   }
-  finish_block<kTma, false>(a, s, warp, lane, rank, bytes_of);
+  finish_block<kTma, false, 1>(a, s, warp, rank);
 }
 
 // ---- one or two rows --------------------------------------------------------------------

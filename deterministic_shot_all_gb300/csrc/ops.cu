@@ -153,7 +153,7 @@ arx::GemmCall product(const void* p, uint64_t ldp, bool p_mn, const void* q, uin
   c.q = q, c.ldq = (q_mn ? k : cols) <= 1 ? (q_mn ? cols : k) : ldq, c.q_mn = q_mn;
   c.rows = rows, c.cols = cols, c.k = k;
   c.act = ARX_ACT_NONE, c.dtype = dtype, c.wdtype = wdtype, c.status = status;
-  c.wait_ns = uint64_t(wait_us ? wait_us : kMostWaitUs) * 1000;
+  c.wait_ns = uint32_t(wait_us ? wait_us : kMostWaitUs) * 1000u;
   return c;
 }
 arx::GemmCall forward_product(const arx_linear_args& a) {

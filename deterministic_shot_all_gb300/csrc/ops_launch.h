@@ -87,7 +87,7 @@ struct GemmCall {
   uint64_t ldout, ldz, ldresidual;
   int act, dtype, wdtype;
   uint32_t* status;
-  uint64_t wait_ns;       // limit of a kernel's wait for its own copies and products
+  uint32_t wait_ns;       // limit of a kernel's wait for its own copies and products
   void* copies;           // gemm_copies_bytes(c) bytes, or null
 };
 cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st);

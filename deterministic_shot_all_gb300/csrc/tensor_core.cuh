@@ -37,46 +37,46 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same, suspended for `ns` at most.
-__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-               " selp.u32 %0, 1, 0, p;\n}"
-               : "=r"(ok) : "r"(bar), "r"(parity), "r"(ns) : "memory");
-  return ok != 0;
-}
-
-// Bound of every wait: `limit` nanoseconds (two seconds unless a call says
-// less) of the global timer, as far as the block was running: what passes
-// between two looks at the timer, 16 polls of 20 us at most, counts as half a
+// Bound of every wait: `limit_ns` (two seconds unless a call says less) of the
+// global timer, as far as the block was running: what passes between two looks
+// at the timer, 64 polls that suspend the thread for 4 us each, counts as half a
 // millisecond at most, so that a block that is suspended in between (time
 // slices, a debugger) does not run out of time standing still (beside a busy
-// process waits of 2.4 ms ran out of 6 ms of the timer alone, none of 4.5 ms so).
-// Or the poll count, in case the timer stood still.  A wait that runs out raises the
-// block's abort flag, which ends its other waits too.
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kWaitPolls = 1u << 26, kPollsToLook = 16, kPollNs = 20000;
-constexpr uint64_t kLookNs = 500000;
+// process waits of 2.4 ms ran out of 6 ms of the timer alone, none of 4.5 ms so),
+// and as a microsecond at least, in case the timer stood still.  A wait that
+// runs out raises the block's abort flag, which ends its other waits too.
+// (32 bits, and no count of the polls: the threads that load operands have no
+// registers to spare around the call.)
+constexpr uint32_t kWaitNs = 2000000000u, kPollsToLook = 64, kLeastNs = 1000, kMostNs = 500000;
 
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort, uint64_t limit) {
-  uint64_t last = global_timer_ns(), waited = 0;
-  for (uint32_t i = 1; i < kWaitPolls; ++i) {
-    if (mbar_try_wait_for(bar, parity, kPollNs)) return true;
-    if (i % kPollsToLook) continue;
-    const uint64_t now = global_timer_ns(), passed = now - last;
+struct Waits {
+  uint32_t limit_ns, abort;
+};
+
+__device__ __forceinline__ uint32_t global_timer_low_ns() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile Waits* w) {
+  uint32_t last = global_timer_low_ns(), waited = 0;
+  do {
+    for (uint32_t i = 0; i < kPollsToLook; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t now = global_timer_low_ns(), passed = now - last;
     last = now;
-    waited += passed < kLookNs ? passed : kLookNs;
-    if (*abort || waited > limit) break;
-  }
-  *abort = 1;
+    waited += passed < kLeastNs ? kLeastNs : passed < kMostNs ? passed : kMostNs;
+  } while (!w->abort && waited <= w->limit_ns);
+  w->abort = 1;
   return false;
 }
 
 // True once the barrier's phase `parity` has completed, false when the block
 // gave up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, uint64_t limit) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile Waits* w) {
   if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, abort, limit);
+  return mbar_wait_slow(bar, parity, w);
 }
 
 // Counts `bytes` of a phase as arrived.
