@@ -60,9 +60,17 @@ constexpr uint32_t kMaxStages = 12;
 // Shared memory of a block's stages.  One wide block, or two split blocks of
 // up to 128 accumulator columns, fit an SM at a time, so the blocks on an SM
 // never want more tensor memory than it has (a block that waited for columns
-// while its cluster waited for it could wait forever); of those with loading
-// threads (704) one fits, and two to four stages took the same time.
+// while its cluster waited for it could wait forever).  Of blocks with loading
+// threads one fits, by its 704 threads' registers, and two to four stages took
+// the same time; a wide one asks for more than it uses (kAloneShared), so that
+// no split block fits beside its 512 columns however few registers it takes.
 constexpr uint32_t kStageBudget = 196608, kSplitBudget = 98304, kLoadedBudget = 98304;
+constexpr uint32_t kAloneShared = 155648;
+// The split form's stages of 16 + 2, 4, 8 and 16 KB; an SM has 228 KB, 1 KB of
+// it goes with every block.
+constexpr uint32_t split_shared(uint32_t bn) { return 1024 + kSplitBudget / (kPBytes + bn * 128) * (kPBytes + bn * 128); }
+static_assert(kAloneShared + split_shared(16) + 2048 > 233472 && kAloneShared + split_shared(32) + 2048 > 233472 &&
+              kAloneShared + split_shared(64) + 2048 > 233472 && kAloneShared + split_shared(128) + 2048 > 233472);
 constexpr uint32_t kStagedBytes = 32 * 33 * 4;  // of an epilogue warp of the wide form
 constexpr uint32_t kMostShared = kStageBudget + 1024 + 8 * kStagedBytes;
 constexpr uint32_t kLoaders = 512;
@@ -1066,9 +1074,11 @@ cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap (&m)[4], int sms, c
   GemmArgs g = a;
   g.whole = halves ? tiles - rest : tiles;
   g.pieces = halves ? tiles + rest : tiles;
-  return launch_cluster<gemm_wide_kernel<D, kWord, kBoth, kSubs>>(
-      2 * (g.pieces < pairs ? g.pieces : pairs), kGemmThreads<kWord == 16>, 2,
-      1024 + g.stages * g.stage_bytes + kEpilogueWarps<kWord == 16> * kStagedBytes, st, g, m[0], m[1], m[2], m[3]);
+  uint32_t smem = 1024 + g.stages * g.stage_bytes + kEpilogueWarps<kWord == 16> * kStagedBytes;
+  if (smem < kAloneShared) smem = kAloneShared;
+  return launch_cluster<gemm_wide_kernel<D, kWord, kBoth, kSubs>>(2 * (g.pieces < pairs ? g.pieces : pairs),
+                                                                 kGemmThreads<kWord == 16>, 2, smem, st, g, m[0], m[1],
+                                                                 m[2], m[3]);
 }
 
 template <int D, int kWord, bool kBoth>
