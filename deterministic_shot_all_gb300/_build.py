@@ -9,7 +9,9 @@ bit-exact rank-order sum depends on.
 
 ``--bounds-check`` (``build(bounds_check=True)``) builds the checking variant,
 ``libarx_boundscheck.so``, with ``-DARX_BOUNDS_CHECK``: every data access of the
-kernels is checked against its buffer, counted and skipped when outside it.
+reduce, step and external-writer kernels is checked against its buffer, counted
+and skipped when outside it.  (The operators' address arithmetic for rows off
+16 bytes is checked on the host, from csrc/spans.h.)
 """
 
 from __future__ import annotations

@@ -145,11 +145,11 @@ __device__ __forceinline__ void st_global(uint2* p, const uint2& v) {
 // ---- bounds checks of the opt-in checking build -----------------------------------
 //
 // Built with ARX_BOUNDS_CHECK (`_build.py --bounds-check`, a separate
-// library), every data access of the kernels -- partials, slots, output --
-// is preceded by a check that [p, p + bytes) lies inside the buffer it
-// belongs to; a failed check adds 1 to a device counter and the access is
-// skipped, so a wrong index is counted instead of touching memory.  In the
-// normal build ARX_CHECKED(...) is exactly the access.
+// library), every data access of the reduce, step and external-writer kernels
+// -- partials, slots, output -- is preceded by a check that [p, p + bytes) lies
+// inside the buffer it belongs to; a failed check adds 1 to a device counter and
+// the access is skipped, so a wrong index is counted instead of touching memory.
+// In the normal build ARX_CHECKED(...) is exactly the access.
 #ifdef ARX_BOUNDS_CHECK
 __device__ __forceinline__ bool in_range(const void* p, size_t bytes, const void* base, size_t nbytes,
                                          uint32_t* counter) {

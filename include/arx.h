@@ -341,8 +341,8 @@ arx_status arx_ctx_query(arx_ctx* ctx, uint32_t* seq, uint32_t* dev_err, void* s
 
 /* ---------------------------------------------------------------------------
  * Bounds checks.  The library can be built a second way, with every data
- * access of its kernels (partials, slots, output) checked against the buffer
- * it belongs to (`python deterministic_shot_all_gb300/_build.py
+ * access of the reduce, step and external-writer kernels (partials, slots,
+ * output) checked against the buffer it belongs to (`python deterministic_shot_all_gb300/_build.py
  * --bounds-check`, which writes libarx_boundscheck.so).  A failed check is
  * counted and the access skipped.  In that build this call reads the count
  * of skipped accesses since the last reset into *count (and zeroes it if
