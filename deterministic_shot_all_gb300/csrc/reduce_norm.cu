@@ -147,8 +147,9 @@ cudaError_t run_w(const ReduceNormArgs& a, bool vec, cudaStream_t st) {
   //  above 4096 columns  1024 threads to a row fill an SM: from 153 rows on .45 to
   //                      .98 (up to 5120 columns), .6 to 1.1 (8192); up to 152
   //                      rows .85 to 1.2
-  //  2049 to 4096        W of 1 to 4 .8 to 1.25; above, from 2.5 million elements
-  //                      on .75 to 1.05, below to 1.2
+  //  2049 to 4096        W of 1 and 2 from 609 rows on .87 to 1.13, below to 1.25; 3
+  //                      and 4 .92 to 1.25; above, from 2.5 million elements on
+  //                      .75 to 1.05, below to 1.2
   //  513 to 2048         W of 1 to 6 .95 to 1.9; 7 and 8 from 2.5 million elements
   //                      on .9 to 1.05, below to 1.8 (fewer warps)
   //  257 to 512          up to 1,216 rows .95 to 1.4, above .75 to 1.15
@@ -163,8 +164,8 @@ cudaError_t run_w(const ReduceNormArgs& a, bool vec, cudaStream_t st) {
       if (n <= 1024 && work) return run<W, 32, 4, 4, 8>(a, st);
       if (n <= 2048 && work) return run<W, 64, 1, 4, 8>(a, st);
     }
-    if constexpr (W > 4)
-      if (n > 2048 && n <= 4096 && work) return run<W, 128, 1, 4, 8>(a, st);
+    if constexpr (W <= 2 || W > 4)
+      if (n > 2048 && n <= 4096 && (W <= 2 ? a.rows > 4 * 152 : work)) return run<W, 128, 1, 4, 8>(a, st);
     if (n <= 1024) return run<W, 128, 1, 1, 8>(a, st);
     if (n <= 2048) return run<W, 256, 1, 1, 8>(a, st);
     if (n <= 4096) return run<W, 512, 1, 1, 8>(a, st);

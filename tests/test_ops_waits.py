@@ -119,7 +119,7 @@ def _ones(rows, cols, lead=0):
 FORMS = {"split": (64, 128, 1 << 24, 0, 0), "split_wide": (1300, 4096, 1 << 19, 0, 0),
          "pairs": (2000, 2000, 1 << 19, 0, 0), "two_accumulators": (4096, 8192, 1 << 18, 0, 0),
          "split_threads": (64, 128, 1 << 22, 1, 1), "split_both_ways": (64, 128, 1 << 22, 0, 1),
-         "pairs_threads": (5000, 5000, 1 << 17, 1, 1), "pairs_both_ways": (4096, 4096, 1 << 17, 1, 0)}
+         "pairs_threads": (5000, 5000, 1 << 18, 1, 1), "pairs_both_ways": (4096, 4096, 1 << 18, 1, 0)}
 
 
 @pytest.mark.gpu
