@@ -1,6 +1,7 @@
 """Binding of the operators around the reduce (``include/arx.h``, "The operators
 around a sublayer's all-reduce"): matrix product with its epilogue, dropout
-with bias and residual, layer norm, and the fused end of a sublayer.
+with bias and residual, layer norm, root-mean-square norm, and the fused ends
+of a sublayer.
 
 Every operator has two forms: a function that checks its tensors and makes one
 C call, and a plan (``arx_layer_norm_plan`` and so on) that checks them once
@@ -16,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 
-ARX_BF16, ARX_F16, ARX_F32 = range(3)
+ARX_BF16, ARX_F16, ARX_F32, ARX_E4M3 = range(4)
 ARX_ACT_NONE, ARX_ACT_RELU, ARX_ACT_GELU, ARX_ACT_GELU_TANH, ARX_ACT_SILU = range(5)
 
 _vp, _u64, _i32, _f32, _f64 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int32, ctypes.c_float, ctypes.c_double
@@ -49,15 +50,25 @@ arx_linear_args = _struct(
 arx_linear_bwd_args = _struct(
     "arx_linear_bwd_args", (_vp, "dout z x w dx dw dbias workspace"), (_u64, "workspace_bytes"), (_vp, "status copies"),
     (_u64, "copies_bytes M N K lddout ldz ldx ldw lddx lddw"), (_i32, "act dtype wdtype wait_us"))
+arx_rms_norm_args = _struct(
+    "arx_rms_norm_args", (_vp, "x residual weight h y q scale rstd"), (_u64, "rows cols ldx ldresidual ldh ldy ldq"),
+    (_f32, "eps"), (_i32, "dtype wdtype reserved"))
+arx_rms_norm_bwd_args = _struct(
+    "arx_rms_norm_bwd_args", (_vp, "dy h rstd weight dresidual dx dweight workspace"),
+    (_u64, "workspace_bytes rows cols lddy ldh lddresidual lddx"), (_i32, "dtype wdtype"))
+arx_reduce_rms_norm_args = _struct(
+    "arx_reduce_rms_norm_args", (_vp, "slots residual weight h y q scale rstd"), (_u64, "rows cols ldq"), (_f32, "eps"),
+    (_i32, "W"))
 
 SIGNATURES = {
     **{f"arx_{op}": ([ctypes.POINTER(t), _vp], ctypes.c_int) for op, t in (
         ("layer_norm", arx_layer_norm_args), ("layer_norm_bwd", arx_layer_norm_bwd_args),
         ("dropout_add", arx_dropout_add_args), ("dropout_add_bwd", arx_dropout_add_bwd_args),
         ("reduce_layer_norm", arx_reduce_layer_norm_args), ("linear", arx_linear_args),
-        ("linear_bwd", arx_linear_bwd_args))},
+        ("linear_bwd", arx_linear_bwd_args), ("rms_norm", arx_rms_norm_args), ("rms_norm_bwd", arx_rms_norm_bwd_args),
+        ("reduce_rms_norm", arx_reduce_rms_norm_args))},
     **{f"arx_{op}_workspace_bytes": ([_u64, _u64], ctypes.c_size_t)
-       for op in ("layer_norm_bwd", "dropout_add_bwd", "linear_bwd")},
+       for op in ("layer_norm_bwd", "dropout_add_bwd", "linear_bwd", "rms_norm_bwd")},
     "arx_stream_capturing": ([_vp], ctypes.c_int),
     **{f"arx_{op}_copies_bytes": ([ctypes.POINTER(t)], ctypes.c_size_t) for op, t in (
         ("linear", arx_linear_args), ("linear_bwd", arx_linear_bwd_args))},
@@ -75,7 +86,8 @@ _DTYPES: dict = {}
 def _dtype(t, name, allowed):
     if not _DTYPES:
         import torch
-        _DTYPES.update({torch.bfloat16: ARX_BF16, torch.float16: ARX_F16, torch.float32: ARX_F32})
+        _DTYPES.update({torch.bfloat16: ARX_BF16, torch.float16: ARX_F16, torch.float32: ARX_F32,
+                        torch.float8_e4m3fn: ARX_E4M3})
     code = _DTYPES.get(t.dtype)
     if code not in allowed:
         raise TypeError(f"{name}: {t.dtype} not supported")
@@ -114,12 +126,13 @@ class _Marshal:
         if t.device.index != self.device:
             raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{self.device}")
 
-    def matrix(self, t, name, rows=None, cols=None, ld=None):
+    def matrix(self, t, name, rows=None, cols=None, ld=None, dtype=None):
         """Sets field ``name`` (and ``ld<name>``) to the matrix and returns (rows, cols)."""
         if t is None:
             return None
-        if t.dtype is not self.dtype:
-            raise TypeError(f"{name}: expected {self.dtype}, got {t.dtype}")
+        dtype = dtype or self.dtype
+        if t.dtype is not dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
         if t.dim() < 2:
             raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimension(s)")
         n = t.shape[-1]
@@ -364,6 +377,62 @@ def _linear_bwd(dout, x, w, dx=None, dw=None, dbias=None, z=None, act=ARX_ACT_NO
     return m.done()
 
 
+def _rms_norm(x, y, residual=None, h=None, weight=None, q=None, scale=None, rstd=None, eps=1e-6, stream=None):
+    import torch
+    m = _Marshal(arx_rms_norm_args(eps=eps), x, "x", _ROW_TYPES)
+    rows, cols = m.matrix(x, "x")
+    m.matrix(residual, "residual", rows, cols)
+    m.matrix(h, "h", rows, cols)
+    m.matrix(y, "y", rows, cols)
+    m.matrix(q, "q", rows, cols, dtype=torch.float8_e4m3fn)
+    m.vector(weight, "weight", cols)
+    m.vector(scale, "scale", rows, torch.float32)
+    m.vector(rstd, "rstd", rows, torch.float32)
+    m.a.rows, m.a.cols = rows, cols
+    return m.done()
+
+
+def _rms_norm_bwd(dy, h, rstd, dx=None, weight=None, dresidual=None, dweight=None, workspace=None, stream=None):
+    import torch
+    m = _Marshal(arx_rms_norm_bwd_args(), h, "h", _ROW_TYPES)
+    rows, cols = m.matrix(h, "h")
+    m.matrix(dy, "dy", rows, cols)
+    m.matrix(dresidual, "dresidual", rows, cols)
+    m.matrix(dx, "dx", rows, cols)
+    m.vector(rstd, "rstd", rows, torch.float32)
+    m.vector(weight, "weight", cols)
+    m.vector(dweight, "dweight", cols)
+    m.workspace(workspace)
+    m.a.rows, m.a.cols = rows, cols
+    return m.done()
+
+
+def _reduce_rms_norm(slots, h, y, residual=None, weight=None, q=None, scale=None, rstd=None, eps=1e-6, stream=None):
+    import torch
+    if len(slots) == 0:
+        raise ValueError("slots: none given")
+    first = slots[0]
+    if first.dtype is not torch.bfloat16:
+        raise TypeError(f"slots[0]: expected torch.bfloat16, got {first.dtype}")
+    if first.dim() < 2:
+        raise ValueError(f"slots[0]: expected a matrix, got {first.dim()} dimension(s)")
+    a = arx_reduce_rms_norm_args(eps=eps, W=len(slots))
+    a.cols = cols = first.shape[-1]
+    a.rows = rows = first.numel() // cols if cols else 0
+    m = _Marshal(a, first, "slots[0]", None)
+    arr = (ctypes.c_void_p * len(slots))(*[m.contiguous(s, f"slots[{i}]", rows, cols) for i, s in enumerate(slots)])
+    a.slots = ctypes.cast(arr, _vp)
+    m.refs.append(arr)
+    a.residual = m.contiguous(residual, "residual", rows, cols)
+    a.h = m.contiguous(h, "h", rows, cols)
+    a.y = m.contiguous(y, "y", rows, cols)
+    m.matrix(q, "q", rows, cols, dtype=torch.float8_e4m3fn)
+    m.vector(weight, "weight", cols, torch.bfloat16)
+    m.vector(scale, "scale", rows, torch.float32)
+    m.vector(rstd, "rstd", rows, torch.float32)
+    return m.done()
+
+
 class _Plan:
     """A checked call: one C call with the stored arguments each time it is called."""
 
@@ -477,6 +546,40 @@ Enqueue dz = dout * act'(z), dx = dz w, dw = dz^T x, dbias = sum over rows of dz
     activation and no dbias.  ``copies``, ``status`` and ``wait_us`` as in ``arx_linear``.
     """)
 
+arx_rms_norm, arx_rms_norm_plan = _function("arx_rms_norm", _rms_norm, """\
+Enqueue h = x + residual, y = h * rstd * weight with rstd = 1 / sqrt(mean(h^2) + eps) of each row.
+
+    ``arx_rms_norm(x, y, residual=None, h=None, weight=None, q=None, scale=None, rstd=None, eps=1e-6,
+    stream=None, check=True)``
+
+    bf16, fp16 or fp32; weight of the same type or fp32.  ``h`` receives the sum (it and ``y``
+    may each be ``x`` or ``residual``, not each other).  ``q``, a float8_e4m3fn matrix, and
+    ``scale``, fp32 [rows], receive y in 8 bits: y = q * scale, scale = max |y| / 448 of each
+    row; ``y`` may then be None.  Give q rows on 16 bytes for ``arx_gated_linear``.
+    """)
+arx_rms_norm_bwd, arx_rms_norm_bwd_plan = _function("arx_rms_norm_bwd", _rms_norm_bwd, """\
+Enqueue the gradients of ``arx_rms_norm``, from its ``h`` and ``rstd``.
+
+    ``arx_rms_norm_bwd(dy, h, rstd, dx=None, weight=None, dresidual=None, dweight=None, workspace=None,
+    stream=None, check=True)``
+
+    ``dx`` is the gradient of x and of the residual alike; ``dresidual`` is added to it; dx may
+    be dy, h or dresidual.  ``workspace``: a device tensor of
+    ``arx_rms_norm_bwd_workspace_bytes(rows, cols)`` bytes when dweight is asked for.
+    """)
+arx_reduce_rms_norm, arx_reduce_rms_norm_plan = _function("arx_reduce_rms_norm", _reduce_rms_norm, """\
+Enqueue h = residual + rank-order sum of slots, then ``arx_rms_norm`` of h.
+
+    ``arx_reduce_rms_norm(slots, h, y, residual=None, weight=None, q=None, scale=None, rstd=None, eps=1e-6,
+    stream=None, check=True)``
+
+    bf16, contiguous (q: rows of any distance); ``h`` and ``y`` (each may be None) may each be a
+    slot or the residual; ``q`` and ``scale`` as in ``arx_rms_norm``.
+    """)
+
+def arx_rms_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_core().lib.arx_rms_norm_bwd_workspace_bytes(rows, cols))
+
 
 def arx_layer_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
     return int(_core().lib.arx_layer_norm_bwd_workspace_bytes(rows, cols))
@@ -509,11 +612,13 @@ def arx_linear_bwd_copies_bytes(dout, x=None, w=None, dx=None, dw=None, act=ARX_
 
 
 __all__ = [
-    "ARX_BF16", "ARX_F16", "ARX_F32", "ARX_ACT_NONE", "ARX_ACT_RELU", "ARX_ACT_GELU", "ARX_ACT_GELU_TANH",
+    "ARX_BF16", "ARX_F16", "ARX_F32", "ARX_E4M3", "ARX_ACT_NONE", "ARX_ACT_RELU", "ARX_ACT_GELU", "ARX_ACT_GELU_TANH",
     "ARX_ACT_SILU",
     *(f"arx_{op}{suffix}" for op in ("layer_norm", "layer_norm_bwd", "dropout_add", "dropout_add_bwd",
-                                     "reduce_layer_norm", "linear", "linear_bwd")
+                                     "reduce_layer_norm", "linear", "linear_bwd", "rms_norm", "rms_norm_bwd",
+                                     "reduce_rms_norm")
       for suffix in ("", "_plan", "_args")),
     "arx_layer_norm_bwd_workspace_bytes", "arx_dropout_add_bwd_workspace_bytes", "arx_linear_bwd_workspace_bytes",
     "arx_linear_copies_bytes", "arx_linear_bwd_copies_bytes", "arx_stream_capturing",
+    "arx_rms_norm_bwd_workspace_bytes",
 ]

@@ -50,6 +50,13 @@ cudaError_t launch_layer_norm_bwd(const arx_layer_norm_bwd_args& a, bool vec, cu
 // Partial rows that the backward pass writes for each of its two sums.
 size_t norm_bwd_parts(uint64_t rows, uint64_t cols);
 
+// The same for the root-mean-square norm; units of 8 elements of q are 8 bytes.
+cudaError_t launch_rms_norm(const arx_rms_norm_args& a, bool vec, cudaStream_t st);
+cudaError_t launch_reduce_rms_norm(const arx_reduce_rms_norm_args& a, bool vec, cudaStream_t st);
+cudaError_t launch_rms_norm_bwd(const arx_rms_norm_bwd_args& a, bool vec, cudaStream_t st);
+// Partial rows of dweight that the backward pass writes.
+size_t rms_bwd_parts(uint64_t rows);
+
 // threshold and scale of a dropout probability (see arx.h).
 void dropout_constants(double p, uint32_t* threshold, float* scale);
 cudaError_t launch_dropout_add(const arx_dropout_add_args& a, bool vec, cudaStream_t st);

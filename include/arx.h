@@ -539,7 +539,9 @@ arx_status arx_step_noalloc(const void* const* inputs, int W, void* out, size_t 
  * the ranks' partials are summed in rank order, and the sum goes through
  * bias, dropout and the residual add into a layer norm
  * (arx_reduce_layer_norm, or arx_reduce, arx_dropout_add and arx_layer_norm
- * one after the other); the *_bwd calls are their backward passes.
+ * one after the other), or, in a block with a root-mean-square norm, through the residual add into that norm
+ * (arx_reduce_rms_norm, or arx_reduce and arx_rms_norm); the *_bwd calls are
+ * their backward passes.
  *
  * Conventions, beside those at the top:
  *  - Matrices are row-major: element (i, j) of x is x[i * ldx + j], ldx in
@@ -569,6 +571,7 @@ arx_status arx_step_noalloc(const void* const* inputs, int W, void* out, size_t 
 #define ARX_BF16 0
 #define ARX_F16 1
 #define ARX_F32 2
+#define ARX_E4M3 3 /* 8-bit floating point, 4 bits of exponent: where a call names it */
 
 /* Layer norm of each row:
  *   mean = sum(x) / cols, var = sum((x - mean)^2) / cols, rstd = 1 / sqrt(var + eps),
@@ -706,6 +709,95 @@ typedef struct arx_reduce_layer_norm_args {
 } arx_reduce_layer_norm_args;
 
 arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stream);
+
+/* Root-mean-square norm of each row, with the residual's addition before it:
+ *   h = x + residual,
+ *   rstd = 1 / sqrt(sum(h^2) / cols + eps),  v = h * rstd * weight,
+ * the norm taken of h before its rounding.  y is v; q is v in 8 bits (e4m3),
+ * with a scale for each row:
+ *   scale = max |v| / 448, or 1 where that is below 2^-126,  q = e4m3(v / scale),
+ * rounded to nearest even and never above 448, the type's largest number.  A row
+ * with a NaN has a NaN scale and NaN in all of q.
+ *   x         [rows, cols] of `dtype`
+ *   residual  [rows, cols], or NULL for 0
+ *   weight    [cols] of `wdtype`, or NULL for 1
+ *   h         [rows, cols], or NULL; may be exactly x or the residual
+ *   y         [rows, cols], or NULL; may be exactly x or the residual
+ *   q         [rows, cols] of ARX_E4M3, or NULL (one of y and q is needed)
+ *   scale     fp32 [rows], with q only (ignored without)
+ *   rstd      fp32 [rows], or NULL */
+typedef struct arx_rms_norm_args {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* h;
+  void* y;
+  void* q;
+  float* scale;
+  float* rstd;
+  uint64_t rows, cols, ldx, ldresidual, ldh, ldy, ldq;
+  float eps;
+  int32_t dtype, wdtype;
+  int32_t reserved;
+} arx_rms_norm_args;
+
+arx_status arx_rms_norm(const arx_rms_norm_args* a, void* stream);
+
+/* Its backward pass, from the forward's h and rstd:
+ *   v = dy * weight, n = h * rstd,
+ *   dx = rstd * (v - n * sum(v * n) / cols) + dresidual,
+ *   dweight = sum over rows of dy * n.
+ * x and the residual of the forward both have the gradient dx.
+ *   dy, h, dresidual  [rows, cols]; dresidual (the gradient that reaches h past the
+ *               norm) may be NULL
+ *   dx          [rows, cols]; may be exactly dy, h or dresidual; NULL skips it
+ *   dweight     [cols] of `wdtype`, or NULL; zero when rows == 0
+ *   workspace   arx_rms_norm_bwd_workspace_bytes(rows, cols) bytes; may be NULL when
+ *               dweight is */
+typedef struct arx_rms_norm_bwd_args {
+  const void* dy;
+  const void* h;
+  const float* rstd;
+  const void* weight;
+  const void* dresidual;
+  void* dx;
+  void* dweight;
+  void* workspace;
+  uint64_t workspace_bytes;
+  uint64_t rows, cols, lddy, ldh, lddresidual, lddx;
+  int32_t dtype, wdtype;
+} arx_rms_norm_bwd_args;
+
+size_t arx_rms_norm_bwd_workspace_bytes(uint64_t rows, uint64_t cols);
+arx_status arx_rms_norm_bwd(const arx_rms_norm_bwd_args* a, void* stream);
+
+/* The end of a sublayer with this norm in one kernel, for bf16 partials:
+ *   h = residual + (((+0 + slot[0]) + slot[1]) + ...) in rank order (as arx_reduce,
+ *   not rounded), then as arx_rms_norm.
+ *   slots     HOST array of W device pointers, each to a contiguous bf16 [rows, cols];
+ *             read during the call only; slots may repeat or overlap each other
+ *   residual  contiguous bf16 [rows, cols] or NULL
+ *   weight    bf16 [cols] or NULL
+ *   h, y      contiguous bf16 [rows, cols] or NULL; each may be exactly a slot or the
+ *             residual, but not each other
+ *   q         [rows, cols] of ARX_E4M3 in rows of ldq, or NULL (one of y and q is needed)
+ *   scale     fp32 [rows], with q only;  rstd  fp32 [rows] or NULL
+ * arx_rms_norm_bwd is its backward pass: every slot has the gradient dx. */
+typedef struct arx_reduce_rms_norm_args {
+  const void* const* slots;
+  const void* residual;
+  const void* weight;
+  void* h;
+  void* y;
+  void* q;
+  float* scale;
+  float* rstd;
+  uint64_t rows, cols, ldq;
+  float eps;
+  int32_t W;
+} arx_reduce_rms_norm_args;
+
+arx_status arx_reduce_rms_norm(const arx_reduce_rms_norm_args* a, void* stream);
 
 /* Matrix product with bias, activation and residual in its epilogue:
  *   z = x w^T + bias,  out = act(z) + residual.
