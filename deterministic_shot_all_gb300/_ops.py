@@ -1,7 +1,7 @@
 """Binding of the operators around the reduce (``include/arx.h``, "The operators
 around a sublayer's all-reduce"): matrix product with its epilogue, dropout
-with bias and residual, layer norm, root-mean-square norm, and the fused ends
-of a sublayer.
+with bias and residual, layer norm, root-mean-square norm, the fused ends of a
+sublayer, and the gated feed-forward block.
 
 Every operator has two forms: a function that checks its tensors and makes one
 C call, and a plan (``arx_layer_norm_plan`` and so on) that checks them once
@@ -59,6 +59,17 @@ arx_rms_norm_bwd_args = _struct(
 arx_reduce_rms_norm_args = _struct(
     "arx_reduce_rms_norm_args", (_vp, "slots residual weight h y q scale rstd"), (_u64, "rows cols ldq"), (_f32, "eps"),
     (_i32, "W"))
+arx_gated_linear_args = _struct(
+    "arx_gated_linear_args",
+    (_vp, "x w_gate w_up x_scale gate_scale up_scale bias_gate bias_up out z_gate z_up status copies"),
+    (_u64, "copies_bytes M N K ldx ldw_gate ldw_up ldout ldz_gate ldz_up"),
+    (_i32, "act dtype out_dtype wdtype wait_us reserved"))
+arx_gated_linear_bwd_args = _struct(
+    "arx_gated_linear_bwd_args",
+    (_vp, "dout z_gate z_up x w_gate w_up dx dw_gate dw_up dbias_gate dbias_up workspace"), (_u64, "workspace_bytes"),
+    (_vp, "status copies"),
+    (_u64, "copies_bytes M N K lddout ldz_gate ldz_up ldx ldw_gate ldw_up lddx lddw_gate lddw_up"),
+    (_i32, "act dtype wdtype wait_us"))
 
 SIGNATURES = {
     **{f"arx_{op}": ([ctypes.POINTER(t), _vp], ctypes.c_int) for op, t in (
@@ -66,12 +77,14 @@ SIGNATURES = {
         ("dropout_add", arx_dropout_add_args), ("dropout_add_bwd", arx_dropout_add_bwd_args),
         ("reduce_layer_norm", arx_reduce_layer_norm_args), ("linear", arx_linear_args),
         ("linear_bwd", arx_linear_bwd_args), ("rms_norm", arx_rms_norm_args), ("rms_norm_bwd", arx_rms_norm_bwd_args),
-        ("reduce_rms_norm", arx_reduce_rms_norm_args))},
+        ("reduce_rms_norm", arx_reduce_rms_norm_args), ("gated_linear", arx_gated_linear_args),
+        ("gated_linear_bwd", arx_gated_linear_bwd_args))},
     **{f"arx_{op}_workspace_bytes": ([_u64, _u64], ctypes.c_size_t)
-       for op in ("layer_norm_bwd", "dropout_add_bwd", "linear_bwd", "rms_norm_bwd")},
+       for op in ("layer_norm_bwd", "dropout_add_bwd", "linear_bwd", "rms_norm_bwd", "gated_linear_bwd")},
     "arx_stream_capturing": ([_vp], ctypes.c_int),
     **{f"arx_{op}_copies_bytes": ([ctypes.POINTER(t)], ctypes.c_size_t) for op, t in (
-        ("linear", arx_linear_args), ("linear_bwd", arx_linear_bwd_args))},
+        ("linear", arx_linear_args), ("linear_bwd", arx_linear_bwd_args), ("gated_linear", arx_gated_linear_args),
+        ("gated_linear_bwd", arx_gated_linear_bwd_args))},
 }
 
 
@@ -257,7 +270,8 @@ class _Marshal:
 
     def done(self):
         if hasattr(self.a, "wdtype"):
-            self.a.wdtype = self.a.dtype if self.wdtype in (None, self.dtype) else ARX_F32
+            own = getattr(self.a, "out_dtype", self.a.dtype)
+            self.a.wdtype = own if self.wdtype in (None, self.dtype) else ARX_F32
         return self
 
 
@@ -433,6 +447,56 @@ def _reduce_rms_norm(slots, h, y, residual=None, weight=None, q=None, scale=None
     return m.done()
 
 
+def _gated_linear(x, w_gate, w_up, out, bias_gate=None, bias_up=None, z_gate=None, z_up=None, act=ARX_ACT_SILU,
+                  x_scale=None, gate_scale=None, up_scale=None, status=None, copies=None, wait_us=0, stream=None):
+    import torch
+    m = _Marshal(arx_gated_linear_args(act=act, wait_us=wait_us), x, "x", (*_PRODUCT_TYPES, ARX_E4M3))
+    M, K = m.matrix(x, "x")
+    N, _ = m.matrix(w_gate, "w_gate", None, K)
+    m.matrix(w_up, "w_up", N, K)
+    if m.a.dtype == ARX_E4M3 and out is not None:  # the outputs and biases have a type of their own
+        m.dtype = out.dtype
+        m.a.out_dtype = _dtype(out, "out", _PRODUCT_TYPES)
+    else:
+        m.a.out_dtype = m.a.dtype
+    m.matrix(out, "out", M, N)
+    m.matrix(z_gate, "z_gate", M, N)
+    m.matrix(z_up, "z_up", M, N)
+    m.vector(bias_gate, "bias_gate", N)
+    m.vector(bias_up, "bias_up", N)
+    for t, name, n in ((x_scale, "x_scale", M), (gate_scale, "gate_scale", N), (up_scale, "up_scale", N)):
+        m.vector(t, name, n, torch.float32)
+    m.status(status)
+    m.a.M, m.a.N, m.a.K = M, N, K
+    if m.a.dtype != ARX_E4M3:
+        m.copies(copies, _core().lib.arx_gated_linear_copies_bytes, ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")),
+                 stream)
+    return m.done()
+
+
+def _gated_linear_bwd(dout, x, w_gate, w_up, z_gate, z_up, dx=None, dw_gate=None, dw_up=None, dbias_gate=None,
+                      dbias_up=None, act=ARX_ACT_SILU, workspace=None, status=None, copies=None, wait_us=0, stream=None):
+    m = _Marshal(arx_gated_linear_bwd_args(act=act, wait_us=wait_us), dout, "dout", _PRODUCT_TYPES)
+    M, N = m.matrix(dout, "dout")
+    K = next((t.shape[-1] for t in (x, w_gate, w_up) if t is not None), 0)
+    m.matrix(z_gate, "z_gate", M, N)
+    m.matrix(z_up, "z_up", M, N)
+    m.matrix(x, "x", M, K)
+    m.matrix(w_gate, "w_gate", N, K)
+    m.matrix(w_up, "w_up", N, K)
+    m.matrix(dx, "dx", M, K)
+    m.matrix(dw_gate, "dw_gate", N, K)
+    m.matrix(dw_up, "dw_up", N, K)
+    m.vector(dbias_gate, "dbias_gate", N)
+    m.vector(dbias_up, "dbias_up", N)
+    m.workspace(workspace)
+    m.status(status)
+    m.a.M, m.a.N, m.a.K = M, N, K
+    m.copies(copies, _core().lib.arx_gated_linear_bwd_copies_bytes, ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")),
+             stream)
+    return m.done()
+
+
 class _Plan:
     """A checked call: one C call with the stored arguments each time it is called."""
 
@@ -576,9 +640,49 @@ Enqueue h = residual + rank-order sum of slots, then ``arx_rms_norm`` of h.
     bf16, contiguous (q: rows of any distance); ``h`` and ``y`` (each may be None) may each be a
     slot or the residual; ``q`` and ``scale`` as in ``arx_rms_norm``.
     """)
+arx_gated_linear, arx_gated_linear_plan = _function("arx_gated_linear", _gated_linear, """\
+Enqueue out = act(x w_gate^T + bias_gate) * (x w_up^T + bias_up) on the tensor cores.
+
+    ``arx_gated_linear(x, w_gate, w_up, out, bias_gate=None, bias_up=None, z_gate=None, z_up=None,
+    act=ARX_ACT_SILU, x_scale=None, gate_scale=None, up_scale=None, status=None, copies=None, wait_us=0,
+    stream=None, check=True)``
+
+    bf16 or fp16, or float8_e4m3fn operands with a bf16 or fp16 ``out``: x [M, K], w_gate and
+    w_up [N, K]; the fp32 scales [M], [N], [N] multiply the 8-bit sums.  8-bit operands are on
+    rows of 16 bytes.  Biases of out's type or fp32.  ``z_gate`` and ``z_up`` receive the two
+    projections for the backward pass.  ``copies`` as in ``arx_linear``, but operands whose rows
+    are off 16 bytes need them (False is an error there).
+    """)
+arx_gated_linear_bwd, arx_gated_linear_bwd_plan = _function("arx_gated_linear_bwd", _gated_linear_bwd, """\
+Enqueue dg = dout * u * act'(g), du = dout * act(g) and from them the gradients of ``arx_gated_linear``.
+
+    ``arx_gated_linear_bwd(dout, x, w_gate, w_up, z_gate, z_up, dx=None, dw_gate=None, dw_up=None,
+    dbias_gate=None, dbias_up=None, act=ARX_ACT_SILU, workspace=None, status=None, copies=None, wait_us=0,
+    stream=None, check=True)``
+
+    dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x, the biases' gradients the sums
+    over rows.  ``workspace`` of ``arx_gated_linear_bwd_workspace_bytes(M, N)`` bytes.
+    """)
+
 
 def arx_rms_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
     return int(_core().lib.arx_rms_norm_bwd_workspace_bytes(rows, cols))
+
+
+def arx_gated_linear_bwd_workspace_bytes(M: int, N: int) -> int:
+    return int(_core().lib.arx_gated_linear_bwd_workspace_bytes(M, N))
+
+
+def arx_gated_linear_copies_bytes(x, w_gate, w_up) -> int:
+    """Bytes of ``copies`` for ``arx_gated_linear`` of these operands."""
+    a = _gated_linear(x, w_gate, w_up, None, copies=False).a
+    return int(_core().lib.arx_gated_linear_copies_bytes(ctypes.byref(a)))
+
+
+def arx_gated_linear_bwd_copies_bytes(dout, x=None, w_gate=None, w_up=None, dx=None, dw_gate=None, dw_up=None) -> int:
+    """Bytes of ``copies`` for ``arx_gated_linear_bwd`` with these arguments."""
+    a = _gated_linear_bwd(dout, x, w_gate, w_up, None, None, dx=dx, dw_gate=dw_gate, dw_up=dw_up, copies=False).a
+    return int(_core().lib.arx_gated_linear_bwd_copies_bytes(ctypes.byref(a)))
 
 
 def arx_layer_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
@@ -616,9 +720,10 @@ __all__ = [
     "ARX_ACT_SILU",
     *(f"arx_{op}{suffix}" for op in ("layer_norm", "layer_norm_bwd", "dropout_add", "dropout_add_bwd",
                                      "reduce_layer_norm", "linear", "linear_bwd", "rms_norm", "rms_norm_bwd",
-                                     "reduce_rms_norm")
+                                     "reduce_rms_norm", "gated_linear", "gated_linear_bwd")
       for suffix in ("", "_plan", "_args")),
     "arx_layer_norm_bwd_workspace_bytes", "arx_dropout_add_bwd_workspace_bytes", "arx_linear_bwd_workspace_bytes",
     "arx_linear_copies_bytes", "arx_linear_bwd_copies_bytes", "arx_stream_capturing",
-    "arx_rms_norm_bwd_workspace_bytes",
+    "arx_rms_norm_bwd_workspace_bytes", "arx_gated_linear_bwd_workspace_bytes", "arx_gated_linear_copies_bytes",
+    "arx_gated_linear_bwd_copies_bytes",
 ]

@@ -96,11 +96,29 @@ struct GemmCall {
   uint32_t* status;
   uint32_t wait_ns;       // limit of a kernel's wait for its own copies and products
   void* copies;           // gemm_copies_bytes(c) bytes, or null
+  const void *p2, *q2;    // null, or a second pair of operands of the same sizes whose product joins
+  uint64_t ldp2, ldq2;    // the sum: all four on rows of 16 bytes, without copies
 };
 cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st);
 // Bytes for copies of the operands whose rows are off 16 bytes, 0 where the
 // product is faster without.
 size_t gemm_copies_bytes(const GemmCall& c);
+
+// The gated block's forward pass (see gated.cu): arx_gated_linear_args, checked.
+cudaError_t launch_gated(const arx_gated_linear_args& a, cudaStream_t st);
+// Bytes for copies of 16-bit operands whose rows are off 16 bytes.
+size_t gated_copies_bytes(const arx_gated_linear_args& a);
+
+// dg = dout * u * act'(g), du = dout * act(g) and their column sums.
+struct GatedGradCall {
+  const void *dout, *z_gate, *z_up;
+  void* dz;              // rows of lddz: dg, and du from column `du` on (on rows of 16 bytes); null: sums only
+  void *dbias_gate, *dbias_up;  // either may be null
+  float* part;           // 2 x column_parts(rows, cols) x cols floats
+  uint64_t rows, cols, lddout, ldz_gate, ldz_up, lddz, du;
+  int act, dtype, wdtype;
+};
+cudaError_t launch_gated_grad(const GatedGradCall& c, bool vec, cudaStream_t st);
 
 // Copies of 16-bit matrices: rows of `cols` elements from `ld` to `ld_dst`
 // (a multiple of 2, at least cols) apart, dst on 4 bytes.
@@ -110,10 +128,10 @@ struct Realign {
   uint64_t rows, ld, ld_dst;
   int64_t cols;
 };
-struct RealignPair {
-  Realign m[2];
+struct RealignSet {
+  Realign m[3];
   int n;
 };
-cudaError_t launch_realign(const RealignPair& pair, cudaStream_t st);
+cudaError_t launch_realign(const RealignSet& set, cudaStream_t st);
 
 }  // namespace arx

@@ -58,9 +58,9 @@ __device__ __forceinline__ void realign_chunk(const Realign& a, const uint16_t* 
     if (kInside || 2 * int64_t(lane + 32 * i) < rest) dst[32 * i] = w[i];  // a last odd column's neighbour is padding
 }
 
-__global__ void __launch_bounds__(32 * kWarps) realign_kernel(const __grid_constant__ RealignPair pair) {
+__global__ void __launch_bounds__(32 * kWarps) realign_kernel(const __grid_constant__ RealignSet set) {
   dependent_launch_prologue();
-  const Realign& a = pair.m[blockIdx.z];
+  const Realign& a = set.m[blockIdx.z];
   const uint32_t lane = threadIdx.x & 31;
   for (int64_t c0 = int64_t(blockIdx.x) * kChunk; c0 < a.cols; c0 += int64_t(gridDim.x) * kChunk)
     for (uint64_t row = blockIdx.y * kWarps + threadIdx.x / 32; row < a.rows; row += uint64_t(gridDim.y) * kWarps) {
@@ -76,15 +76,15 @@ __global__ void __launch_bounds__(32 * kWarps) realign_kernel(const __grid_const
 
 }  // namespace
 
-cudaError_t launch_realign(const RealignPair& pair, cudaStream_t st) {
+cudaError_t launch_realign(const RealignSet& set, cudaStream_t st) {
   uint64_t rows = 0, cols = 0;
-  for (int i = 0; i < pair.n; ++i) {
-    if (pair.m[i].rows > rows) rows = pair.m[i].rows;
-    if (uint64_t(pair.m[i].cols) > cols) cols = uint64_t(pair.m[i].cols);
+  for (int i = 0; i < set.n; ++i) {
+    if (set.m[i].rows > rows) rows = set.m[i].rows;
+    if (uint64_t(set.m[i].cols) > cols) cols = uint64_t(set.m[i].cols);
   }
   const uint64_t y = (rows + kWarps - 1) / kWarps, x = (cols + kChunk - 1) / kChunk;
-  return launch_op(realign_kernel, dim3(unsigned(x), unsigned(y < 65535 ? y : 65535), unsigned(pair.n)), 32 * kWarps, 0,
-                   st, pair);
+  return launch_op(realign_kernel, dim3(unsigned(x), unsigned(y < 65535 ? y : 65535), unsigned(set.n)), 32 * kWarps, 0,
+                   st, set);
 }
 
 }  // namespace arx

@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t global_timer_low_ns() {
   return t;
 }
 
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile Waits* w) {
+inline __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile Waits* w) {
   uint32_t last = global_timer_low_ns(), waited = 0;
   do {
     for (uint32_t i = 0; i < kPollsToLook; ++i)
@@ -235,6 +235,21 @@ __device__ __forceinline__ void mma_f16(uint32_t tmem, uint64_t a, uint64_t b, u
         :: "r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)) : "memory");
 }
 
+// The same over 32 contraction steps of 8-bit operands (both e4m3).
+template <bool kPair>
+__device__ __forceinline__ void mma_f8(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+        :: "r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)) : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+        :: "r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)) : "memory");
+}
+
 // Arrives on `bar` (of both blocks of a pair) when every matrix instruction
 // this thread issued is done.
 template <bool kPair>
@@ -256,7 +271,8 @@ __device__ __forceinline__ void mma_commit_own(uint32_t bar) {
     mma_commit<false>(bar);
 }
 
-// Instruction descriptor: fp32 accumulators, both operands bf16 or both fp16.
+// Instruction descriptor: fp32 accumulators, both operands bf16 or both fp16, or,
+// without bf16 in an 8-bit instruction, both e4m3.
 inline uint32_t mma_descriptor(bool bf16, bool a_mn, bool b_mn, uint32_t m, uint32_t n) {
   return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (uint32_t(a_mn) << 15) |
          (uint32_t(b_mn) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);

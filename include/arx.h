@@ -539,9 +539,10 @@ arx_status arx_step_noalloc(const void* const* inputs, int W, void* out, size_t 
  * the ranks' partials are summed in rank order, and the sum goes through
  * bias, dropout and the residual add into a layer norm
  * (arx_reduce_layer_norm, or arx_reduce, arx_dropout_add and arx_layer_norm
- * one after the other), or, in a block with a root-mean-square norm, through the residual add into that norm
- * (arx_reduce_rms_norm, or arx_reduce and arx_rms_norm); the *_bwd calls are
- * their backward passes.
+ * one after the other), or, in a block with a root-mean-square norm and a gated
+ * feed-forward part, through the residual add into that norm
+ * (arx_reduce_rms_norm, or arx_reduce and arx_rms_norm) and on to both
+ * projections (arx_gated_linear); the *_bwd calls are their backward passes.
  *
  * Conventions, beside those at the top:
  *  - Matrices are row-major: element (i, j) of x is x[i * ldx + j], ldx in
@@ -889,6 +890,87 @@ typedef struct arx_linear_bwd_args {
 size_t arx_linear_bwd_workspace_bytes(uint64_t M, uint64_t N);
 size_t arx_linear_bwd_copies_bytes(const arx_linear_bwd_args* a);
 arx_status arx_linear_bwd(const arx_linear_bwd_args* a, void* stream);
+
+/* Gated feed-forward block, both projections and their product in one kernel:
+ *   g = x w_gate^T + bias_gate,  u = x w_up^T + bias_up,  out = act(g) * u.
+ *   x       [M, K], w_gate and w_up [N, K], of `dtype`: ARX_BF16, ARX_F16 or ARX_E4M3;
+ *           products summed in fp32 on the tensor cores.  The weights may be parts of
+ *           one buffer, one after the other or with interleaved rows
+ *   x_scale, gate_scale, up_scale  fp32 [M], [N] and [N], with ARX_E4M3 only (there each
+ *           may be NULL for 1): g is the sum times x_scale[m] * gate_scale[n], u times
+ *           x_scale[m] * up_scale[n], before the biases
+ *   bias_gate, bias_up  [N] of `wdtype` (out_dtype or ARX_F32); either may be NULL
+ *   out     [M, N] of `out_dtype`: `dtype`, or ARX_BF16 or ARX_F16 with ARX_E4M3
+ *   z_gate, z_up  [M, N] of out_dtype, or NULL: g and u, for arx_gated_linear_bwd
+ *   act     ARX_ACT_*, as in arx_linear
+ *   copies  arx_gated_linear_copies_bytes(a) bytes on 16 bytes: 16-bit operands whose
+ *           address or leading dimension is off 16 bytes are copied here first.  May be
+ *           NULL where that is 0; 8-bit operands have to be on 16 bytes (their
+ *           leading dimension a multiple of 16; K may be any)
+ *   status, wait_us  as in arx_linear */
+typedef struct arx_gated_linear_args {
+  const void* x;
+  const void* w_gate;
+  const void* w_up;
+  const float* x_scale;
+  const float* gate_scale;
+  const float* up_scale;
+  const void* bias_gate;
+  const void* bias_up;
+  void* out;
+  void* z_gate;
+  void* z_up;
+  uint32_t* status;
+  void* copies;
+  uint64_t copies_bytes;
+  uint64_t M, N, K, ldx, ldw_gate, ldw_up, ldout, ldz_gate, ldz_up;
+  int32_t act, dtype, out_dtype, wdtype;
+  int32_t wait_us, reserved;
+} arx_gated_linear_args;
+
+size_t arx_gated_linear_copies_bytes(const arx_gated_linear_args* a);
+arx_status arx_gated_linear(const arx_gated_linear_args* a, void* stream);
+
+/* Its backward pass, for 16-bit operands:
+ *   dg = dout * u * act'(g),  du = dout * act(g),
+ *   dx = dg w_gate + du w_up (one sum),  dw_gate = dg^T x,  dw_up = du^T x,
+ *   dbias_gate = sum over rows of dg,  dbias_up = sum over rows of du.
+ * dg and du are operands of the products and so rounded to `dtype`; the bias
+ * gradients sum them unrounded.
+ *   dout, z_gate, z_up  [M, N]; z_gate (g) and z_up (u) from the forward
+ *   x, w_gate, w_up     as in the forward; x may be NULL without dw_gate and dw_up, the
+ *           weights without dx
+ *   dx      [M, K], dw_gate and dw_up [N, K], dbias_gate and dbias_up [N] of `wdtype`;
+ *           any may be NULL.  M == 0 sets the weights' and biases' gradients to zero
+ *   workspace  arx_gated_linear_bwd_workspace_bytes(M, N) bytes (dg, du, partial sums)
+ *   copies  arx_gated_linear_bwd_copies_bytes(a) bytes: of w_gate and w_up, then of x;
+ *           may be NULL where that is 0
+ *   status, wait_us  as in arx_linear */
+typedef struct arx_gated_linear_bwd_args {
+  const void* dout;
+  const void* z_gate;
+  const void* z_up;
+  const void* x;
+  const void* w_gate;
+  const void* w_up;
+  void* dx;
+  void* dw_gate;
+  void* dw_up;
+  void* dbias_gate;
+  void* dbias_up;
+  void* workspace;
+  uint64_t workspace_bytes;
+  uint32_t* status;
+  void* copies;
+  uint64_t copies_bytes;
+  uint64_t M, N, K, lddout, ldz_gate, ldz_up, ldx, ldw_gate, ldw_up, lddx, lddw_gate, lddw_up;
+  int32_t act, dtype, wdtype;
+  int32_t wait_us;
+} arx_gated_linear_bwd_args;
+
+size_t arx_gated_linear_bwd_workspace_bytes(uint64_t M, uint64_t N);
+size_t arx_gated_linear_bwd_copies_bytes(const arx_gated_linear_bwd_args* a);
+arx_status arx_gated_linear_bwd(const arx_gated_linear_bwd_args* a, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,4 +1,4 @@
-"""Host-side checks of the root-mean-square norm's entry points (no GPU, no kernel launched).
+"""Host-side checks of the root-mean-square norm's and the gated block's entry points (no GPU, no kernel launched).
 
 * the 64-bit plain forms' gradients are pinned to differences of their formulas;
 * the binding's structs have the layout that a C compiler gives the header's;
@@ -19,7 +19,7 @@ import gated_plain as plain
 from conftest import ROOT, gpu_available
 
 FAKE = 1 << 40
-STRUCTS = ("rms_norm", "rms_norm_bwd", "reduce_rms_norm")
+STRUCTS = ("rms_norm", "rms_norm_bwd", "reduce_rms_norm", "gated_linear", "gated_linear_bwd")
 
 
 # ---- the plain forms ----------------------------------------------------------------
@@ -41,6 +41,22 @@ def test_rms_norm_gradients_against_differences():
         e[j] = h
         assert abs((loss(x, w + e) - loss(x, w - e)) / (2 * h) - dw[j]) < 1e-7
     assert np.allclose(plain.rms_norm_bwd(dy, x, rstd, w, dy)[0], dx + dy)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_gated_gradients_against_differences(act):
+    r = np.random.default_rng(1)
+    a = [r.normal(size=s) for s in ((3, 5), (4, 5), (4, 5), (4,), (4,))]  # x, both weights, both biases
+    dout = r.normal(size=(3, 4))
+    loss = lambda a: (plain.gated(*a[:3], act, *a[3:])[0] * dout).sum()  # noqa: E731
+    _, g, u = plain.gated(*a[:3], act, *a[3:])
+    grads, h = plain.gated_bwd(dout, g, u, *a[:3], act), 1e-6
+    for i, grad in enumerate(grads):
+        for at in np.ndindex(a[i].shape):
+            up, down = [t.copy() for t in a], [t.copy() for t in a]
+            up[i][at] += h
+            down[i][at] -= h
+            assert abs((loss(up) - loss(down)) / (2 * h) - grad[at]) < 1e-7
 
 
 # ---- the C interface ----------------------------------------------------------------
@@ -79,6 +95,14 @@ def _good(arx, op):
         a = arx.arx_rms_norm_bwd_args(rows=4, cols=16, lddy=16, ldh=16, lddresidual=16, lddx=16)
         a.workspace_bytes = arx.arx_rms_norm_bwd_workspace_bytes(4, 16)
         names = "dy h rstd weight dresidual dx dweight workspace"
+    elif op == "gated_linear":
+        a = arx.arx_gated_linear_args(M=4, N=16, K=8, ldx=8, ldw_gate=8, ldw_up=8, ldout=16, ldz_gate=16, ldz_up=16, act=4)
+        names = "x w_gate w_up bias_gate bias_up out z_gate z_up status"
+    elif op == "gated_linear_bwd":
+        a = arx.arx_gated_linear_bwd_args(M=4, N=16, K=8, lddout=16, ldz_gate=16, ldz_up=16, ldx=8, ldw_gate=8, ldw_up=8,
+                                          lddx=8, lddw_gate=8, lddw_up=8, act=4)
+        a.workspace_bytes = arx.arx_gated_linear_bwd_workspace_bytes(4, 16)
+        names = "dout z_gate z_up x w_gate w_up dx dw_gate dw_up dbias_gate dbias_up workspace status"
     else:
         a = arx.arx_reduce_rms_norm_args(rows=4, cols=16, ldq=16, W=2, eps=1e-6)
         slots = (ctypes.c_void_p * 2)(_region(20), _region(21))
@@ -150,6 +174,46 @@ REFUSED = [
     ("reduce_rms_norm", {"h": _region(20) + 2}, "EOVERLAP", "h overlaps a slot"),
     ("reduce_rms_norm", {"q": _region(21)}, "EOVERLAP", "q overlaps a slot"),
     ("reduce_rms_norm", {"y": _region(1)}, "EOVERLAP", "y overlaps weight"),
+    ("gated_linear", {"x": 0}, "EINVAL", "x is null"),
+    ("gated_linear", {"w_gate": 0}, "EINVAL", "w_gate is null"),
+    ("gated_linear", {"w_up": 0}, "EINVAL", "w_up is null"),
+    ("gated_linear", {"out": 0}, "EINVAL", "out is null"),
+    ("gated_linear", {"dtype": 2, "out_dtype": 2, "wdtype": 2}, "EINVAL", "dtype"),
+    ("gated_linear", {"dtype": 4}, "EINVAL", "dtype"),
+    ("gated_linear", {"dtype": 0, "out_dtype": 1}, "EINVAL", "out_dtype 1 is not dtype"),
+    ("gated_linear", {"dtype": 3, "out_dtype": 3}, "EINVAL", "dtype"),
+    ("gated_linear", {"dtype": 3, "out_dtype": 2}, "EINVAL", "dtype"),
+    ("gated_linear", {"dtype": 3, "wdtype": 1}, "EINVAL", "wdtype"),
+    ("gated_linear", {"dtype": 3}, "EINVAL", "8-bit x not on rows of 16 bytes"),
+    ("gated_linear", {"dtype": 3, "ldx": 16, "ldw_gate": 16, "ldw_up": 24}, "EINVAL", "8-bit w_up not on rows"),
+    ("gated_linear", {"dtype": 3, "ldx": 16, "ldw_gate": 16, "ldw_up": 16, "w_gate": _region(1) + 8}, "EINVAL", "8-bit w_gate"),
+    ("gated_linear", {"x_scale": _region(30)}, "EINVAL", "scales without 8-bit operands"),
+    ("gated_linear", {"up_scale": _region(30)}, "EINVAL", "scales without 8-bit operands"),
+    ("gated_linear", {"dtype": 3, "gate_scale": _region(30) + 2}, "EINVAL", "gate_scale not 4-byte aligned"),
+    ("gated_linear", {"act": 5}, "EINVAL", "activation"),
+    ("gated_linear", {"act": -1}, "EINVAL", "activation"),
+    ("gated_linear", {"wait_us": -1}, "EINVAL", "wait_us=-1"),
+    ("gated_linear", {"wait_us": 2000001}, "EINVAL", "wait_us=2000001"),
+    ("gated_linear", {"N": 1 << 31}, "EINVAL", "2^31"),
+    ("gated_linear", {"ldw_up": 7}, "EINVAL", "leading dimension"),
+    ("gated_linear", {"x": FAKE + 1}, "EINVAL", "aligned"),
+    ("gated_linear", {"out": _region(0)}, "EOVERLAP", "out overlaps x"),
+    ("gated_linear", {"z_gate": _region(5)}, "EOVERLAP", "z_gate overlaps out"),
+    ("gated_linear", {"z_up": _region(6)}, "EOVERLAP", "z_up overlaps z_gate"),
+    ("gated_linear", {"out": _region(4)}, "EOVERLAP", "out overlaps bias_up"),
+    ("gated_linear_bwd", {"dout": 0}, "EINVAL", "dout is null"),
+    ("gated_linear_bwd", {"z_gate": 0}, "EINVAL", "z_gate is null"),
+    ("gated_linear_bwd", {"z_up": 0}, "EINVAL", "z_up is null"),
+    ("gated_linear_bwd", {"x": 0}, "EINVAL", "x is null"),
+    ("gated_linear_bwd", {"w_up": 0}, "EINVAL", "w_up is null"),
+    ("gated_linear_bwd", {"dtype": 3, "wdtype": 3}, "EINVAL", "dtype"),
+    ("gated_linear_bwd", {"act": 7}, "EINVAL", "activation"),
+    ("gated_linear_bwd", {"wait_us": -5}, "EINVAL", "wait_us=-5"),
+    ("gated_linear_bwd", {"workspace": 0}, "EINVAL", "workspace is null"),
+    ("gated_linear_bwd", {"workspace_bytes": 16}, "EINVAL", "need"),
+    ("gated_linear_bwd", {"dx": _region(0)}, "EOVERLAP", "dx overlaps dout"),
+    ("gated_linear_bwd", {"dw_up": _region(7)}, "EOVERLAP", "dw_up overlaps dw_gate"),
+    ("gated_linear_bwd", {"workspace": _region(3)}, "EOVERLAP", "workspace overlaps x"),
 ]
 
 
@@ -164,7 +228,8 @@ def test_refusals(arx, op, change, status, words):
 
 @pytest.mark.parametrize("op,change", [
     ("rms_norm", {"rows": 0}), ("rms_norm", {"cols": 0}), ("rms_norm_bwd", {"cols": 0}), ("reduce_rms_norm", {"rows": 0}),
-    ("rms_norm_bwd", {"dx": 0, "dweight": 0})])
+    ("rms_norm_bwd", {"dx": 0, "dweight": 0}), ("gated_linear", {"M": 0}), ("gated_linear", {"N": 0}),
+    ("gated_linear_bwd", {"dx": 0, "dw_gate": 0, "dw_up": 0, "dbias_gate": 0, "dbias_up": 0})])
 def test_nothing_to_do_launches_nothing(arx, op, change):
     a = _good(arx, op)
     for k, v in change.items():
@@ -180,7 +245,13 @@ def test_nothing_to_do_launches_nothing(arx, op, change):
     ("rms_norm", {"ldq": 17, "q": _region(5) + 3}),                          # bytes at any address
     ("rms_norm_bwd", {"dx": _region(0)}), ("rms_norm_bwd", {"dx": _region(1)}), ("rms_norm_bwd", {"dx": _region(4)}),
     ("rms_norm_bwd", {"dweight": 0, "workspace": 0}), ("rms_norm_bwd", {"rows": 0}),
-    ("reduce_rms_norm", {"h": _region(0), "y": _region(20)}), ("reduce_rms_norm", {"h": 0}), ("reduce_rms_norm", {"y": 0})])
+    ("reduce_rms_norm", {"h": _region(0), "y": _region(20)}), ("reduce_rms_norm", {"h": 0}), ("reduce_rms_norm", {"y": 0}),
+    ("gated_linear", {"bias_gate": 0, "z_up": 0, "status": 0}), ("gated_linear", {"w_up": _region(1)}),
+    ("gated_linear", {"w_up": _region(1) + 16, "ldw_gate": 16, "ldw_up": 16}),
+    ("gated_linear", {"dtype": 3, "out_dtype": 1, "wdtype": 1, "ldx": 16, "ldw_gate": 16, "ldw_up": 16, "x_scale": _region(30)}),
+    ("gated_linear", {"K": 0, "x": 0, "w_gate": 0, "w_up": 0}),
+    ("gated_linear_bwd", {"dx": 0, "w_gate": 0, "w_up": 0}), ("gated_linear_bwd", {"dw_gate": 0, "dw_up": 0, "x": 0}),
+    ("gated_linear_bwd", {"dx": 0, "dw_gate": 0, "dw_up": 0, "x": 0, "w_gate": 0, "w_up": 0})])
 def test_allowed_aliases_and_omissions(arx, op, change):
     a = _good(arx, op)
     for k, v in change.items():
@@ -192,6 +263,46 @@ def test_workspace_bytes(arx):
     f = arx.arx_rms_norm_bwd_workspace_bytes
     assert f(0, 0) == 0 and f(1 << 31, 8) == 0 and f(8, 1 << 31) == 0
     assert f(1, 4096) == 4096 * 4 and f(100, 4096) < f(5000, 4096) <= f(50000, 4096)
+
+    f = arx.arx_gated_linear_bwd_workspace_bytes
+    assert f(0, 0) == 0 and f(1 << 31, 8) == 0 and f(8, 1 << 31) == 0
+    assert f(10, 13) >= 2 * (10 * 16 * 2 + 13 * 4) and f(100, 4096) < f(5000, 4096)
+
+
+@pytest.mark.parametrize("op,operand", [("gated_linear", "w_up"), ("gated_linear_bwd", "w_gate"), ("gated_linear_bwd", "x")])
+def test_copies_are_needed_and_checked(arx, op, operand):
+    """Operands whose rows are off 16 bytes: the call asks for copies and does nothing without."""
+    query, call = getattr(arx.lib, f"arx_{op}_copies_bytes"), getattr(arx.lib, f"arx_{op}")
+    a = _good(arx, op)
+    a.M, a.N, a.K = M, N, K = 1003, 204, 4100
+    for n, _ in a._fields_:
+        if n.startswith("ld"):
+            setattr(a, n, K if n in ("ldx", "ldw_gate", "ldw_up", "lddx", "lddw_gate", "lddw_up") else N)
+    if op == "gated_linear_bwd":
+        a.workspace_bytes = arx.arx_gated_linear_bwd_workspace_bytes(M, N)
+    n = query(ctypes.byref(a))
+    assert n == (M + 2 * N if op == "gated_linear" else max(2 * N, M)) * 4104 * 2
+    assert call(ctypes.byref(a), None) == arx.ARX_EINVAL and f"copies is null, {n} bytes needed" in arx.arx_last_error()
+    a.copies, a.copies_bytes = _region(40), n - 1
+    assert call(ctypes.byref(a), None) == arx.ARX_EINVAL and "copies" in arx.arx_last_error()
+    a.copies, a.copies_bytes = _region(40) + 8, n
+    assert call(ctypes.byref(a), None) == arx.ARX_EINVAL and "copies not 16-byte aligned" in arx.arx_last_error()
+    a.copies = getattr(a, operand)
+    assert call(ctypes.byref(a), None) == arx.ARX_EOVERLAP and "copies" in arx.arx_last_error()
+    for name in ("ldx", "ldw_gate", "ldw_up"):
+        setattr(a, name, 4104)
+    assert query(ctypes.byref(a)) == 0
+    a.M = 1 << 31
+    assert query(ctypes.byref(a)) == 0
+    assert query(None) == 0
+
+
+def test_one_or_two_rows_of_small_weights_need_no_copies(arx):
+    a = _good(arx, "gated_linear")
+    a.M, a.K, a.ldx, a.ldw_gate, a.ldw_up = 2, 13, 13, 13, 15
+    assert arx.lib.arx_gated_linear_copies_bytes(ctypes.byref(a)) == 0
+    a.M = 3
+    assert arx.lib.arx_gated_linear_copies_bytes(ctypes.byref(a)) == (3 + 16 + 16) * 16 * 2
 
 
 def test_binding_rejects_tensors_of_the_wrong_kind(arx):
@@ -210,3 +321,10 @@ def test_binding_rejects_tensors_of_the_wrong_kind(arx):
         arx.arx_reduce_rms_norm([], x, x)
     with pytest.raises(ValueError, match="CUDA tensor"):
         arx.arx_rms_norm_plan(x, None, q=q)
+    out = torch.zeros(4, 4, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        arx.arx_gated_linear(x, x, x, out)
+    with pytest.raises(TypeError, match="not supported"):
+        arx.arx_gated_linear(x.float(), x.float(), x.float(), out.float())
+    with pytest.raises(TypeError, match="not supported"):
+        arx.arx_gated_linear_bwd(q, q, q, q, q, q)
