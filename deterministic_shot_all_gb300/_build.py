@@ -32,11 +32,11 @@ CHECK_OBJ_DIR = os.path.join(PKG, "_build_boundscheck")
 CHECK_LIB = os.path.join(PKG, "libarx_boundscheck.so")
 
 SOURCES = ["reduce.cu", "step.cu", "abi.cu", "step_noalloc.cu", "external.cu", "ops.cu", "norm.cu",
-           "reduce_norm.cu", "dropout.cu", "linear.cu", "realign.cu", "ops_gated.cu", "rms_norm.cu", "rms_norm_bwd.cu",
+           "reduce_norm.cu", "dropout.cu", "linear.cu", "realign.cu", "ops_gated.cu", "rms_norm.cu", "rms_norm_bwd.cu", "reduce_rms_norm.cu",
            "gated.cu", "gated_grad.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("arx_device.cuh", "arx_internal.h", "arx_rows.cuh", "norm.cuh",
                                            "activation.cuh", "tensor_core.cuh", "ops_launch.h", "spans.h",
-                                           "ops_check.h", "rms_norm.cuh", "gemm.cuh", "tiles.cuh")] + [
+                                           "ops_check.h", "rms_norm.cuh", "gemm.cuh", "tiles.cuh", "pairs.cuh")] + [
     os.path.join(INCLUDE, "arx.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "arx.h"
+#include "pairs.cuh"
 
 namespace arx {
 
@@ -64,28 +65,6 @@ __device__ __forceinline__ float gelu_tanh(float z) {
 // NaN passes.  Products and sums are packed two to an instruction.  (With an
 // erf and an exponential of their own the gradient's pass was bound by
 // arithmetic: 118 us at [8185, 8192], three times the bytes' time.)
-struct Pair {
-  uint64_t v;
-};
-__device__ __forceinline__ Pair pair(float a, float b) {
-  Pair p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
-  return p;
-}
-__device__ __forceinline__ Pair pair(float a) { return pair(a, a); }
-__device__ __forceinline__ void halves(Pair p, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
-}
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
-  Pair p;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
-  return p;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair p;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return p;
-}
 // exp(-a^2 / 2) and Phi(-a) of a = |z| cut at 30.
 __device__ __forceinline__ void normal_tail(Pair a, Pair& e, Pair& tail) {
   float x, y;

@@ -1,10 +1,22 @@
-// A row of the root-mean-square norm held in registers, and its output in 8
-// bits: shared by the kernels of rms_norm.cu.
+// Root-mean-square norm, forward: h = residual + the rank-order sum of W rows
+// (one, of any type, or up to eight bf16 partials), y = h rstd weight, and q,
+// y in 8 bits with a scale for each row (rms_norm.cu, reduce_rms_norm.cu).
+//
+// Bound by HBM: each row is read once and each output written once.  A row
+// stays in its threads' registers between the pass that sums its squares and
+// the pass that uses the sum; the largest |y|, which q's scale needs, is found
+// with the sum (see row_most).
 #pragma once
 
+#include <cuda_runtime.h>
+
+#include "arx_internal.h"
 #include "norm.cuh"
+#include "ops_launch.h"
+#include "pairs.cuh"
 
 namespace arx {
+namespace {
 
 constexpr float kE4m3Most = 448.0f;                       // largest e4m3 number
 constexpr float kLeastScale = 1.1754943508222875e-38f;    // 2^-126
@@ -27,6 +39,13 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&f)[V]) {
 #pragma unroll
     for (int k = 0; k < V; ++k) p[k] = uint8_t(round_e4m3x2(f[k], 0.0f));
   }
+}
+
+// The largest magnitude of three, NaN if one is.
+__device__ __forceinline__ float most3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Magnitudes as bits: ordered as the numbers are, NaN above infinity, so that an
@@ -74,4 +93,398 @@ __device__ __forceinline__ float row_most(uint32_t m, float rstd, bool& again) {
   return p * rstd;
 }
 
+template <int D>
+struct RmsArgs {
+  using S = typename Elem<D>::S;
+  const S* slot[kMaxW];
+  const S* residual;
+  const void* weight;
+  S *h, *y;
+  uint8_t* q;
+  float *scale, *rstd;
+  uint64_t rows, cols, ldx, ldresidual, ldh, ldy, ldq;
+  float eps, inv_cols;
+  int wdtype, W;
+};
+
+// The terms of h at the V columns from c on of a row, and their sum before its
+// rounding.
+template <int D, int W, int V>
+struct Terms {
+  Pack<D, V> p[W], r;
+  __device__ __forceinline__ void load(const RmsArgs<D>& a, size_t row, size_t c) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) p[w].load(a.slot[w] + row * a.ldx + c);
+    if (a.residual) r.load(a.residual + row * a.ldresidual + c);
+  }
+  __device__ __forceinline__ void sum(const RmsArgs<D>& a, float (&f)[V]) const {
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      p[w].get(v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] = __fadd_rn(f[k], v[k]);
+    }
+    if (a.residual) {
+      r.get(v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] += v[k];
+    }
+  }
+};
+template <int D, int W, int V>
+__device__ __forceinline__ void load_sum(const RmsArgs<D>& a, size_t row, size_t c, float (&f)[V]) {
+  Terms<D, W, V> t;
+  t.load(a, row, c);
+  t.sum(a, f);
+}
+
+// Two elements to an instruction, where registers in pairs cost nothing (32-bit
+// rows of 1024 threads spilled with them: 608 rows of 8192, 13.1 us against 9.6).
+template <int D, int V>
+constexpr bool kPairs = V == 8 && D != ARX_F32;
+
+template <int D, int NV, int V>
+__device__ __forceinline__ void scale_row(float (&f)[NV][V], float by) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < V; k += kPairs<D, V> ? 2 : 1) {
+      if constexpr (kPairs<D, V>)
+        halves(pair(f[i][k], f[i][k + 1]) * pair(by), f[i][k], f[i][k + 1]);
+      else
+        f[i][k] *= by;
+    }
+}
+
+template <int D, int T, int NV, int V>
+__device__ __forceinline__ void store_row(typename Elem<D>::S* p, uint32_t cols, const float (&f)[NV][V]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t c = row_col<T, V>(i);
+    Pack<D, V> o;
+    o.set(f[i]);
+    if (c < cols) o.store(p + c);
+  }
+}
+
+// The rest of a row whose h is in `f` (columns past the end hold 0) and whose
+// weights are in `g`.  `buf`: 4 T / 32 words of the row's shared memory.
+template <int D, int T, int RPC, int NV, int V>
+__device__ __forceinline__ void finish_row(const RmsArgs<D>& a, size_t row, uint32_t cols, float (&f)[NV][V],
+                                           const float (&g)[NV][V], float* buf) {
+  float s = 0.0f, most = 0.0f;
+  if constexpr (kPairs<D, V>) {
+    Pair sum = pair(0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        const Pair v = pair(f[i][k], f[i][k + 1]);
+        sum = fma2(v, v, sum);
+      }
+    float other;
+    halves(sum, s, other);
+    s += other;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) s += f[i][k] * f[i][k];
+  }
+  if (a.q) {
+#pragma unroll
+    for (int i = 0; i < NV * V; i += 2) {
+      const int j = i + 1 < NV * V ? i + 1 : i;
+      most = most3(most, f[i / V][i % V] * g[i / V][i % V], f[j / V][j % V] * g[j / V][j % V]);
+    }
+  }
+  uint32_t m = __float_as_uint(most);  // not negative
+  if (a.h) store_row<D, T, NV, V>(a.h + row * a.ldh, cols, f);
+  row_sum_max<T, RPC>(s, m, buf);
+  const float rstd = 1.0f / sqrtf(s * a.inv_cols + a.eps);
+  scale_row<D, NV, V>(f, rstd);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < V; k += kPairs<D, V> ? 2 : 1) {
+      if constexpr (kPairs<D, V>)
+        halves(pair(f[i][k], f[i][k + 1]) * pair(g[i][k], g[i][k + 1]), f[i][k], f[i][k + 1]);
+      else
+        f[i][k] *= g[i][k];
+    }
+  float scale = 0.0f;
+  if (a.q) {
+    bool again;
+    most = row_most(m, rstd, again);
+    if (again) {
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (row_col<T, V>(i) < cols)
+#pragma unroll
+          for (int k = 0; k < V; ++k) m = max(m, magnitude(f[i][k]));
+      row_sum_max<T, RPC>(s, m, buf + 2 * (T / 32));
+      most = __uint_as_float(m);
+    }
+    if (a.y) store_row<D, T, NV, V>(a.y + row * a.ldy, cols, f);
+    float inverse;
+    scale = row_scale(most, inverse);
+    scale_row<D, NV, V>(f, inverse);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t c = row_col<T, V>(i);
+      if (c < cols) store_e4m3<V>(a.q + row * a.ldq + c, f[i]);
+    }
+  } else {
+    store_row<D, T, NV, V>(a.y + row * a.ldy, cols, f);
+  }
+  if (threadIdx.x % T == 0) {
+    if (a.q) a.scale[row] = scale;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+}
+
+// Few rows: one block (or a warp of one) to a row, the fewer columns to a
+// thread the sooner it ends.
+template <int D, int W, int T, int RPC, int NV, int V>
+__global__ void __launch_bounds__(T* RPC) rms_kernel(const __grid_constant__ RmsArgs<D> a) {
+  __shared__ float buf[RPC][4 * (T / 32)];
+  dependent_launch_prologue();
+  const size_t row = size_t(blockIdx.x) * RPC + threadIdx.x / T;
+  if (RPC > 1 && row >= a.rows) return;  // whole warps; RPC > 1 has one warp per row and no barrier
+  const uint32_t cols = uint32_t(a.cols);
+  float f[NV][V], g[NV][V];
+  // Units whose loads are in flight together.
+  constexpr int kWords = (T > 512 ? 20 : 40) / (W + 1), kGroup = V == 8 ? 1 : kWords < 8 ? kWords : 8;
+#pragma unroll
+  for (int i0 = 0; i0 < NV; i0 += kGroup) {
+    Terms<D, W, V> t[kGroup];
+#pragma unroll
+    for (int i = i0; i < i0 + kGroup && i < NV; ++i)
+      if (row_col<T, V>(i) < cols) t[i - i0].load(a, row, row_col<T, V>(i));
+#pragma unroll
+    for (int i = i0; i < i0 + kGroup && i < NV; ++i) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[i][k] = 0.0f;
+      if (row_col<T, V>(i) < cols) t[i - i0].sum(a, f[i]);
+    }
+  }
+  hold_params<T, NV, V>(g, a.weight, a.wdtype, cols, 1.0f);
+  finish_row<D, T, 1, NV, V>(a, row, cols, f, g, buf[threadIdx.x / T]);
+}
+
+// Many rows of whole aligned units: persistent, the weights in registers and the
+// rows coming in through a ring of kRing rows in shared memory, each thread
+// copying what it reads itself.
+template <int T, int RPC>
+constexpr int kRingBlocks = T * RPC > 512 ? 1 : 2;
+
+template <int D, int T, int RPC, int NV, int kRing>
+__global__ void __launch_bounds__(T* RPC, kRingBlocks<T, RPC>)
+    rms_ring_kernel(const __grid_constant__ RmsArgs<D> a, uint32_t slot) {
+  using S = typename Elem<D>::S;
+  constexpr int V = 8;
+  __shared__ float buf[2][RPC][4 * (T / 32)];
+  extern __shared__ __align__(16) uint8_t smem[];  // [RPC][kRing][slots, residual][slot]
+  dependent_launch_prologue();
+  const uint32_t cols = uint32_t(a.cols), sub = threadIdx.x / T, W = a.W, arrays = W + (a.residual ? 1 : 0);
+  uint8_t* ring = smem + sub * kRing * arrays * slot;
+  const size_t step = size_t(gridDim.x) * RPC;
+  size_t row = size_t(blockIdx.x) * RPC + sub;
+  const auto start = [&](size_t r, uint32_t at) {  // one group, empty past the last row
+    if (r < a.rows) {
+      uint8_t* dst = ring + at * arrays * slot;
+      for (uint32_t w = 0; w < W; ++w) copy_matrix_row<D, T, NV, V>(dst + w * slot, a.slot[w], a.ldx, r, a.rows, cols);
+      if (a.residual) copy_matrix_row<D, T, NV, V>(dst + W * slot, a.residual, a.ldresidual, r, a.rows, cols);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i + 1 < kRing; ++i) start(row + i * step, i);
+  float g[NV][V];
+  hold_params<T, NV, V>(g, a.weight, a.wdtype, cols, 1.0f);
+  uint32_t at = 0;
+  int parity = 0;
+  for (; row < a.rows; row += step) {
+    cp_async_wait<kRing - 2>();
+    const uint8_t* base = ring + at * arrays * slot;
+    float f[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t c = row_col<T, V>(i);
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[i][k] = 0.0f;
+      if (c >= cols) continue;
+      float v[V];
+#pragma unroll 4
+      for (uint32_t w = 0; w < W; ++w) {
+        read_shared<D, V>(base + w * slot + c * sizeof(S), v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[i][k] = __fadd_rn(f[i][k], v[k]);
+      }
+      if (a.residual) {
+        read_shared<D, V>(base + W * slot + c * sizeof(S), v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[i][k] += v[k];
+      }
+    }
+    // The slot of the row before, which this thread has read.
+    start(row + (kRing - 1) * step, at == 0 ? kRing - 1 : at - 1);
+    finish_row<D, T, RPC, NV, V>(a, row, cols, f, g, buf[parity][sub]);
+    parity ^= 1;
+    at = at + 1 == kRing ? 0 : at + 1;
+  }
+  cp_async_wait<0>();
+}
+
+// Any row length: one block per row, h computed anew in each pass and stored,
+// with y and q, in the last, after its element's last read.
+template <int D, int W>
+__global__ void __launch_bounds__(512) rms_long_kernel(const __grid_constant__ RmsArgs<D> a) {
+  __shared__ float buf[2][32];
+  dependent_launch_prologue();
+  const size_t row = blockIdx.x;
+  float s = 0.0f;
+  uint32_t m = 0;
+  for (size_t c = threadIdx.x; c < a.cols; c += 512) {
+    float h[1];
+    load_sum<D, W, 1>(a, row, c, h);
+    s += h[0] * h[0];
+    if (a.q) m = max(m, magnitude(a.weight ? h[0] * load_param(a.weight, a.wdtype, c) : h[0]));
+  }
+  row_sum_max<512, 1>(s, m, buf[0]);
+  const float rstd = 1.0f / sqrtf(s / float(a.cols) + a.eps);
+  float inverse = 0.0f;
+  if (a.q) {
+    bool again;
+    float most = row_most(m, rstd, again);
+    if (again) {
+      m = 0;
+      for (size_t c = threadIdx.x; c < a.cols; c += 512) {
+        float h[1];
+        load_sum<D, W, 1>(a, row, c, h);
+        m = max(m, magnitude(a.weight ? h[0] * rstd * load_param(a.weight, a.wdtype, c) : h[0] * rstd));
+      }
+      row_sum_max<512, 1>(s, m, buf[1]);
+      most = __uint_as_float(m);
+    }
+    const float scale = row_scale(most, inverse);
+    if (threadIdx.x == 0) a.scale[row] = scale;
+  }
+  if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+  for (size_t c = threadIdx.x; c < a.cols; c += 512) {
+    float h[1];
+    load_sum<D, W, 1>(a, row, c, h);
+    float v = h[0] * rstd;
+    if (a.weight) v *= load_param(a.weight, a.wdtype, c);
+    if (a.h) a.h[row * a.ldh + c] = Elem<D>::round(h[0]);
+    if (a.y) a.y[row * a.ldy + c] = Elem<D>::round(v);
+    if (a.q) a.q[row * a.ldq + c] = uint8_t(round_e4m3x2(v * inverse, 0.0f));
+  }
+}
+
+template <int D, int W, int T, int RPC, int NV, int V>
+cudaError_t run(const RmsArgs<D>& a, cudaStream_t st) {
+  return launch_op(rms_kernel<D, W, T, RPC, NV, V>, dim3(unsigned((a.rows + RPC - 1) / RPC)), T * RPC, 0, st, a);
+}
+
+// Shared memory of an SM that its blocks' rings may fill, and of one block.
+constexpr size_t kRingBytes = 222 * 1024, kBlockRingBytes = 220 * 1024;
+constexpr unsigned kSms = 152;
+
+// Four rows in the ring, two where four are too large; *done is false where two
+// are as well.
+template <int D, int T, int RPC, int NV>
+cudaError_t run_ring(const RmsArgs<D>& a, bool* done, cudaStream_t st) {
+  const size_t row = size_t(row_slot(a.cols, sizeof(typename Elem<D>::S), 8)) * (a.W + (a.residual ? 1 : 0)) * RPC;
+  const auto with = [&](auto rows) {
+    constexpr int kRing = decltype(rows)::value;
+    const size_t smem = kRing * row;
+    size_t per_sm = kRingBytes / (smem + 2048);
+    if (per_sm > kRingBlocks<T, RPC>) per_sm = kRingBlocks<T, RPC>;
+    const uint64_t need = (a.rows + RPC - 1) / RPC, most = per_sm * kSms;
+    constexpr auto kernel = rms_ring_kernel<D, T, RPC, NV, kRing>;
+    const cudaError_t e = allow_dynamic_smem<kernel>(kBlockRingBytes);
+    if (e != cudaSuccess) return e;
+    return launch_op(kernel, dim3(unsigned(need < most ? need : most)), T * RPC, smem, st, a,
+                     row_slot(a.cols, sizeof(typename Elem<D>::S), 8));
+  };
+  *done = true;
+  if (4 * row <= kBlockRingBytes) return with(std::integral_constant<int, 4>{});
+  if (2 * row <= kBlockRingBytes) return with(std::integral_constant<int, 2>{});
+  *done = false;
+  return cudaSuccess;
+}
+
+// One block to a row or the ring?  Measured, GPU time in microseconds (16-bit rows
+// with residual and y, 32-bit weights; one row to a block, then the ring):
+//   aligned        152 rows       608          2,432        8,192
+//   2048 columns   1.7  2.1     3.0  3.0     8.1  8.7    23.5  22.4
+//   4096           2.0  2.2     4.5  4.5    16.1 15.3    46.7  43.8
+//   5120           2.3  2.4     5.0  6.0    21.8 20.7
+//   8192           3.0  3.3     9.0 10.4    33.0 31.4
+//   12288          3.7  4.3    17.2 14.6    64.3 45.6
+// 32-bit rows of 4096 columns and more gain 9 to 13 % from 2,432 rows on; sums of 3
+// and 4 ranks above 4096 columns 5 to 11 %, at 4096 none (4 ranks, 1,024 rows of 8192:
+// 22.4 against 19.1); with q, whose largest |y|
+// takes issue slots, the ring costs 1 to 14 %.  Rows off 16 bytes, read element
+// by element, took 1.1 to 2 times as long through it.
+// The threads to a row: 640 up to 5120 columns (1024: 2,432 rows of 5120, 34.7 us
+// against 21.8); above, 512 with two units each (1024: 41.7 against 33.0 at 8192,
+// 152 rows alike), but 1024 for 32-bit rows (31.3 against 45.8 us).  A warp to rows
+// of up to 512 columns from 1,217 on (10,000 rows: 11.7 against 8.2 us, 608: 1.85
+// alike).  Off 16 bytes and above 5120 columns, 512 threads for one and two ranks
+// from 305 rows on (8191: 2,432 rows 42 against 56 us, 152: 3.9 against 3.6), else
+// 1024 (4 ranks 1.7 times as long with 512); up to 16384 columns 1024 up to 304 rows
+// (152 rows of 12001: 5.3 against 10.3 us), above, two passes over the row are as fast.
+template <int D, int W>
+cudaError_t run_w(const RmsArgs<D>& a, bool vec, cudaStream_t st) {
+  const uint64_t n = a.cols;
+  if (vec) {
+    const bool ring = a.rows >= 16 * kSms && !a.q;
+    bool done = false;
+    cudaError_t e = cudaSuccess;
+    if (n <= 256) return run<D, W, 32, 4, 1, 8>(a, st);
+    if (n <= 512 && a.rows > 8 * kSms) return run<D, W, 32, 4, 2, 8>(a, st);
+    if (n <= 1024) return run<D, W, 128, 1, 1, 8>(a, st);
+    if (n <= 2048) return run<D, W, 256, 1, 1, 8>(a, st);
+    if (n <= 4096) {
+      if (ring && W <= 2) e = run_ring<D, 512, 1, 1>(a, &done, st);
+      return e != cudaSuccess || done ? e : run<D, W, 512, 1, 1, 8>(a, st);
+    }
+    if (n <= 5120) {
+      if (ring && W <= 4) e = run_ring<D, 640, 1, 1>(a, &done, st);
+      return e != cudaSuccess || done ? e : run<D, W, 640, 1, 1, 8>(a, st);
+    }
+    if (n <= 8192) {
+      if ((W > 2 ? a.rows >= 5 * kSms && !a.q : ring) && W <= 4) e = run_ring<D, 1024, 1, 1>(a, &done, st);
+      if (e != cudaSuccess || done) return e;
+      if constexpr (D == ARX_F32) return run<D, W, 1024, 1, 1, 8>(a, st);
+      return run<D, W, 512, 1, 2, 8>(a, st);
+    }
+    if (n <= 16384) {
+      if (a.rows > 2 * kSms && W <= 2) e = run_ring<D, 1024, 1, 2>(a, &done, st);
+      if (e != cudaSuccess || done) return e;
+      if constexpr (W > 2) return run<D, W, 1024, 1, 2, 8>(a, st);
+      return run<D, W, 512, 1, 4, 8>(a, st);
+    }
+  } else {
+    if (n <= 256) return run<D, W, 32, 4, 8, 1>(a, st);
+    if (n <= 512 && a.rows > 8 * kSms) return run<D, W, 64, 1, 8, 1>(a, st);
+    if (n <= 1024) return run<D, W, 128, 1, 8, 1>(a, st);
+    if (n <= 2048) return run<D, W, 256, 1, 8, 1>(a, st);
+    if (n <= 4096) return run<D, W, 512, 1, 8, 1>(a, st);
+    if (n <= 5120) return run<D, W, 640, 1, 8, 1>(a, st);
+    if constexpr (W <= 2)
+      if (n <= 8192 && a.rows > 2 * kSms) return run<D, W, 512, 1, 16, 1>(a, st);
+    if (n <= 8192) return run<D, W, 1024, 1, 8, 1>(a, st);
+    if (n <= 16384 && a.rows <= 2 * kSms) return run<D, W, 1024, 1, 16, 1>(a, st);
+  }
+  return launch_op(rms_long_kernel<D, W>, dim3(unsigned(a.rows)), 512, 0, st, a);
+}
+
+}  // namespace
 }  // namespace arx
