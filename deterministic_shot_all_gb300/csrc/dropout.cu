@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) act_grad_kernel(con
 // out[c] = sum over i < parts of p[i][c]: 32 columns per block, 32 lanes of
 // partial rows, each added in order and then joined in order.
 constexpr unsigned kSumLanes = 32;
+constexpr unsigned kSumBatch = 10;  // loads in flight: the 304 parts of two blocks to an SM at once
 __global__ void __launch_bounds__(32 * kSumLanes) column_sum_kernel(const float* p0, void* out0, const float* p1,
                                                                     void* out1, unsigned parts, uint64_t cols,
                                                                     int dtype) {
@@ -169,8 +170,15 @@ __global__ void __launch_bounds__(32 * kSumLanes) column_sum_kernel(const float*
   const size_t c = size_t(blockIdx.x) * 32 + tx;
   float s = 0.0f;
   if (c < cols) {
-#pragma unroll 4
-    for (unsigned i = ty; i < parts; i += kSumLanes) s += p[size_t(i) * cols + c];
+    for (unsigned i0 = ty; i0 < parts; i0 += kSumBatch * kSumLanes) {
+      float v[kSumBatch];
+#pragma unroll
+      for (unsigned k = 0; k < kSumBatch; ++k)
+        if (i0 + k * kSumLanes < parts) v[k] = p[size_t(i0 + k * kSumLanes) * cols + c];
+#pragma unroll
+      for (unsigned k = 0; k < kSumBatch; ++k)
+        if (i0 + k * kSumLanes < parts) s += v[k];
+    }
   }
   join[ty][tx] = s;
   __syncthreads();

@@ -19,15 +19,15 @@ namespace {
 
 constexpr unsigned kSms = 152;
 
-template <int T, int RPC>
-constexpr int kBlocks = T * RPC > 256 ? 1 : 2;
+template <int T, int RPC, int NV, int V>
+constexpr int kBlocks = T * RPC <= 256 || (T == 512 && NV * V == 8) ? 2 : 1;
 
 template <int D, int T, int RPC, int NV, int V, int kRing>
-__global__ void __launch_bounds__(T* RPC, kBlocks<T, RPC>)
+__global__ void __launch_bounds__(T* RPC, kBlocks<T, RPC, NV, V>)
     rms_bwd_kernel(const __grid_constant__ arx_rms_norm_bwd_args a, uint32_t slot, float inv_cols) {
   using S = typename Elem<D>::S;
   constexpr int kWarps = T / 32;
-  constexpr bool kHold = NV * V <= 16 && T <= 512;  // the weights, n and v stay in registers
+  constexpr bool kHold = NV * V <= (T <= 512 ? 16 : 8);  // the weights, n and v stay in registers
   __shared__ float buf[2][RPC][kWarps];
   extern __shared__ __align__(16) uint8_t smem[];  // [RPC][kRing][h, dy, dresidual][slot]
   dependent_launch_prologue();
@@ -197,7 +197,7 @@ constexpr unsigned kColumnChunks = 64;
 template <int D, int T, int RPC, int NV, int V, int kRing>
 cudaError_t ring(const arx_rms_norm_bwd_args& a, unsigned* parts, uint32_t slot, size_t smem, cudaStream_t st) {
   size_t per_sm = kRingBytes / (smem + 2048);
-  if (per_sm > kBlocks<T, RPC>) per_sm = kBlocks<T, RPC>;
+  if (per_sm > kBlocks<T, RPC, NV, V>) per_sm = kBlocks<T, RPC, NV, V>;
   if (per_sm < 1) per_sm = 1;
   const uint64_t need = (a.rows + RPC - 1) / RPC;
   const unsigned blocks = unsigned(need < per_sm * kSms ? need : per_sm * kSms);
@@ -221,6 +221,10 @@ cudaError_t run(const arx_rms_norm_bwd_args& a, unsigned* parts, bool* done, cud
                                     : ring<D, T, RPC, NV, V, 2>(a, parts, slot, 2 * row, st);
 }
 
+// 512 threads to 16-bit rows of 2049 to 4096 columns, whose rings leave room for two
+// blocks on an SM ([8192, 4096] with dresidual: 46.0 us against 47.0 with 256 threads;
+// with 256 and two rows in the ring of three blocks 54.6); 640 to rows of 4097 to
+// 5120 columns off 16 bytes ([3001, 5003] in 32 bits: 36.0 against 37.4 with 320).
 template <int D>
 cudaError_t any(const arx_rms_norm_bwd_args& a, bool vec, unsigned* parts, cudaStream_t st) {
   const uint64_t n = a.cols;
@@ -235,6 +239,8 @@ cudaError_t any(const arx_rms_norm_bwd_args& a, bool vec, unsigned* parts, cudaS
       e = run<D, 64, 4, 2, 8>(a, parts, &done, st);
     else if (n <= 2048)
       e = run<D, 128, 2, 2, 8>(a, parts, &done, st);
+    else if (n <= 4096 && D != ARX_F32)
+      e = run<D, 512, 1, 1, 8>(a, parts, &done, st);
     else if (n <= 4096)
       e = run<D, 256, 1, 2, 8>(a, parts, &done, st);
     else if (n <= 8192)
@@ -255,7 +261,7 @@ cudaError_t any(const arx_rms_norm_bwd_args& a, bool vec, unsigned* parts, cudaS
     else if (n <= 4096)
       e = run<D, 256, 1, 16, 1>(a, parts, &done, st);
     else if (n <= 5120)
-      e = run<D, 320, 1, 16, 1>(a, parts, &done, st);
+      e = run<D, 640, 1, 8, 1>(a, parts, &done, st);
     else if (n <= 8192)
       e = run<D, 512, 1, 16, 1>(a, parts, &done, st);
     else if (n <= 16384)
