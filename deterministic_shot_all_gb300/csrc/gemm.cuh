@@ -187,10 +187,6 @@ __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint
   return true;
 }
 
-__device__ __forceinline__ void prefetch_l2_line(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" :: "l"(p));
-}
-
 // Loads of the residual, zero without `on`: predicated, as a load inside a
 // branch is waited for where the branch ends, and volatile, so that they stay
 // ahead of what they are to overlap with.

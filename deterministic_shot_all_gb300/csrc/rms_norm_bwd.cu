@@ -22,18 +22,27 @@ constexpr unsigned kSms = 152;
 template <int T, int RPC, int NV, int V>
 constexpr int kBlocks = T * RPC <= 256 || (T == 512 && NV * V == 8) ? 2 : 1;
 
+// Weights and n stay in registers, beside v; else n is worked out twice and the
+// weights come from shared memory, [cols] behind the rings, if there is room, or
+// from L1; and where two rows of three arrays have no room, dresidual does not come
+// through the ring.  ([2432, 12288] bf16 with dresidual: 72.5 us with all of it
+// from L1 and worked out twice.)
+template <int T, int NV, int V>
+constexpr bool kHolds = NV * V <= (T <= 512 ? 16 : 8);
+
 template <int D, int T, int RPC, int NV, int V, int kRing>
 __global__ void __launch_bounds__(T* RPC, kBlocks<T, RPC, NV, V>)
-    rms_bwd_kernel(const __grid_constant__ arx_rms_norm_bwd_args a, uint32_t slot, float inv_cols) {
+    rms_bwd_kernel(const __grid_constant__ arx_rms_norm_bwd_args a, uint32_t slot, float inv_cols, uint32_t res_ring,
+                   uint32_t weights) {
   using S = typename Elem<D>::S;
   constexpr int kWarps = T / 32;
-  constexpr bool kHold = NV * V <= (T <= 512 ? 16 : 8);  // the weights, n and v stay in registers
+  constexpr bool kHold = kHolds<T, NV, V>;
   __shared__ float buf[2][RPC][kWarps];
-  extern __shared__ __align__(16) uint8_t smem[];  // [RPC][kRing][h, dy, dresidual][slot]
+  extern __shared__ __align__(16) uint8_t smem[];  // [RPC][kRing][h, dy and, with res_ring, dresidual][slot]
   dependent_launch_prologue();
   const uint32_t cols = uint32_t(a.cols);
   const bool res = a.dresidual && a.dx;
-  const uint32_t arrays = res ? 3 : 2, sub = threadIdx.x / T;
+  const uint32_t arrays = res_ring ? 3 : 2, sub = threadIdx.x / T;
   uint8_t* ring = smem + sub * kRing * arrays * slot;
   const S *gh = static_cast<const S*>(a.h), *gdy = static_cast<const S*>(a.dy),
           *gdr = static_cast<const S*>(a.dresidual);
@@ -43,9 +52,12 @@ __global__ void __launch_bounds__(T* RPC, kBlocks<T, RPC, NV, V>)
       uint8_t* dst = ring + at * arrays * slot;
       copy_matrix_row<D, T, NV, V>(dst, gh, a.ldh, row, a.rows, cols);
       copy_matrix_row<D, T, NV, V>(dst + slot, gdy, a.lddy, row, a.rows, cols);
-      if (res) copy_matrix_row<D, T, NV, V>(dst + 2 * slot, gdr, a.lddresidual, row, a.rows, cols);
+      if (res_ring) copy_matrix_row<D, T, NV, V>(dst + 2 * slot, gdr, a.lddresidual, row, a.rows, cols);
     }
     cp_async_commit();
+    // A dresidual that has no room in the ring is on its way to L2 at least.
+    if (!kHold && res && !res_ring && row < a.rows)
+      for (uint32_t c = threadIdx.x % T * (128 / sizeof(S)); c < cols; c += T * (128 / sizeof(S))) prefetch_l2_line(gdr + row * a.lddresidual + c);
   };
 
   float acc[NV][V] = {}, w[kHold ? NV : 1][V];
@@ -54,6 +66,21 @@ __global__ void __launch_bounds__(T* RPC, kBlocks<T, RPC, NV, V>)
 #pragma unroll
   for (int i = 0; i + 1 < kRing; ++i) start(row + i * step, i);
   if constexpr (kHold) hold_params<T, NV, V>(w, a.weight, a.wdtype, cols, 1.0f);
+  float* held = nullptr;  // of a block with one row at a time
+  if constexpr (!kHold)
+    if (weights && a.weight) {
+      held = reinterpret_cast<float*>(smem + kRing * arrays * slot);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t c = row_col<T, V>(i);
+        float g[V];
+        if (c < cols) {
+          load_params<V>(a.weight, a.wdtype, c, g);
+#pragma unroll
+          for (int k = 0; k < V; ++k) held[c + k] = g[k];  // this thread's own columns: no barrier
+        }
+      }
+    }
   float rstd = row < a.rows ? a.rstd[row] : 0.0f;
   uint32_t at = 0;
   int parity = 0;
@@ -67,29 +94,29 @@ __global__ void __launch_bounds__(T* RPC, kBlocks<T, RPC, NV, V>)
     const uint8_t* h = base + row_offset<V>(gh + row * a.ldh);
     const uint8_t* dy = base + slot + row_offset<V>(gdy + row * a.lddy);
     const uint8_t* dr = base + 2 * slot + row_offset<V>(gdr + row * a.lddresidual);
-    float n[kHold ? NV : 1][V], v[kHold ? NV : 1][V], sum = 0.0f;
-    // Unit i's n and v; the first pass also adds up.
-    const auto unit = [&](int i, uint32_t c, float (&un)[V], float (&uv)[V], bool first) {
+    float n[kHold ? NV : 1][V], v[NV][V], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t c = row_col<T, V>(i);
+      if (c >= cols) continue;
+      float (&un)[V] = n[kHold ? i : 0], (&uv)[V] = v[i], g[V];
       read_shared<D, V>(h + c * sizeof(S), un);
       read_shared<D, V>(dy + c * sizeof(S), uv);
-      float g[V];
       if constexpr (!kHold) {
 #pragma unroll
         for (int k = 0; k < V; ++k) g[k] = 1.0f;
-        if (a.weight) load_params<V>(a.weight, a.wdtype, c, g);
+        if (held)
+          read_shared<ARX_F32, V>(reinterpret_cast<const uint8_t*>(held + c), g);
+        else if (a.weight)
+          load_params<V>(a.weight, a.wdtype, c, g);
       }
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         un[k] *= rstd;
-        if (first) acc[i][k] += uv[k] * un[k];
+        acc[i][k] += uv[k] * un[k];
         uv[k] *= kHold ? w[kHold ? i : 0][k] : g[k];
-        if (first) sum += uv[k] * un[k];
+        sum += uv[k] * un[k];
       }
-    };
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint32_t c = row_col<T, V>(i);
-      if (c < cols) unit(i, c, n[kHold ? i : 0], v[kHold ? i : 0], true);
     }
     if (a.dx) {
       const float mean = row_sum<T, RPC>(sum, buf[parity][sub]) * inv_cols;
@@ -99,13 +126,23 @@ __global__ void __launch_bounds__(T* RPC, kBlocks<T, RPC, NV, V>)
       for (int i = 0; i < NV; ++i) {
         const uint32_t c = row_col<T, V>(i);
         if (c >= cols) continue;
-        float (&un)[V] = n[kHold ? i : 0], (&uv)[V] = v[kHold ? i : 0], o[V];
-        if constexpr (!kHold) unit(i, c, un, uv, false);
+        float (&un)[V] = n[kHold ? i : 0], o[V];
+        if constexpr (!kHold) {
+          read_shared<D, V>(h + c * sizeof(S), un);
+#pragma unroll
+          for (int k = 0; k < V; ++k) un[k] *= rstd;
+        }
 #pragma unroll
         for (int k = 0; k < V; ++k) o[k] = 0.0f;
-        if (res) read_shared<D, V>(dr + c * sizeof(S), o);
+        if (res_ring) {
+          read_shared<D, V>(dr + c * sizeof(S), o);
+        } else if (!kHold && res) {
+          Pack<D, V> r;
+          r.load(gdr + row * a.lddresidual + c);
+          r.get(o);
+        }
 #pragma unroll
-        for (int k = 0; k < V; ++k) o[k] += rstd * (uv[k] - un[k] * mean);
+        for (int k = 0; k < V; ++k) o[k] += rstd * (v[i][k] - un[k] * mean);
         Pack<D, V> out;
         out.set(o);
         out.store(dx + c);
@@ -122,9 +159,14 @@ __global__ void __launch_bounds__(T* RPC, kBlocks<T, RPC, NV, V>)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const uint32_t c = row_col<T, V>(i);
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (c < cols) (RPC > 1 ? join + sub * cols : to)[c + k] = acc[i][k];
+    float* p = (RPC > 1 ? join + sub * cols : to) + c;
+    if (c >= cols) continue;
+    if constexpr (V == 8) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    } else {
+      p[0] = acc[i][0];
+    }
   }
   if constexpr (RPC > 1) {
     __syncthreads();
@@ -195,7 +237,11 @@ constexpr unsigned kColumnChunks = 64;
 // As many blocks as 152 SMs hold at once: a constant, so that the order of the
 // sums depends on the sizes alone.
 template <int D, int T, int RPC, int NV, int V, int kRing>
-cudaError_t ring(const arx_rms_norm_bwd_args& a, unsigned* parts, uint32_t slot, size_t smem, cudaStream_t st) {
+cudaError_t ring(const arx_rms_norm_bwd_args& a, unsigned* parts, uint32_t slot, bool res_ring, cudaStream_t st) {
+  size_t smem = size_t(kRing) * (res_ring ? 3 : 2) * slot * RPC;
+  const size_t params = RPC == 1 && a.weight ? a.cols * 4 : 0;
+  const bool weights = params && smem + params <= kBlockRingBytes && !kHolds<T, NV, V>;
+  if (weights) smem += params;
   size_t per_sm = kRingBytes / (smem + 2048);
   if (per_sm > kBlocks<T, RPC, NV, V>) per_sm = kBlocks<T, RPC, NV, V>;
   if (per_sm < 1) per_sm = 1;
@@ -205,20 +251,25 @@ cudaError_t ring(const arx_rms_norm_bwd_args& a, unsigned* parts, uint32_t slot,
   constexpr auto kernel = rms_bwd_kernel<D, T, RPC, NV, V, kRing>;
   const cudaError_t e = allow_dynamic_smem<kernel>(kBlockRingBytes);
   if (e != cudaSuccess) return e;
-  return launch_op(kernel, dim3(blocks), T * RPC, smem, st, a, slot, 1.0f / float(a.cols));
+  return launch_op(kernel, dim3(blocks), T * RPC, smem, st, a, slot, 1.0f / float(a.cols), uint32_t(res_ring),
+                   uint32_t(weights));
 }
 
-// Three rows in the ring, two where three are too large; *done is false where
-// two are as well.
+// Three rows in the ring, two where three are too large, of the longest rows
+// without dresidual; *done is false where two are too large as well.
 template <int D, int T, int RPC, int NV, int V>
 cudaError_t run(const arx_rms_norm_bwd_args& a, unsigned* parts, bool* done, cudaStream_t st) {
   const uint32_t slot = row_slot(a.cols, sizeof(typename Elem<D>::S), V);
-  const size_t row = size_t(a.dresidual && a.dx ? 3 : 2) * slot * RPC;
+  const bool res = a.dresidual && a.dx;
+  const size_t row = size_t(res ? 3 : 2) * slot * RPC;
+  *done = true;
   // (Two rows of two arrays hold the RPC rows of sums, too.)
-  *done = 2 * row <= kBlockRingBytes;
-  if (!*done) return cudaSuccess;
-  return 3 * row <= kBlockRingBytes ? ring<D, T, RPC, NV, V, 3>(a, parts, slot, 3 * row, st)
-                                    : ring<D, T, RPC, NV, V, 2>(a, parts, slot, 2 * row, st);
+  if (3 * row <= kBlockRingBytes) return ring<D, T, RPC, NV, V, 3>(a, parts, slot, res, st);
+  if (2 * row <= kBlockRingBytes) return ring<D, T, RPC, NV, V, 2>(a, parts, slot, res, st);
+  if constexpr (!kHolds<T, NV, V>)
+    if (size_t(4) * slot <= kBlockRingBytes) return ring<D, T, RPC, NV, V, 2>(a, parts, slot, false, st);
+  *done = false;
+  return cudaSuccess;
 }
 
 // 512 threads to 16-bit rows of 2049 to 4096 columns, whose rings leave room for two
