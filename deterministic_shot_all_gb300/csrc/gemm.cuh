@@ -61,6 +61,9 @@ struct GemmArgs {
   uint32_t split;      // blocks of a cluster that share a tile's contraction
   uint32_t whole, pieces;  // wide form: tiles that are one piece, and pieces in all
   uint32_t tiles_p, tiles_q;
+  uint32_t tiles_first;  // of the first of two stacked products
+  uint16_t* out2;        // the second's output
+  uint64_t ldout2;
   uint32_t idesc, tmem_columns;
   uint32_t quads, octets;  // out, z and residual allow accesses of 4 elements; of 8, bias and width too
 };
@@ -114,15 +117,41 @@ __device__ __forceinline__ void copy_operand(uint32_t dst, const CUtensorMap* ma
 
 // ---- the roles, for one tile -------------------------------------------------------
 
-// The maps of a second pair of operands, whose product joins the first's in one
-// sum (dx of a gated block): the contraction runs over the first pair, then over
-// the second.
-template <bool kTwo>
+// A second product in the same launch (the backward pass of a gated block).
+//  kSum    a second pair of operands, whose product joins the first's in one sum:
+//          the contraction runs over the first pair, then over the second.
+//  kStack  a second operand in the place of the call's p, with an output of its
+//          own: its tiles follow the first's.
+enum Extra : int { kNone, kSum, kStack };
+template <int kExtra>
 struct SecondMaps {};
 template <>
-struct SecondMaps<true> {
+struct SecondMaps<kSum> {
   CUtensorMap p, q;
 };
+template <>
+struct SecondMaps<kStack> {
+  CUtensorMap in, out;  // the operand (P of a wide tile, Q of a split one), the output
+};
+
+struct Output {
+  uint16_t* p;
+  uint64_t ld;
+};
+
+// Is tile t of the stacked dimension the second product's?  t counts from its
+// own product's first then.
+template <int kExtra>
+__device__ __forceinline__ bool second_product(const GemmArgs& a, uint32_t& t) {
+  if (kExtra != kStack || t < a.tiles_first) return false;
+  t -= a.tiles_first;
+  return true;
+}
+template <int kExtra>
+__device__ __forceinline__ Output output_of(const GemmArgs& a, bool second) {
+  if (kExtra == kStack && second) return {a.out2, a.ldout2};
+  return {a.out, a.ldout};
+}
 
 // Bytes that the copy engine brings to a block's stage for `subs` accumulators.
 __device__ __forceinline__ uint32_t copied_bytes(const GemmArgs& a, uint32_t subs) {
@@ -133,9 +162,9 @@ __device__ __forceinline__ uint32_t copied_bytes(const GemmArgs& a, uint32_t sub
 // block fills its own half of the stage; both halves count on the first
 // block's barrier.  Returns the stages filled, fewer than last - first after a
 // wait ran out.
-template <bool kPair, uint32_t kSubs, bool kTwo>
+template <bool kPair, uint32_t kSubs, int kExtra>
 __device__ __forceinline__ uint32_t copy_tile(const GemmArgs& a, const CUtensorMap* mp, const CUtensorMap* mq,
-                                              const SecondMaps<kTwo>* m2, Shared& s, uint8_t* stages, Ring& ring,
+                                              const SecondMaps<kExtra>* m2, Shared& s, uint8_t* stages, Ring& ring,
                                               uint32_t p0, uint32_t q0, uint32_t first, uint32_t last, uint32_t rank) {
   const uint32_t bytes = copied_bytes(a, kSubs);
   for (uint32_t i = first; i < last; ++i) {
@@ -146,7 +175,7 @@ __device__ __forceinline__ uint32_t copy_tile(const GemmArgs& a, const CUtensorM
     if (kPair) bar = cluster_peer_address(bar, 0);
     const CUtensorMap *p = mp, *q = mq;
     uint32_t k0 = i * kStep;
-    if constexpr (kTwo)
+    if constexpr (kExtra == kSum)
       if (i >= a.first_steps) p = &m2->p, q = &m2->q, k0 = (i - a.first_steps) * kStep;
     if (a.p_copy) copy_operand<kPair>(addr_of(dst), p, a.p_layout, p0, k0, kLanes, bar);
     if (a.q_copy)

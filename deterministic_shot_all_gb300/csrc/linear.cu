@@ -231,7 +231,7 @@ __device__ __forceinline__ void finish_boxes(const GemmArgs& a, const CUtensorMa
 // the activation's branches and the residual's latency once for each of them
 // were 230 cycles a row.
 template <int D, uint32_t kRows, bool kFull>  // kFull: n >= kRows
-__device__ __forceinline__ void finish_rows(const GemmArgs& a, const float* staged, uint64_t row, uint32_t n, uint32_t col,
+__device__ __forceinline__ void finish_rows(const GemmArgs& a, const Output& o, const float* staged, uint64_t row, uint32_t n, uint32_t col,
                                             float bias) {
   uint16_t res[kRows];
   const uint16_t* p = a.residual + row * a.ldresidual + col;
@@ -252,14 +252,14 @@ __device__ __forceinline__ void finish_rows(const GemmArgs& a, const float* stag
 #pragma unroll
     for (uint32_t k = 0; k < kRows; ++k) v[k] += Elem<D>::widen(res[k]);
   }
-  uint16_t* out = a.out + row * a.ldout + col;
+  uint16_t* out = o.p + row * o.ld + col;
 #pragma unroll
-  for (uint32_t k = 0; k < kRows; ++k, out += a.ldout)
+  for (uint32_t k = 0; k < kRows; ++k, out += o.ld)
     if (kFull || k < n) *out = Elem<D>::round(v[k]);
 }
 
 template <int D, uint32_t kRows>
-__device__ __forceinline__ void finish_staged(const GemmArgs& a, const float* staged, uint32_t row0, uint32_t col,
+__device__ __forceinline__ void finish_staged(const GemmArgs& a, const Output& o, const float* staged, uint32_t row0, uint32_t col,
                                               uint32_t lane) {
   const uint32_t rows = row0 < a.P ? (a.P - row0 < 32 ? a.P - row0 : 32) : 0;
   if (col >= a.Q) return;
@@ -267,19 +267,20 @@ __device__ __forceinline__ void finish_staged(const GemmArgs& a, const float* st
 #pragma unroll 1
   for (uint32_t r = 0; r < rows; r += kRows) {
     if (rows - r >= kRows)
-      finish_rows<D, kRows, true>(a, staged + r * 33 + lane, row0 + r, kRows, col, bias);
+      finish_rows<D, kRows, true>(a, o, staged + r * 33 + lane, row0 + r, kRows, col, bias);
     else
-      finish_rows<D, kRows, false>(a, staged + r * 33 + lane, row0 + r, rows - r, col, bias);
+      finish_rows<D, kRows, false>(a, o, staged + r * 33 + lane, row0 + r, rows - r, col, bias);
   }
 }
 
 constexpr uint16_t kNan16 = 0x7FFF;  // in bf16 and in fp16
 
 // 32 rows by n columns of the outputs, by a warp.
-__device__ __noinline__ void fill_nan(const GemmArgs& a, uint32_t row0, uint32_t col0, uint32_t n, uint32_t lane) {
+__device__ __noinline__ void fill_nan(const GemmArgs& a, Output o, uint32_t row0, uint32_t col0, uint32_t n,
+                                      uint32_t lane) {
   for (uint32_t row = row0; row < row0 + 32 && row < a.P; ++row)
     for (uint32_t c = col0 + lane; c < col0 + n && c < a.Q; c += 32) {
-      a.out[row * a.ldout + c] = kNan16;
+      o.p[row * o.ld + c] = kNan16;
       if (a.z) a.z[row * a.ldz + c] = kNan16;
     }
 }
@@ -298,7 +299,7 @@ __device__ __forceinline__ uint2 residual4(const GemmArgs& a, uint32_t row, uint
 }
 
 template <int D>
-__device__ __forceinline__ void finish4(const GemmArgs& a, float (&v)[4], uint2 res, uint32_t row, uint32_t col) {
+__device__ __forceinline__ void finish4(const GemmArgs& a, const Output& o, float (&v)[4], uint2 res, uint32_t row, uint32_t col) {
   const uint32_t n = col < a.P ? a.P - col : 0;
   const bool whole = a.quads && n >= 4;
   const auto store = [&](uint16_t* p) {
@@ -321,15 +322,15 @@ __device__ __forceinline__ void finish4(const GemmArgs& a, float (&v)[4], uint2 
     v[0] += Elem<D>::widen(uint16_t(res.x)), v[1] += Elem<D>::widen(uint16_t(res.x >> 16));
     v[2] += Elem<D>::widen(uint16_t(res.y)), v[3] += Elem<D>::widen(uint16_t(res.y >> 16));
   }
-  store(a.out + row * a.ldout + col);
+  store(o.p + row * o.ld + col);
 }
 
 // kSubs: accumulators to a tile.
-template <int D, int kWord, bool kBoth, uint32_t kSubs, bool kTwo>
+template <int D, int kWord, bool kBoth, uint32_t kSubs, int kExtra>
 __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     gemm_wide_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap mp,
                      const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mout,
-                     const __grid_constant__ CUtensorMap mz, const __grid_constant__ SecondMaps<kTwo> m2) {
+                     const __grid_constant__ CUtensorMap mz, const __grid_constant__ SecondMaps<kExtra> m2) {
   constexpr bool kTma = kWord == 16;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
@@ -344,13 +345,16 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
   if (copies || loads) {
     uint32_t t = first_piece, filled = 0;
     for (; t < pieces; t += step) {
-      const Piece w = piece_at<kSubs>(a, t);
+      Piece w = piece_at<kSubs>(a, t);
+      const CUtensorMap* p = &mp;
+      if constexpr (kExtra == kStack)
+        if (second_product<kExtra>(a, w.tp)) p = &m2.in;
       const uint32_t p0 = (2 * w.tp + rank) * kLanes, q0 = w.q0 + rank * a.bq;
       filled = 0;
       if (copies && kSubs == 2 && w.subs == 2)
-        filled = copy_tile<true, kSubs, kTwo>(a, &mp, &mq, &m2, s, stages, ring, p0, q0, 0, a.steps, rank);
+        filled = copy_tile<true, kSubs, kExtra>(a, p, &mq, &m2, s, stages, ring, p0, q0, 0, a.steps, rank);
       else if (copies)
-        filled = copy_tile<true, 1, kTwo>(a, &mp, &mq, &m2, s, stages, ring, p0, q0, 0, a.steps, rank);
+        filled = copy_tile<true, 1, kExtra>(a, p, &mq, &m2, s, stages, ring, p0, q0, 0, a.steps, rank);
       else if constexpr (!kTma)
         filled = load_tile<kWord, kBoth, true>(a, s, stages, ring, p0, q0, 0, a.steps, threadIdx.x - kFirstLoader<kTma>);
       if (filled < a.steps) break;
@@ -375,7 +379,12 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
     Boxes boxes{addr_of(stages + a.stages * a.stage_bytes) + (warp - 2) * 4096, 0};
     uint32_t n = 0, t = first_piece;
     for (; t < pieces; t += step, ++n) {
-      const Piece w = piece_at<kSubs>(a, t);
+      Piece w = piece_at<kSubs>(a, t);
+      const bool second = second_product<kExtra>(a, w.tp);
+      const Output o = output_of<kExtra>(a, second);
+      const CUtensorMap* map = &mout;
+      if constexpr (kExtra == kStack)
+        if (second) map = &m2.out;
       const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
       const uint32_t row0 = (2 * w.tp + rank) * kLanes + quarter * 32;
       const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = 0.0f;
           }
-          finish_boxes<D>(a, &mout, &mz, v, ahead, row0, col, column(i + 1), i + 1 < runs, boxes, lane);
+          finish_boxes<D>(a, map, &mz, v, ahead, row0, col, column(i + 1), i + 1 < runs, boxes, lane);
         } else {
           __syncwarp();
 #pragma unroll
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
             for (int k = 0; k < 16; ++k) staged[lane * 33 + h + k] = v[k];
           }
           __syncwarp();
-          finish_staged<D, kTma ? 16 : 8>(a, staged, row0, col + lane, lane);
+          finish_staged<D, kTma ? 16 : 8>(a, o, staged, row0, col + lane, lane);
         }
       }
       tmem_fence_before();
@@ -431,10 +440,11 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
       if (lane == 0) mbar_arrive_cluster(cluster_peer_address(addr_of(&s.acc_empty[b]), 0));
     }
     for (; t < pieces; t += step) {  // after a wait ran out
-      const Piece w = piece_at<kSubs>(a, t);
+      Piece w = piece_at<kSubs>(a, t);
+      const Output o = output_of<kExtra>(a, second_product<kExtra>(a, w.tp));
       const uint32_t half = kTma ? a.bn / 2 : a.bn, c0 = kTma ? (warp - 2) / 4 * half : 0;
       for (uint32_t j = 0; j < w.subs; ++j)
-        fill_nan(a, (2 * w.tp + rank) * kLanes + quarter * 32, w.q0 + j * a.bn + c0, half, lane);
+        fill_nan(a, o, (2 * w.tp + rank) * kLanes + quarter * 32, w.q0 + j * a.bn + c0, half, lane);
     }
     if (kTma && lane == 0) bulk_wait_all();
   }
@@ -444,10 +454,10 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, 1)
 
 // One tile per cluster; block r of the cluster takes the r-th share of the
 // contraction.  P's rows are the output's columns here, Q's rows its rows.
-template <int D, int kWord, bool kBoth, bool kTwo>
+template <int D, int kWord, bool kBoth, int kExtra>
 __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1)
     gemm_split_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap mp,
-                      const __grid_constant__ CUtensorMap mq, const __grid_constant__ SecondMaps<kTwo> m2) {
+                      const __grid_constant__ CUtensorMap mq, const __grid_constant__ SecondMaps<kExtra> m2) {
   constexpr bool kTma = kWord == 16;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
@@ -456,7 +466,10 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
   setup<kTma, false>(a, &mp, &mq, s, warp);
   dependent_launch_prologue();
   const uint32_t rank = blockIdx.x % a.split, tile = blockIdx.x / a.split;
-  const uint32_t tp = tile % a.tiles_p, tq = tile / a.tiles_p;
+  const uint32_t tp = tile % a.tiles_p;
+  uint32_t tq = tile / a.tiles_p;
+  const bool second = second_product<kExtra>(a, tq);
+  const Output o = output_of<kExtra>(a, second);
   const uint32_t p0 = tp * kLanes, q0 = tq * a.bn;
   const uint32_t share = (a.steps + a.split - 1) / a.split;
   const uint32_t first = rank * share < a.steps ? rank * share : a.steps;
@@ -466,7 +479,10 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
   Ring ring;
   const bool copies = threadIdx.x == 0 && (a.p_copy | a.q_copy), loads = !kTma && threadIdx.x >= kFirstLoader<kTma>;
   if (copies) {
-    const uint32_t filled = copy_tile<false, 1, kTwo>(a, &mp, &mq, &m2, s, stages, ring, p0, q0, first, last, 0);
+    const CUtensorMap* q = &mq;
+    if constexpr (kExtra == kStack)
+      if (second) q = &m2.in;
+    const uint32_t filled = copy_tile<false, 1, kExtra>(a, &mp, q, &m2, s, stages, ring, p0, q0, first, last, 0);
     note_fills<kTma>(s, filled, true, warp, lane);
   } else if (loads) {
     if constexpr (!kTma) {
@@ -528,7 +544,7 @@ __global__ void __launch_bounds__(kGemmThreads<kWord == 16>, kWord == 16 ? 2 : 1
 #pragma unroll
     for (uint32_t r = 0; r < 8; ++r)
       if (r < a.split) v[0] += in[r].x, v[1] += in[r].y, v[2] += in[r].z, v[3] += in[r].w;
-    finish4<D>(a, v, res, row, j);
+    finish4<D>(a, o, v, res, row, j);
   }
   finish_block<kTma, false, 1>(a, s, warp, rank);
 }
@@ -615,8 +631,8 @@ __global__ void __launch_bounds__(kDotThreads) dot_kernel(const __grid_constant_
 
 // A persistent grid: as many pairs as the device holds at once (two blocks to
 // a pair, one block to an SM), or fewer tiles.
-template <int D, int kWord, bool kBoth, uint32_t kSubs, bool kTwo>
-cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap (&m)[4], const SecondMaps<kTwo>& m2, int sms,
+template <int D, int kWord, bool kBoth, uint32_t kSubs, int kExtra>
+cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap (&m)[4], const SecondMaps<kExtra>& m2, int sms,
                         cudaStream_t st) {
   const uint32_t tiles = a.tiles_p * a.tiles_q, pairs = uint32_t(sms) / 2, rest = tiles % pairs;
   const bool halves = kSubs == 2 && 2 * rest <= pairs;
@@ -625,14 +641,14 @@ cudaError_t launch_wide(const GemmArgs& a, const CUtensorMap (&m)[4], const Seco
   g.pieces = halves ? tiles + rest : tiles;
   uint32_t smem = 1024 + g.stages * g.stage_bytes + kEpilogueWarps<kWord == 16> * kStagedBytes;
   if (smem < kAloneShared) smem = kAloneShared;
-  return launch_cluster<gemm_wide_kernel<D, kWord, kBoth, kSubs, kTwo>>(2 * (g.pieces < pairs ? g.pieces : pairs),
+  return launch_cluster<gemm_wide_kernel<D, kWord, kBoth, kSubs, kExtra>>(2 * (g.pieces < pairs ? g.pieces : pairs),
                                                                        kGemmThreads<kWord == 16>, 2, smem, st, g, m[0],
                                                                        m[1], m[2], m[3], m2);
 }
 
-template <int D, int kWord, bool kBoth, bool kTwo>
-cudaError_t launch_split(const GemmArgs& a, const CUtensorMap (&m)[4], const SecondMaps<kTwo>& m2, cudaStream_t st) {
-  return launch_cluster<gemm_split_kernel<D, kWord, kBoth, kTwo>>(a.tiles_p * a.tiles_q * a.split,
+template <int D, int kWord, bool kBoth, int kExtra>
+cudaError_t launch_split(const GemmArgs& a, const CUtensorMap (&m)[4], const SecondMaps<kExtra>& m2, cudaStream_t st) {
+  return launch_cluster<gemm_split_kernel<D, kWord, kBoth, kExtra>>(a.tiles_p * a.tiles_q * a.split,
                                                                   kGemmThreads<kWord == 16>, a.split,
                                                                   1024 + a.stages * a.stage_bytes, st, a, m[0], m[1], m2);
 }
@@ -743,13 +759,16 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   a.act = c.act, a.wdtype = c.wdtype;
   a.K = uint32_t(c.k);
   a.steps = a.first_steps = ceil_div(c.k, kStep);
-  if (c.p2) a.steps *= 2;
+  const bool sum = c.p2 && c.q2, stack = c.p2 && !c.q2;
+  if (sum) a.steps *= 2;
+  a.out2 = static_cast<uint16_t*>(c.out2), a.ldout2 = c.ldout2;
 
   const auto aligned = [](const void* p, uint64_t ld, unsigned elements) {
     return !p || (reinterpret_cast<uintptr_t>(p) % (2 * elements) == 0 && ld % elements == 0);
   };
   const auto out_aligned = [&](unsigned n) {
-    return aligned(a.out, a.ldout, n) && aligned(a.z, a.ldz, n) && aligned(a.residual, a.ldresidual, n);
+    return aligned(a.out, a.ldout, n) && aligned(a.z, a.ldz, n) && aligned(a.residual, a.ldresidual, n) &&
+           aligned(a.out2, a.ldout2, n);
   };
   a.quads = out_aligned(4);
   a.octets = out_aligned(8) && c.cols % 8 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
@@ -776,7 +795,9 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   if (!cp_copy) bits |= reinterpret_cast<uintptr_t>(cp) | (cp_rows > 1 ? c.ldp * 2 : 0);
   if (!cq_copy) bits |= reinterpret_cast<uintptr_t>(cq) | (cq_rows > 1 ? c.ldq * 2 : 0);
   const uint32_t word = cp_copy && cq_copy ? 16 : bits % 8 == 0 ? 8 : 2;
-  const Form form = choose_form(c, a.steps, cp_copy, cq_copy);
+  GemmCall shape = c;
+  if (stack) shape.rows *= 2;
+  const Form form = choose_form(shape, a.steps, cp_copy, cq_copy);
   const bool wide = form.wide;
   a.bn = form.bn;
   a.split = form.split;
@@ -796,6 +817,11 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   const uint32_t lanes = wide ? 2 * kLanes : kLanes;
   a.tiles_p = ceil_div(a.P, lanes);
   a.tiles_q = ceil_div(a.Q, form.subs * a.bn);
+  if (stack) {
+    uint32_t& tiles = wide ? a.tiles_p : a.tiles_q;
+    a.tiles_first = tiles;
+    tiles *= 2;
+  }
   a.stage_bytes = kPBytes + form.subs * a.bq * 128;
   a.stages = (word != 16 ? kLoadedBudget : wide || a.bn > 128 ? kStageBudget : kSplitBudget) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
@@ -810,15 +836,22 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
     err = encode(&m[1], &a.q_layout, a.q, a.ldq, a.Q, a.K, a.q_mn, a.bq, bf16);
     if (err != cudaSuccess) return err;
   }
-  SecondMaps<true> m2{};
+  SecondMaps<kSum> two{};
+  SecondMaps<kStack> stacked{};
   if (c.p2) {
-    if (word != 16) return cudaErrorInvalidValue;  // the caller brings both pairs onto rows of 16 bytes
-    uint32_t layout;  // that of the first pair: it goes by the sizes
-    const void *p = wide ? c.p2 : c.q2, *q = wide ? c.q2 : c.p2;
-    const uint64_t ldp = wide ? c.ldp2 : c.ldq2, ldq = wide ? c.ldq2 : c.ldp2;
-    err = encode(&m2.p, &layout, static_cast<const uint16_t*>(p), ldp, a.P, a.K, a.p_mn, kLanes, bf16);
-    if (err == cudaSuccess)
-      err = encode(&m2.q, &layout, static_cast<const uint16_t*>(q), ldq, a.Q, a.K, a.q_mn, a.bq, bf16);
+    if (word != 16) return cudaErrorInvalidValue;  // the caller brings all operands onto rows of 16 bytes
+    // The layouts are those of the first operands: they go by the sizes.
+    uint32_t layout;
+    const auto* p2 = static_cast<const uint16_t*>(c.p2);
+    const auto* q2 = static_cast<const uint16_t*>(c.q2);
+    const auto second = [&](CUtensorMap* m, const uint16_t* base, uint64_t ld, bool is_p) {
+      return is_p ? encode(m, &layout, base, ld, a.P, a.K, a.p_mn, kLanes, bf16)
+                  : encode(m, &layout, base, ld, a.Q, a.K, a.q_mn, a.bq, bf16);
+    };
+    err = second(sum ? (wide ? &two.p : &two.q) : &stacked.in, p2, c.ldp2, wide);
+    if (err == cudaSuccess && sum) err = second(wide ? &two.q : &two.p, q2, c.ldq2, !wide);
+    if (err == cudaSuccess && stack && wide && a.octets)
+      err = encode_output(&stacked.out, a.out2, a.ldout2, a.P, a.Q, bf16);
     if (err != cudaSuccess) return err;
   }
   if (wide && word == 16 && a.octets) {
@@ -831,20 +864,22 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
     constexpr bool kBoth = decltype(both)::value;
     const auto pairs = [&](const auto& second) {
       using M = std::remove_const_t<std::remove_reference_t<decltype(second)>>;
-      constexpr bool kTwo = std::is_same_v<M, SecondMaps<true>>;
+      constexpr int kExtra = std::is_same_v<M, SecondMaps<kSum>> ? kSum : std::is_same_v<M, SecondMaps<kStack>> ? kStack : kNone;
       if constexpr (kWord == 16)
         if (wide && form.subs == 2)
-          return bf16 ? launch_wide<ARX_BF16, kWord, kBoth, 2, kTwo>(a, m, second, sms, st)
-                      : launch_wide<ARX_F16, kWord, kBoth, 2, kTwo>(a, m, second, sms, st);
+          return bf16 ? launch_wide<ARX_BF16, kWord, kBoth, 2, kExtra>(a, m, second, sms, st)
+                      : launch_wide<ARX_F16, kWord, kBoth, 2, kExtra>(a, m, second, sms, st);
       if (wide)
-        return bf16 ? launch_wide<ARX_BF16, kWord, kBoth, 1, kTwo>(a, m, second, sms, st)
-                    : launch_wide<ARX_F16, kWord, kBoth, 1, kTwo>(a, m, second, sms, st);
-      return bf16 ? launch_split<ARX_BF16, kWord, kBoth, kTwo>(a, m, second, st)
-                  : launch_split<ARX_F16, kWord, kBoth, kTwo>(a, m, second, st);
+        return bf16 ? launch_wide<ARX_BF16, kWord, kBoth, 1, kExtra>(a, m, second, sms, st)
+                    : launch_wide<ARX_F16, kWord, kBoth, 1, kExtra>(a, m, second, sms, st);
+      return bf16 ? launch_split<ARX_BF16, kWord, kBoth, kExtra>(a, m, second, st)
+                  : launch_split<ARX_F16, kWord, kBoth, kExtra>(a, m, second, st);
     };
-    if constexpr (kWord == 16)
-      if (c.p2) return pairs(m2);
-    return pairs(SecondMaps<false>{});
+    if constexpr (kWord == 16) {
+      if (sum) return pairs(two);
+      if (stack) return pairs(stacked);
+    }
+    return pairs(SecondMaps<kNone>{});
   };
   using std::integral_constant;
   const bool both = !cp_copy && !cq_copy;

@@ -42,7 +42,7 @@ bool off_16(const void* p, uint64_t ld, uint64_t rows) {
 }
 
 // The copies of a backward pass, of rows of K rounded up to 8: both weights for
-// dx, then, in their place, x for the weights' gradients.
+// dx, and x for the weights' gradients.
 struct BackwardCopies {
   bool gate, up, x;
   uint64_t pitch, w_bytes, bytes;
@@ -55,15 +55,17 @@ BackwardCopies backward_copies(const arx_gated_linear_bwd_args& a) {
   c.gate = a.dx && off_16(a.w_gate, a.ldw_gate, a.N);
   c.up = a.dx && off_16(a.w_up, a.ldw_up, a.N);
   c.x = (a.dw_gate || a.dw_up) && off_16(a.x, a.ldx, a.M);
-  const uint64_t weights = (c.gate + c.up) * c.w_bytes, x = c.x ? a.M * c.pitch * 2 : 0;
-  c.bytes = weights > x ? weights : x;
+  c.bytes = (c.gate + c.up) * c.w_bytes + (c.x ? a.M * c.pitch * 2 : 0);
   return c;
 }
 
-// A matrix to be copied onto rows of 16 bytes at dst; p and ld become the copy's.
-void add_copy(arx::RealignSet& set, const void*& p, uint64_t& ld, uint64_t rows, uint64_t cols, uint64_t pitch, void* dst) {
-  set.m[set.n++] = {static_cast<const uint16_t*>(p), static_cast<uint16_t*>(dst), rows, ld, pitch, int64_t(cols)};
+// A matrix to be copied onto rows of 16 bytes at dst, which moves past it; p and ld
+// become the copy's.
+void add_copy(arx::RealignSet& set, const void*& p, uint64_t& ld, uint64_t rows, uint64_t cols, uint64_t pitch,
+              uint8_t*& dst) {
+  set.m[set.n++] = {static_cast<const uint16_t*>(p), reinterpret_cast<uint16_t*>(dst), rows, ld, pitch, int64_t(cols)};
   p = dst, ld = pitch;
+  dst += rows * pitch * 2;
 }
 
 }  // namespace
@@ -256,36 +258,34 @@ arx_status arx_gated_linear_bwd(const arx_gated_linear_bwd_args* a, void* stream
     const cudaError_t e = arx::launch_gated_grad(g, units(in[0]) && units(in[1]) && units(in[2]), st);
     if (e != cudaSuccess) return launched(e, "arx_gated_linear_bwd");
   }
-  const auto copy = [&](const arx::RealignSet& set) { return set.n ? arx::launch_realign(set, st) : cudaSuccess; };
-  if (a->dx && a->M && a->K) {
-    const void *wg = a->w_gate, *wu = a->w_up;
-    uint64_t ldg = in[4].ld, ldu = in[5].ld;
+  const void *wg = a->w_gate, *wu = a->w_up, *x = a->x;
+  uint64_t ldg = in[4].ld, ldu = in[5].ld, ldx = in[3].ld;
+  if (copies.bytes) {
     uint8_t* to = static_cast<uint8_t*>(a->copies);
     arx::RealignSet set{};
     if (copies.gate) add_copy(set, wg, ldg, a->N, a->K, copies.pitch, to);
-    if (copies.up) add_copy(set, wu, ldu, a->N, a->K, copies.pitch, to + (copies.gate ? copies.w_bytes : 0));
-    cudaError_t e = copy(set);
+    if (copies.up) add_copy(set, wu, ldu, a->N, a->K, copies.pitch, to);
+    if (copies.x) add_copy(set, x, ldx, a->M, a->K, copies.pitch, to);
+    const cudaError_t e = arx::launch_realign(set, st);
     if (e != cudaSuccess) return launched(e, "arx_gated_linear_bwd");
+  }
+  if (a->dx && a->M && a->K) {
     arx::GemmCall c = product(dg, lddz, false, wg, ldg, true, a->M, a->K, a->N, a->dtype, a->wdtype, a->status, a->wait_us);
     if (a->N) c.p2 = du, c.ldp2 = c.ldp, c.q2 = wu, c.ldq2 = a->N <= 1 ? a->K : ldu;
     c.out = a->dx, c.ldout = out[0].ld;
-    e = arx::launch_gemm(c, st);
+    const cudaError_t e = arx::launch_gemm(c, st);
     if (e != cudaSuccess) return launched(e, "arx_gated_linear_bwd");
   }
-  if (weights && a->N && a->K) {
-    const void* x = a->x;
-    uint64_t ldx = in[3].ld;
-    arx::RealignSet set{};  // in the place of the weights' copies, which have been read by then
-    if (copies.x) add_copy(set, x, ldx, a->M, a->K, copies.pitch, a->copies);
-    cudaError_t e = copy(set);
-    if (e != cudaSuccess) return launched(e, "arx_gated_linear_bwd");
+  if (weights && a->N && a->K) {  // both in one launch, so that their tiles fill the SMs together
+    const bool both = a->dw_gate && a->dw_up && a->M;
     for (int i = 0; i < 2; ++i) {
       const Mat& dw = out[1 + i];
-      if (!dw.p) continue;
+      if (!dw.p || (both && i)) continue;
       arx::GemmCall c = product(i ? du : dg, lddz, true, x, ldx, true, a->N, a->K, a->M, a->dtype, a->wdtype, a->status,
                                 a->wait_us);
       c.out = const_cast<void*>(dw.p), c.ldout = dw.ld;
-      e = arx::launch_gemm(c, st);
+      if (both) c.p2 = du, c.ldp2 = c.ldp, c.out2 = a->dw_up, c.ldout2 = out[2].ld;
+      const cudaError_t e = arx::launch_gemm(c, st);
       if (e != cudaSuccess) return launched(e, "arx_gated_linear_bwd");
     }
   }

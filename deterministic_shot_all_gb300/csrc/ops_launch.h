@@ -96,8 +96,13 @@ struct GemmCall {
   uint32_t* status;
   uint32_t wait_ns;       // limit of a kernel's wait for its own copies and products
   void* copies;           // gemm_copies_bytes(c) bytes, or null
-  const void *p2, *q2;    // null, or a second pair of operands of the same sizes whose product joins
-  uint64_t ldp2, ldq2;    // the sum: all four on rows of 16 bytes, without copies
+  // A second product in the launch, all operands on rows of 16 bytes, without copies:
+  // p2 and q2, of the same sizes, whose product joins the sum; or p2 alone, whose
+  // product with q goes to out2.
+  const void *p2, *q2;
+  uint64_t ldp2, ldq2;
+  void* out2;
+  uint64_t ldout2;
 };
 cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st);
 // Bytes for copies of the operands whose rows are off 16 bytes, 0 where the

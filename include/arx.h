@@ -943,8 +943,8 @@ arx_status arx_gated_linear(const arx_gated_linear_args* a, void* stream);
  *   dx      [M, K], dw_gate and dw_up [N, K], dbias_gate and dbias_up [N] of `wdtype`;
  *           any may be NULL.  M == 0 sets the weights' and biases' gradients to zero
  *   workspace  arx_gated_linear_bwd_workspace_bytes(M, N) bytes (dg, du, partial sums)
- *   copies  arx_gated_linear_bwd_copies_bytes(a) bytes: of w_gate and w_up, then of x;
- *           may be NULL where that is 0
+ *   copies  arx_gated_linear_bwd_copies_bytes(a) bytes: of w_gate, w_up and x; may be
+ *           NULL where that is 0
  *   status, wait_us  as in arx_linear */
 typedef struct arx_gated_linear_bwd_args {
   const void* dout;

@@ -281,7 +281,7 @@ def test_copies_are_needed_and_checked(arx, op, operand):
     if op == "gated_linear_bwd":
         a.workspace_bytes = arx.arx_gated_linear_bwd_workspace_bytes(M, N)
     n = query(ctypes.byref(a))
-    assert n == (M + 2 * N if op == "gated_linear" else max(2 * N, M)) * 4104 * 2
+    assert n == (M + 2 * N) * 4104 * 2
     assert call(ctypes.byref(a), None) == arx.ARX_EINVAL and f"copies is null, {n} bytes needed" in arx.arx_last_error()
     a.copies, a.copies_bytes = _region(40), n - 1
     assert call(ctypes.byref(a), None) == arx.ARX_EINVAL and "copies" in arx.arx_last_error()
