@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kGemmThreads<true>, 2)
 
 constexpr uint32_t kDotRows = 2;
 constexpr uint32_t kDotThreads = 256;
-constexpr int kDotBatch = 4;
+constexpr int kDotBatch = 4;  // 2 took 1.0 to 1.25 times as long, 8 1.2 to 1.5 (fewer blocks at once)
 
 // Two e4m3 in 16 bits, widened.
 __device__ __forceinline__ void widen_e4m3x2(uint32_t v, float& a, float& b) {
@@ -439,6 +439,14 @@ __global__ void __launch_bounds__(kDotThreads) gated_dot_kernel(const __grid_con
   const uint32_t j = blockIdx.x * per + warp / a.split, share = warp % a.split;
   const uint8_t* row[2] = {reinterpret_cast<const uint8_t*>(a.q) + j * a.ldq * kSize,
                            static_cast<const uint8_t*>(w_up) + j * ldw_up * kSize};
+  // A hint only, as in linear.cu: the weights' way to L2 starts while the stream's
+  // previous kernel, whose output x may be, still runs.  The first batch of the
+  // feature's warps: asked for whole, rows of 16 KB came twice (8192 x 8192: 55.8
+  // against 44.5 us; none 44.9, but 2048 x 4096 7.3 against 6.2).
+  if (kV > 1 && share == 0 && lane == 0 && j < a.Q && a.K > 0) {
+    const uint32_t bytes = a.K * kSize, batch = 32 * kDotBatch * 16 * a.split;
+    for (int h = 0; h < 2; ++h) prefetch_l2_bulk(row[h], bytes < batch ? bytes : batch);
+  }
   dependent_launch_prologue();
   float acc[2 * kM] = {};
   if (j < a.Q) {
@@ -532,13 +540,20 @@ bool on_16_bytes(const void* p, uint64_t ld, uint64_t rows, uint64_t size) {
 
 uint64_t size_of(int dtype) { return dtype == ARX_E4M3 ? 1 : 2; }
 
-// Do dot products take the call in whole units?  One by one (16 bits)?
+// Do dot products take the call in whole units?  Measured, microseconds (dot, split
+// form): one row, 16 bits, 2048 x 4096 6.2, 9.4; 4096 x 8192 21.6, 23.3; 8192 x 8192
+// 43.9, 41.9; e4m3 the dot form up to there.  Two rows, whose second halves the
+// reading's share of the issue slots, 4096 x 4096 13.0, 13.9; 4096 x 8192 25.0, 23.4;
+// e4m3, with its conversions, 512 x 1024 2.4, 4.3; 1024 x 2048 4.7, 4.6; 4096 x 8192
+// 21.3, 14.7.
 bool dot_units(const arx_gated_linear_args& c) {
-  const uint64_t size = size_of(c.dtype);
-  return c.M <= kDotRows && c.K * size % 16 == 0 && on_16_bytes(c.x, c.ldx, c.M, size) &&
+  const uint64_t size = size_of(c.dtype), weights = 2 * c.N * c.K;
+  if (c.M > kDotRows) return false;
+  if (c.dtype == ARX_E4M3 ? c.M == 2 && weights > (1u << 22) : weights >= (c.M == 2 ? 3u << 24 : 1u << 27)) return false;
+  return c.K * size % 16 == 0 && on_16_bytes(c.x, c.ldx, c.M, size) &&
          on_16_bytes(c.w_gate, c.ldw_gate, c.N, size) && on_16_bytes(c.w_up, c.ldw_up, c.N, size);
 }
-// As the products of linear.cu: up to about 8 million weights.
+// One by one (16 bits)?  As the products of linear.cu: up to about 8 million weights.
 bool dot_single(const arx_gated_linear_args& c) {
   return c.M <= kDotRows && c.dtype != ARX_E4M3 && 2 * c.N * c.K < (uint64_t(1) << 23);
 }
