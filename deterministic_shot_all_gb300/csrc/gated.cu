@@ -80,10 +80,12 @@ __device__ __forceinline__ uint32_t copy_split(const GatedArgs& a, const CUtenso
 
 // ---- epilogues ------------------------------------------------------------------------
 
-// What 32 columns from `col` on need from memory: a lane has those of column
-// col + lane.
+// Biases and scales of 32 columns from `col` on: asked for by the lanes a run of
+// columns ahead, then put into shared memory, from where a warp reads four columns'
+// at once.  (Handed round by shuffles they took an instruction for each column
+// and vector: 128 of a run's 900 or so.)
 struct Columns32 {
-  float bias_g, bias_u, scale_g, scale_u;
+  float v[4];  // of this lane's column: bias_gate, bias_up, gate_scale, up_scale
 };
 __device__ __forceinline__ float ask_bias(const void* p, int wdtype, int D, uint32_t col, bool on) {
   on = on && p;
@@ -95,42 +97,76 @@ template <int D, bool k8>
 __device__ __forceinline__ Columns32 ask_columns(const GatedArgs& a, uint32_t col, bool on) {
   on = on && col < a.g.Q;
   Columns32 c;
-  c.bias_g = ask_bias(a.g.bias, a.g.wdtype, D, col, on);
-  c.bias_u = ask_bias(a.bias_up, a.g.wdtype, D, col, on);
-  c.scale_g = c.scale_u = 1.0f;
+  c.v[0] = ask_bias(a.g.bias, a.g.wdtype, D, col, on);
+  c.v[1] = ask_bias(a.bias_up, a.g.wdtype, D, col, on);
+  c.v[2] = c.v[3] = 1.0f;
   if (k8) {
-    if (a.gate_scale) c.scale_g = __uint_as_float(load_ahead4(a.gate_scale + col, on));
-    if (a.up_scale) c.scale_u = __uint_as_float(load_ahead4(a.up_scale + col, on));
+    if (a.gate_scale) c.v[2] = __uint_as_float(load_ahead4(a.gate_scale + col, on));
+    if (a.up_scale) c.v[3] = __uint_as_float(load_ahead4(a.up_scale + col, on));
   }
   return c;
 }
 
-__device__ __forceinline__ void load32(uint32_t acc, bool any, float (&v)[32]) {
-  if (!any) {
+// Both projections' 32 columns: all loads on their way before the first wait.
+__device__ __forceinline__ void load_sums(uint32_t gate, uint32_t up, bool any, float (&g)[32], float (&u)[32]) {
+  uint32_t r[4][16];
+  if (any) {
+    tmem_load16_start(gate, r[0]);
+    tmem_load16_start(gate + 16, r[1]);
+    tmem_load16_start(up, r[2]);
+    tmem_load16_start(up + 16, r[3]);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = 0.0f;
-    return;
+    for (int i = 0; i < 4; ++i) tmem_load_wait(r[i]);
   }
-  uint32_t lo[16], hi[16];
-  tmem_load16_start(acc, lo);
-  tmem_load16_start(acc + 16, hi);
-  tmem_load_wait(lo);
-  tmem_load_wait(hi);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(lo[k]), v[16 + k] = __uint_as_float(hi[k]);
+  for (int k = 0; k < 32; ++k) {
+    g[k] = any ? __uint_as_float(r[k / 16][k % 16]) : 0.0f;
+    u[k] = any ? __uint_as_float(r[2 + k / 16][k % 16]) : 0.0f;
+  }
 }
 
-// v = v * scales + bias of 32 columns of this lane's row.
+// v = v * scales + bias of 32 columns of this lane's row; the columns' at `bias`
+// and `scale` in shared memory.
 template <bool k8>
-__device__ __forceinline__ void finish_sums(float (&v)[32], float row_scale, float col_scale, const void* bias, float col_bias) {
-  if (k8) {
+__device__ __forceinline__ void finish_sums(float (&v)[32], float row_scale, const float* scale, bool has_bias,
+                                            const float* bias) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] *= row_scale * __shfl_sync(0xFFFFFFFFu, col_scale, k);
+  for (int k = 0; k < 32; k += 4) {
+    Pair lo = pair(v[k], v[k + 1]), hi = pair(v[k + 2], v[k + 3]);
+    if (k8) {
+      const float4 f = *reinterpret_cast<const float4*>(scale + k);
+      lo = lo * (pair(row_scale) * pair(f.x, f.y));
+      hi = hi * (pair(row_scale) * pair(f.z, f.w));
+    }
+    if (has_bias) {
+      const float4 f = *reinterpret_cast<const float4*>(bias + k);
+      lo = lo + pair(f.x, f.y);
+      hi = hi + pair(f.z, f.w);
+    }
+    halves(lo, v[k], v[k + 1]);
+    halves(hi, v[k + 2], v[k + 3]);
   }
-  if (bias) {
+}
+
+// As store_box, of the first 16 columns alone (rows of 32 bytes, not swizzled).
+template <int D>
+__device__ __forceinline__ void store_box16(const CUtensorMap* map, const float (&v)[32], uint32_t row0, uint32_t col,
+                                            Boxes& boxes, uint32_t lane) {
+  const uint32_t box = boxes.addr + boxes.turn * 2048;
+  boxes.turn ^= 1;
+  if (lane == 0) bulk_wait_read<1>();  // the box's last store has read it
+  __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] += __shfl_sync(0xFFFFFFFFu, col_bias, k);
+  for (uint32_t u = 0; u < 2; ++u) {
+    uint32_t w[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) w[i] = Elem<D>::round2(v[8 * u + 2 * i], v[8 * u + 2 * i + 1]);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                 :: "r"(box + lane * 32 + u * 16), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
   }
+  fence_async_shared();
+  __syncwarp();
+  if (lane == 0) tma_store_2d(map, col, row0, box);
 }
 
 // Rows off 16 bytes: 32 rows by 32 columns staged in shared memory as [row][33];
@@ -161,13 +197,27 @@ __device__ __noinline__ void fill_outputs_nan(const GatedArgs& a, uint32_t row0,
     }
 }
 
+// A warp's features of an accumulator: `width` from c0 on, a multiple of 16, in
+// runs of 32 and at the end perhaps 16.
+struct Share {
+  uint32_t c0, width;
+  __device__ __forceinline__ uint32_t runs() const { return (width + 31) / 32; }
+};
+__device__ __forceinline__ Share share_of(const GemmArgs& a, uint32_t warp) {
+  const uint32_t first = (a.bq / 2 + 15) / 16 * 16;
+  return warp < 6 ? Share{0, first} : Share{first, a.bq - first};
+}
+
+struct OutputMaps {
+  CUtensorMap out, z_gate, z_up;
+};
+
 // D: type of the outputs (and of 16-bit operands); kSubs: accumulators to a tile.
 template <int D, bool k8, uint32_t kSubs>
 __global__ void __launch_bounds__(kGemmThreads<true>, 1)
     gated_wide_kernel(const __grid_constant__ GatedArgs args, const __grid_constant__ CUtensorMap mx,
                       const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mu,
-                      const __grid_constant__ CUtensorMap mout, const __grid_constant__ CUtensorMap mzg,
-                      const __grid_constant__ CUtensorMap mzu) {
+                      const __grid_constant__ OutputMaps m32, const __grid_constant__ OutputMaps m16) {
   const GemmArgs& a = args.g;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
@@ -204,19 +254,17 @@ __global__ void __launch_bounds__(kGemmThreads<true>, 1)
     }
   } else if (warp >= 2) {
     const uint32_t quarter = warp & 3;  // the accumulator lanes this warp may read
-    const uint32_t half = a.bq / 2, c0 = (warp - 2) / 4 * half;  // its features of each accumulator
+    const Share share = share_of(a, warp);
     float* staged = reinterpret_cast<float*>(stages + a.stages * a.stage_bytes) + (warp - 2) * 32 * 33;
     Boxes boxes{addr_of(stages + a.stages * a.stage_bytes) + (warp - 2) * 4096, 0};
+    uint8_t* const box0 = stages + a.stages * a.stage_bytes + (warp - 2) * 4096;
     uint32_t n = 0, t = first_piece;
     for (; t < pieces; t += step, ++n) {
       const Piece w = piece_at<kSubs>(a, t);
       const uint32_t b = kSubs == 2 ? 0 : n & 1, use = kSubs == 2 ? n : n >> 1;
       const uint32_t row0 = (2 * w.tp + rank) * kLanes + quarter * 32, n0 = w.q0 / 2;
-      const uint32_t runs = row0 < a.P ? w.subs * (half / 32) : 0;
-      const auto column = [&](uint32_t i) {
-        const uint32_t j = i * 32 >= half;
-        return n0 + j * a.bq + c0 + i * 32 - j * half;
-      };
+      const uint32_t per = share.runs(), runs = row0 < a.P ? w.subs * per : 0;
+      const auto column = [&](uint32_t i) { return n0 + i / per * a.bq + share.c0 + i % per * 32; };
       Columns32 ahead = ask_columns<D, k8>(args, column(0) + lane, runs > 0);
       float row_scale = 1.0f;
       if (k8 && args.x_scale) row_scale = __uint_as_float(load_ahead4(args.x_scale + row0 + lane, row0 + lane < a.P));
@@ -225,28 +273,39 @@ __global__ void __launch_bounds__(kGemmThreads<true>, 1)
         tmem_fence_after();
       }
       for (uint32_t i = 0; i < runs; ++i) {
-        const uint32_t col = column(i), j = i * 32 >= half;
+        const uint32_t col = column(i), j = i / per;
         if (col >= a.Q) break;  // and so are those after it
+        const uint32_t wide = share.width - i % per * 32;  // 16, or 32 and more
         const uint32_t acc = s.tmem + (b + j) * 256 + (quarter * 32 << 16) + (col - n0 - j * a.bq);
         float g[32], u[32];
-        load32(acc, a.steps > 0, g);
-        load32(acc + a.bq, a.steps > 0, u);
-        const Columns32 c = ahead;
-        ahead = ask_columns<D, k8>(args, column(i + 1) + lane, i + 1 < runs);
-        finish_sums<k8>(g, row_scale, c.scale_g, a.bias, c.bias_g);
-        finish_sums<k8>(u, row_scale, c.scale_u, args.bias_up, c.bias_u);
-        const auto store = [&](const CUtensorMap* map, const float(&v)[32], uint16_t* p, uint64_t ld) {
-          if (a.octets)
-            store_box<D>(map, v, row0, col, boxes, lane);
+        load_sums(acc, acc + a.bq, a.steps > 0, g, u);
+        if (k8 || a.bias || args.bias_up) {
+          // In the box (or staging rows) that the run's first store takes afterwards.
+          float(*own)[32] = reinterpret_cast<float(*)[32]>(a.octets ? box0 + boxes.turn * 2048 : reinterpret_cast<uint8_t*>(staged));
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) own[k][lane] = ahead.v[k];
+          __syncwarp();
+          ahead = ask_columns<D, k8>(args, column(i + 1) + lane, i + 1 < runs);
+          finish_sums<k8>(g, row_scale, own[2], a.bias != nullptr, own[0]);
+          finish_sums<k8>(u, row_scale, own[3], args.bias_up != nullptr, own[1]);
+        }
+        const auto store = [&](const CUtensorMap* map32, const CUtensorMap* map16, const float(&v)[32], uint16_t* p,
+                               uint64_t ld) {
+          if (!a.octets)
+            store_staged<D>(staged, v, p, ld, a.P, row0, col, wide < 32 && col + 16 < a.Q ? col + 16 : a.Q, lane);
+          else if (wide < 32)
+            store_box16<D>(map16, v, row0, col, boxes, lane);
           else
-            store_staged<D>(staged, v, p, ld, a.P, row0, col, a.Q, lane);
+            store_box<D>(map32, v, row0, col, boxes, lane);
         };
-        if (a.z) store(&mzg, g, a.z, a.ldz);
-        if (args.z_up) store(&mzu, u, args.z_up, args.ldz_up);
+        if (a.z) store(&m32.z_gate, &m16.z_gate, g, a.z, a.ldz);
+        if (args.z_up) store(&m32.z_up, &m16.z_up, u, args.z_up, args.ldz_up);
         activate<32>(g, a.act);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) g[k] *= u[k];
-        store(&mout, g, a.out, a.ldout);
+        for (int k = 0; k < 32; k += 2) halves(pair(g[k], g[k + 1]) * pair(u[k], u[k + 1]), g[k], g[k + 1]);
+        store(&m32.out, &m16.out, g, a.out, a.ldout);
       }
       tmem_fence_before();
       __syncwarp();
@@ -255,7 +314,7 @@ __global__ void __launch_bounds__(kGemmThreads<true>, 1)
     for (; t < pieces; t += step) {  // after a wait ran out
       const Piece w = piece_at<kSubs>(a, t);
       for (uint32_t j = 0; j < w.subs; ++j)
-        fill_outputs_nan(args, (2 * w.tp + rank) * kLanes + quarter * 32, w.q0 / 2 + j * a.bq + c0, half, lane);
+        fill_outputs_nan(args, (2 * w.tp + rank) * kLanes + quarter * 32, w.q0 / 2 + j * a.bq + share.c0, share.width, lane);
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -576,6 +635,42 @@ GatedCopies copies_of(const arx_gated_linear_args& c) {
   return r;
 }
 
+// The split form's estimate is choose_form's.  The wide form's tiles are 64 to 128
+// features (bn / 2) to an accumulator, so that the last round of tiles is full: of
+// e4m3 [1024, 8192] x [8192, 8192], two accumulators, 152 pairs of tiles in two
+// rounds of 76 take 91.7 us with 128 features, and 148 of 112 84.4 (one
+// accumulator, four rounds: 90.1, 89.0).  Measured, cycles of a stage: 600
+// for one accumulator of 256 columns, bound by the copies (55 bytes a cycle into
+// an SM), 580 for one of 224; 4.25 a column of two, bound by the products (4.2);
+// what is outside the stages of a round with two accumulators, whose epilogue no
+// products hide, 12500, and 2900 for each projection that is kept.
+Form choose_gated_form(const arx_gated_linear_args& c, uint32_t steps) {
+  GemmCall shape{};
+  shape.rows = c.M, shape.cols = 2 * c.N, shape.k = c.K;
+  Form best = choose_form(shape, steps, true, true, false);
+  constexpr uint32_t pairs = 152 / 2;
+  const double kept = 2900.0 * ((c.z_gate != nullptr) + (c.z_up != nullptr));
+  best.cycles += kept;
+  for (uint32_t bn = 256; bn >= 128; bn -= 32)
+    for (uint32_t subs = 1; subs <= 2; ++subs) {
+      const uint32_t tiles = ceil_div(c.M, 2 * kLanes) * ceil_div(c.N, subs * bn / 2), rest = tiles % pairs;
+      const double engine = (64 - 10.0 * (tiles < pairs ? tiles : pairs) / pairs) * (bn < 192 ? 0.86 : 1);
+      const double copies = (kLanes + bn / 2) * 128.0 / engine, one = copies > 2.1 * bn ? copies : 2.1 * bn;
+      double cycles;
+      if (subs == 1) {
+        const double tile = steps * one, epilogue = 4000 + kept;
+        cycles = ceil_div(tiles, pairs) * (tile > epilogue ? tile : epilogue) + 18000 + kept;
+      } else {
+        const double all = (kLanes + bn) * 128.0 / 46, two = all > 4.25 * bn ? all : 4.25 * bn;
+        const bool halves = rest && 2 * rest <= pairs;
+        cycles = (tiles / pairs + (rest && !halves)) * (steps * two + 12500 + kept) +
+                 (halves ? steps * one * 1.25 + 8000 + kept : 0) + 11000;
+      }
+      if (cycles < best.cycles) best = {true, bn, 1, subs, cycles};
+    }
+  return best;
+}
+
 template <int I, int O, int kV>
 cudaError_t launch_dot(const GatedArgs& a, const void* w_up, uint64_t ldw_up, cudaStream_t st) {
   const dim3 grid(ceil_div(a.g.Q, kDotThreads / 32 / a.g.split));
@@ -584,7 +679,8 @@ cudaError_t launch_dot(const GatedArgs& a, const void* w_up, uint64_t ldw_up, cu
 }
 
 template <int D, bool k8, uint32_t kSubs>
-cudaError_t launch_wide(const GatedArgs& a, const CUtensorMap (&m)[6], int sms, cudaStream_t st) {
+cudaError_t launch_wide(const GatedArgs& a, const CUtensorMap (&m)[3], const OutputMaps (&o)[2], int sms,
+                        cudaStream_t st) {
   const uint32_t tiles = a.g.tiles_p * a.g.tiles_q, pairs = uint32_t(sms) / 2, rest = tiles % pairs;
   const bool halves = kSubs == 2 && 2 * rest <= pairs;
   GatedArgs b = a;
@@ -593,12 +689,11 @@ cudaError_t launch_wide(const GatedArgs& a, const CUtensorMap (&m)[6], int sms, 
   uint32_t smem = 1024 + b.g.stages * b.g.stage_bytes + kEpilogueWarps<true> * kStagedBytes;
   if (smem < kAloneShared) smem = kAloneShared;
   return launch_cluster<gated_wide_kernel<D, k8, kSubs>>(2 * (b.g.pieces < pairs ? b.g.pieces : pairs),
-                                                        kGemmThreads<true>, 2, smem, st, b, m[0], m[1], m[2], m[3], m[4],
-                                                        m[5]);
+                                                        kGemmThreads<true>, 2, smem, st, b, m[0], m[1], m[2], o[0], o[1]);
 }
 
 template <int D, bool k8>
-cudaError_t launch_split(const GatedArgs& a, const CUtensorMap (&m)[6], cudaStream_t st) {
+cudaError_t launch_split(const GatedArgs& a, const CUtensorMap (&m)[3], cudaStream_t st) {
   return launch_cluster<gated_split_kernel<D, k8>>(a.g.tiles_p * a.g.tiles_q * a.g.split, kGemmThreads<true>, a.g.split,
                                                    1024 + a.g.stages * a.g.stage_bytes, st, a, m[0], m[1], m[2]);
 }
@@ -672,9 +767,7 @@ cudaError_t launch_gated(const arx_gated_linear_args& c, cudaStream_t st) {
   g.quads = out_aligned(4);
   g.octets = out_aligned(8) && c.N % 8 == 0;
 
-  GemmCall shape{};
-  shape.rows = c.M, shape.cols = 2 * c.N, shape.k = c.K;
-  const Form form = choose_form(shape, g.steps, true, true);
+  const Form form = choose_gated_form(c, g.steps);
   g.bn = form.bn, g.split = form.split;
   g.p_copy = g.q_copy = c.K > 0;
   if (form.wide) {
@@ -695,7 +788,8 @@ cudaError_t launch_gated(const arx_gated_linear_args& c, cudaStream_t st) {
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   g.idesc = mma_descriptor(c.dtype == ARX_BF16, false, false, form.wide ? 2 * kLanes : kLanes, g.bn);
 
-  CUtensorMap m[6] = {};  // x, w_gate, w_up, out, z_gate, z_up
+  CUtensorMap m[3] = {};  // x, w_gate, w_up
+  OutputMaps o[2] = {};   // boxes of 32 columns and of 16
   if (c.K > 0) {
     const uint32_t w_tile = form.wide ? g.bq : kFeatures;
     err = encode_rows(&m[0], c.x, c.ldx, c.M, c.K, form.wide ? kLanes : g.bn, c.dtype);
@@ -703,17 +797,19 @@ cudaError_t launch_gated(const arx_gated_linear_args& c, cudaStream_t st) {
     if (err == cudaSuccess) err = encode_rows(&m[2], c.w_up, c.ldw_up, c.N, c.K, w_tile, c.dtype);
     if (err != cudaSuccess) return err;
   }
-  if (form.wide && g.octets) {
-    err = encode_output(&m[3], g.out, g.ldout, g.P, g.Q, bf16);
-    if (err == cudaSuccess && g.z) err = encode_output(&m[4], g.z, g.ldz, g.P, g.Q, bf16);
-    if (err == cudaSuccess && a.z_up) err = encode_output(&m[5], a.z_up, a.ldz_up, g.P, g.Q, bf16);
-    if (err != cudaSuccess) return err;
-  }
+  if (form.wide && g.octets)
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t columns = i ? 16 : 32;
+      err = encode_output(&o[i].out, g.out, g.ldout, g.P, g.Q, bf16, columns);
+      if (err == cudaSuccess && g.z) err = encode_output(&o[i].z_gate, g.z, g.ldz, g.P, g.Q, bf16, columns);
+      if (err == cudaSuccess && a.z_up) err = encode_output(&o[i].z_up, a.z_up, a.ldz_up, g.P, g.Q, bf16, columns);
+      if (err != cudaSuccess) return err;
+    }
   const auto run = [&](auto type, auto eight) {
     constexpr int D = decltype(type)::value;
     constexpr bool kE = decltype(eight)::value;
     if (!form.wide) return launch_split<D, kE>(a, m, st);
-    return form.subs == 2 ? launch_wide<D, kE, 2>(a, m, sms, st) : launch_wide<D, kE, 1>(a, m, sms, st);
+    return form.subs == 2 ? launch_wide<D, kE, 2>(a, m, o, sms, st) : launch_wide<D, kE, 1>(a, m, o, sms, st);
   };
   using Bf16 = std::integral_constant<int, ARX_BF16>;
   using F16 = std::integral_constant<int, ARX_F16>;

@@ -473,15 +473,18 @@ inline cudaError_t encode(CUtensorMap* m, uint32_t* layout, const uint16_t* base
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Map of an output, for boxes of 32 rows by 32 columns.
-inline cudaError_t encode_output(CUtensorMap* m, uint16_t* base, uint64_t ld, uint32_t rows, uint32_t cols, bool bf16) {
+// Map of an output, for boxes of 32 rows by 32 columns (in store_box's swizzle) or
+// 16 (without).
+inline cudaError_t encode_output(CUtensorMap* m, uint16_t* base, uint64_t ld, uint32_t rows, uint32_t cols, bool bf16,
+                                 uint32_t box_columns = 32) {
   cudaError_t err = cudaSuccess;
   auto f = encode_function(&err);
   if (!f) return err;
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {(rows > 1 ? ld : cols) * 2};
-  const cuuint32_t box[2] = {32, 32}, el[2] = {1, 1};
+  const cuuint32_t box[2] = {box_columns, 32}, el[2] = {1, 1};
   const CUresult r = f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims,
-                       strides, box, el, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                       strides, box, el, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       box_columns == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -524,7 +527,8 @@ struct Form {
   double cycles;
 };
 
-inline Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy) {
+// (allow_wide: false leaves the wide forms out.)
+inline Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, bool allow_wide = true) {
   constexpr uint32_t sms = 152;
   Form best{};
   const auto consider = [&](const Form& f) {
@@ -546,7 +550,7 @@ inline Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_c
   // tile 25 a row of Q, 30 to 40 through a cluster; of a wide tile all but the last
   // run under the next one's products, 2800 + 7 a row at the least.
   constexpr uint32_t pairs = sms / 2;
-  for (uint32_t bn = 256; bn >= 128; bn /= 2) {
+  for (uint32_t bn = 256; bn >= 128 && allow_wide; bn /= 2) {
     const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, bn);
     const double engine = (58 - 12.0 * (tiles < pairs ? tiles : pairs) / pairs) * (bn == 128 ? 0.86 : 1);
     const double products = steps * stage(kLanes, bn / 2, bn, engine, 12), store = 2800 + 7 * bn;
@@ -555,7 +559,7 @@ inline Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_c
   // Two accumulators to a tile: 1290 cycles a stage (630 us against 681 at
   // 8192^3, where the card's power sets the clock), and no tile's epilogue runs
   // under the next one's products.
-  if (!threads) {
+  if (!threads && allow_wide) {
     const uint32_t tiles = ceil_div(c.rows, 2 * kLanes) * ceil_div(c.cols, 512), rest = tiles % pairs;
     const bool halves = rest && 2 * rest <= pairs;
     const double rounds = tiles / pairs + (rest && !halves);
