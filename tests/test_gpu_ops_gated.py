@@ -125,6 +125,17 @@ def test_activations(arx, M, N, K, act):
     forward(arx, M, N, K, Q8, act, otype=BF, bias=False, z=False)
 
 
+# Tiles of 80 to 128 features on one accumulator and on two, whole and cut, with a last run of
+# 16 columns; the last round of tiles in halves.
+@pytest.mark.parametrize("M,N,K", [(3000, 776, 2048), (3000, 775, 2050), (1500, 792, 1024), (1500, 1920, 4096),
+                                   (1500, 1925, 4096), (3000, 1184, 4096), (3000, 1186, 4096), (3000, 1344, 4096),
+                                   (3000, 1181, 520), (3000, 800, 264), (4864, 1024, 2048)])
+@pytest.mark.parametrize("dtype", [BF, Q8], ids=str)
+def test_large_forms(arx, M, N, K, dtype):
+    forward(arx, M, N, K * (2 if dtype is Q8 else 1), dtype, "gelu", z=False, bias=False)
+    forward(arx, M, N, K * (2 if dtype is Q8 else 1), dtype, opad=1 if K == 264 else 0)
+
+
 @pytest.mark.parametrize("M,N,K", [(2, 72, 136), (5, 72, 136), (1300, 2600, 80)])
 @pytest.mark.parametrize("pad,lead,opad,olead", [(8, 8, 8, 8), (0, 1, 0, 0), (3, 0, 0, 0), (8, 0, 3, 1), (1, 3, 0, 4)])
 def test_strides_and_alignment(arx, M, N, K, pad, lead, opad, olead):

@@ -102,7 +102,8 @@ def test_forward_strides(arx, cols, pads):
 
 
 @pytest.mark.parametrize("rows,cols", [(609, 4096), (2433, 1024), (5000, 264), (1300, 8192), (1000, 4099), (700, 5000),
-                                       (3000, 2048), (9000, 256), (700, 16384)])
+                                       (3000, 2048), (9000, 256), (700, 16384), (2500, 4096), (2440, 5000), (2440, 8192),
+                                       (700, 8191), (100, 12001), (400, 12288), (2000, 500)])
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_forward_many_rows(arx, dtype, rows, cols):
     forward(arx, rows, cols, dtype, wdtype=F32, seed=rows)
@@ -146,6 +147,23 @@ def test_a_row_beyond_32_bit_squares(arx, cols):
     assert not bool(y.any()) and not bool(q.float().any()) and bool((s == 1).all())
 
 
+@pytest.mark.parametrize("cols", [4096, 8192, 5000])
+def test_in_place_through_the_ring(arx, cols):
+    x, r, w = make((2500, cols), BF, 1), make((2500, cols), BF, 2), make((cols,), BF, 3, 0.2, 1)
+    want_h, want_y = torch.empty_like(x), torch.empty_like(x)
+    arx.arx_rms_norm(x, want_y, residual=r, h=want_h, weight=w)
+    arx.arx_rms_norm(x, r, residual=r, h=x, weight=w)
+    assert torch.equal(r, want_y) and torch.equal(x, want_h)
+
+
+def test_h_without_a_residual_is_x(arx):
+    x = make((5, 1000), BF, 1)
+    h, y, want = (torch.empty_like(x) for _ in range(3))
+    arx.arx_rms_norm(x, y, h=h)
+    arx.arx_rms_norm(x, want)
+    assert torch.equal(h, x) and torch.equal(y, want)
+
+
 @pytest.mark.parametrize("cols", [1000, 4096, 4099, 20001])
 def test_in_place(arx, cols):
     x, r, w = make((7, cols), BF, 1), make((7, cols), BF, 2), make((cols,), BF, 3, 0.2, 1)
@@ -174,14 +192,18 @@ def test_reduce_forward(arx, W, cols):
         check([f64(t) for t in slots] + ([f64(r)] if res else []), f64(w), 1e-6, h, y, q, s, rstd)
 
 
-@pytest.mark.parametrize("rows,cols", [(700, 4096), (1300, 1024), (3000, 264), (400, 8192), (500, 4100)])
-@pytest.mark.parametrize("W", [2, 5, 8])
+@pytest.mark.parametrize("rows,cols", [(700, 4096), (1300, 1024), (3000, 264), (400, 8192), (500, 4100), (2500, 4096),
+                                       (2440, 5120), (800, 8192), (400, 12288), (700, 6001)])
+@pytest.mark.parametrize("W", [2, 4, 5, 8])
 def test_reduce_many_rows(arx, W, rows, cols):
     slots = [make((rows, cols), BF, 10 + k) for k in range(W)]
     r, w = make((rows, cols), BF, 1), make((cols,), BF, 2, 0.2, 1.0)
     h, y, q, s, rstd = Out((rows, cols), BF), Out((rows, cols), BF), OutQ(rows, cols), Out((rows,), F32), Out((rows,), F32)
     arx.arx_reduce_rms_norm(slots, h.t, y.t, residual=r, weight=w, q=q.t, scale=s.t, rstd=rstd.t)
     check([f64(t) for t in slots] + [f64(r)], f64(w), 1e-6, h, y, q, s, rstd)
+    h2, y2 = Out((rows, cols), BF), Out((rows, cols), BF)  # without q, which other kernels may take
+    arx.arx_reduce_rms_norm(slots, h2.t, y2.t, residual=r, weight=w)
+    check([f64(t) for t in slots] + [f64(r)], f64(w), 1e-6, h2, y2)
 
 
 def test_reduce_is_the_reduce_and_then_the_norm(arx):
@@ -253,7 +275,7 @@ def test_backward_strides(arx, cols, pads):
 
 
 @pytest.mark.parametrize("rows,cols", [(1300, 4096), (2600, 1024), (9000, 264), (700, 8192), (1000, 4099), (700, 5003),
-                                       (3000, 2048), (700, 16384), (200, 20001)])
+                                       (3000, 2048), (700, 16384), (200, 20001), (400, 12288), (400, 12001), (700, 8191)])
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_backward_many_rows(arx, dtype, rows, cols):
     backward(arx, rows, cols, dtype, wdtype=F32, seed=rows)
