@@ -136,6 +136,23 @@ def test_large_forms(arx, M, N, K, dtype):
     forward(arx, M, N, K * (2 if dtype is Q8 else 1), dtype, opad=1 if K == 264 else 0)
 
 
+@pytest.mark.parametrize("N", [5072, 5074])
+def test_a_last_round_of_tiles_in_halves(arx, N):
+    # Six rounds of whole tiles and 24 tiles more; compared on the GPU, row block by row block.
+    M, K = 6144, 8192
+    x, wg, wu = operands(M, N, K, BF)
+    out = Out((M, N), BF)
+    arx.arx_gated_linear(x, wg, wu, out.t)
+    out.check_guards()
+    for r in range(0, M, 1024):
+        X, W = x[r:r + 1024].double(), [t.double().t() for t in (wg, wu)]
+        (g, u), (eg, eu) = [X @ w for w in W], [chain(K) * (X.abs() @ w.abs()) for w in W]
+        f = g * torch.sigmoid(g)
+        want, err = f * u, (1.2 * eg + 24 * E * (1 + g.abs())) * (u.abs() + eu) + f.abs() * eu
+        off = (out.t[r:r + 1024].double() - want).abs() - err - U[BF] * want.abs() * (1 + 2 * U[BF]) - 2 * E * want.abs()
+        assert bool((off <= TINY[BF]).all())
+
+
 @pytest.mark.parametrize("M,N,K", [(2, 72, 136), (5, 72, 136), (1300, 2600, 80)])
 @pytest.mark.parametrize("pad,lead,opad,olead", [(8, 8, 8, 8), (0, 1, 0, 0), (3, 0, 0, 0), (8, 0, 3, 1), (1, 3, 0, 4)])
 def test_strides_and_alignment(arx, M, N, K, pad, lead, opad, olead):
