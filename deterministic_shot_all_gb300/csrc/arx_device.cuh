@@ -169,6 +169,19 @@ __device__ __forceinline__ bool in_range(const void* p, size_t bytes, const void
   } while (0)
 #endif
 
+// 16 bytes, zeros without `on`: predicated, as a load inside a branch is waited for
+// where the branch ends, and volatile, so that it stays ahead of what it is to
+// overlap with.
+__device__ __forceinline__ uint4 load_ahead16(const void* p, bool on) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@q ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"(uint32_t(on)) : "memory");
+  return v;
+}
+
 // Bulk prefetch of [p, p + bytes) into L2 (p 16-byte aligned, bytes a multiple
 // of 16).  A hint only: no data is returned and nothing is made visible.
 __device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {

@@ -216,18 +216,7 @@ __device__ __forceinline__ bool multiply_tile(const GemmArgs& a, Shared& s, uint
   return true;
 }
 
-// Loads of the residual, zero without `on`: predicated, as a load inside a
-// branch is waited for where the branch ends, and volatile, so that they stay
-// ahead of what they are to overlap with.
-__device__ __forceinline__ uint4 load_ahead16(const void* p, bool on) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@q ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"(uint32_t(on)) : "memory");
-  return v;
-}
+// As load_ahead16.
 __device__ __forceinline__ uint2 load_ahead8(const void* p, bool on) {
   uint2 v;
   asm volatile(

@@ -14,6 +14,11 @@ cudaError_t launch_reduce_rms_norm(const arx_reduce_rms_norm_args& c, bool vec, 
   a.rows = c.rows, a.cols = c.cols;
   a.ldx = a.ldresidual = a.ldh = a.ldy = c.cols, a.ldq = c.ldq;
   a.eps = c.eps, a.inv_cols = 1.0f / float(c.cols);
+  const auto place = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16; };
+  a.alike = place(c.weight) == 0;
+  for (const void* p : {c.residual, static_cast<const void*>(c.h), static_cast<const void*>(c.y)})
+    a.alike = a.alike && (!p || place(p) == place(c.slots[0]));
+  for (int r = 1; r < c.W; ++r) a.alike = a.alike && place(c.slots[r]) == place(c.slots[0]);
   switch (c.W) {
     case 1: return run_w<ARX_BF16, 1>(a, vec, st);
     case 2: return run_w<ARX_BF16, 2>(a, vec, st);

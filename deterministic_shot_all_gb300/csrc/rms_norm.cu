@@ -16,6 +16,12 @@ cudaError_t rms_norm(const arx_rms_norm_args& c, bool vec, cudaStream_t st) {
   a.rows = c.rows, a.cols = c.cols;
   a.ldx = c.ldx, a.ldresidual = c.ldresidual, a.ldh = c.ldh, a.ldy = c.ldy, a.ldq = c.ldq;
   a.eps = c.eps, a.inv_cols = 1.0f / float(c.cols);
+  // Contiguous matrices that begin alike.
+  const auto alike = [&](const void* p, uint64_t ld) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == reinterpret_cast<uintptr_t>(c.x) % 16 && (c.rows <= 1 || ld == c.cols));
+  };
+  a.alike = c.wdtype == c.dtype && reinterpret_cast<uintptr_t>(c.weight) % 16 == 0 && alike(c.x, c.ldx) &&
+            alike(c.residual, c.ldresidual) && alike(c.h, c.ldh) && alike(c.y, c.ldy);
   return run_w<D, 1>(a, vec, st);
 }
 

@@ -10,6 +10,8 @@
 
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "arx_internal.h"
 #include "norm.cuh"
 #include "ops_launch.h"
@@ -105,6 +107,7 @@ struct RmsArgs {
   uint64_t rows, cols, ldx, ldresidual, ldh, ldy, ldq;
   float eps, inv_cols;
   int wdtype, W;
+  bool alike;  // rows lie alike in every matrix, to their address modulo 16 bytes, and the weights are 16 bits on 16 bytes
 };
 
 // The terms of h at the V columns from c on of a row, and their sum before its
@@ -170,11 +173,17 @@ __device__ __forceinline__ void store_row(typename Elem<D>::S* p, uint32_t cols,
   }
 }
 
-// The rest of a row whose h is in `f` (columns past the end hold 0) and whose
-// weights are in `g`.  `buf`: 4 T / 32 words of the row's shared memory.
-template <int D, int T, int RPC, int NV, int V>
-__device__ __forceinline__ void finish_row(const RmsArgs<D>& a, size_t row, uint32_t cols, float (&f)[NV][V],
-                                           const float (&g)[NV][V], float* buf) {
+// rstd of a row whose h is in `f` and whose weights are in `g`, and, for q, what is
+// known of the largest |v|.  (Columns past the end hold 0 in f.)
+struct RowSums {
+  float rstd, most;
+  bool again;  // `most` is not it
+};
+// `buf`: 4 T / 32 words of the row's shared memory; store_h() stores f while the
+// sums are on their way.
+template <int D, int T, int RPC, int NV, int V, typename StoreH>
+__device__ __forceinline__ RowSums row_statistics(const RmsArgs<D>& a, const float (&f)[NV][V], const float (&g)[NV][V],
+                                                  float* buf, const StoreH& store_h) {
   float s = 0.0f, most = 0.0f;
   if constexpr (kPairs<D, V>) {
     Pair sum = pair(0.0f);
@@ -202,9 +211,18 @@ __device__ __forceinline__ void finish_row(const RmsArgs<D>& a, size_t row, uint
     }
   }
   uint32_t m = __float_as_uint(most);  // not negative
-  if (a.h) store_row<D, T, NV, V>(a.h + row * a.ldh, cols, f);
+  if (a.h) store_h();
   row_sum_max<T, RPC>(s, m, buf);
-  const float rstd = 1.0f / sqrtf(s * a.inv_cols + a.eps);
+  RowSums r;
+  r.rstd = 1.0f / sqrtf(s * a.inv_cols + a.eps);
+  r.most = 0.0f, r.again = false;
+  if (a.q) r.most = row_most(m, r.rstd, r.again);
+  return r;
+}
+
+// f = f rstd g.
+template <int D, int NV, int V>
+__device__ __forceinline__ void normalise_row(float (&f)[NV][V], const float (&g)[NV][V], float rstd) {
   scale_row<D, NV, V>(f, rstd);
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -215,23 +233,34 @@ __device__ __forceinline__ void finish_row(const RmsArgs<D>& a, size_t row, uint
       else
         f[i][k] *= g[i][k];
     }
+}
+
+// The largest |v| of the row, v in `f` (columns past the end hold 0).
+template <int T, int RPC, int NV, int V>
+__device__ __forceinline__ float largest(const RowSums& r, const float (&f)[NV][V], float* buf) {
+  if (!r.again) return r.most;
+  uint32_t m = 0;
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) m = max(m, magnitude(f[i][k]));
+  row_sum_max<T, RPC>(s, m, buf + 2 * (T / 32));
+  return __uint_as_float(m);
+}
+
+// The rest of a row.
+template <int D, int T, int RPC, int NV, int V>
+__device__ __forceinline__ void finish_row(const RmsArgs<D>& a, size_t row, uint32_t cols, float (&f)[NV][V],
+                                           const float (&g)[NV][V], float* buf) {
+  const RowSums sums = row_statistics<D, T, RPC, NV, V>(
+      a, f, g, buf, [&] { store_row<D, T, NV, V>(a.h + row * a.ldh, cols, f); });
+  normalise_row<D, NV, V>(f, g, sums.rstd);
   float scale = 0.0f;
   if (a.q) {
-    bool again;
-    most = row_most(m, rstd, again);
-    if (again) {
-      m = 0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (row_col<T, V>(i) < cols)
-#pragma unroll
-          for (int k = 0; k < V; ++k) m = max(m, magnitude(f[i][k]));
-      row_sum_max<T, RPC>(s, m, buf + 2 * (T / 32));
-      most = __uint_as_float(m);
-    }
     if (a.y) store_row<D, T, NV, V>(a.y + row * a.ldy, cols, f);
     float inverse;
-    scale = row_scale(most, inverse);
+    scale = row_scale(largest<T, RPC, NV, V>(sums, f, buf), inverse);
     scale_row<D, NV, V>(f, inverse);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -243,7 +272,7 @@ __device__ __forceinline__ void finish_row(const RmsArgs<D>& a, size_t row, uint
   }
   if (threadIdx.x % T == 0) {
     if (a.q) a.scale[row] = scale;
-    if (a.rstd) a.rstd[row] = rstd;
+    if (a.rstd) a.rstd[row] = sums.rstd;
   }
 }
 
@@ -338,6 +367,119 @@ __global__ void __launch_bounds__(T* RPC, kRingBlocks<T, RPC>)
     at = at + 1 == kRing ? 0 : at + 1;
   }
   cp_async_wait<0>();
+}
+
+// Rows off 16 bytes that lie alike in every matrix (contiguous ones of one shape):
+// a thread takes the 8 elements of an aligned unit, whichever columns those are,
+// so that all but a row's two end units move 16 bytes at a time.  `off`: elements
+// of the row's first unit before the row.  The weights, which begin on 16 bytes,
+// are the halves of two units, shifted by `off`.
+struct Span {
+  int c0, cols;  // first column (negative in the first unit), of how many
+  __device__ __forceinline__ bool whole() const { return c0 >= 0 && c0 + 8 <= cols; }
+  __device__ __forceinline__ bool has(int k) const { return c0 + k >= 0 && c0 + k < cols; }
+  __device__ __forceinline__ bool any() const { return c0 < cols; }  // off < 8: no unit ends before the row
+};
+
+template <int D>
+__device__ __forceinline__ void load_span(Pack<D, 8>& p, const uint16_t* row, const Span& s) {
+  if (s.whole()) {
+    p.load(row + s.c0);
+  } else {
+    p.zero();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s.has(k)) p.w[k / 2] |= uint32_t(row[s.c0 + k]) << (k % 2 * 16);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store_span(uint16_t* row, const float (&f)[8], const Span& s) {
+  Pack<D, 8> p;
+  p.set(f);
+  if (s.whole()) {
+    p.store(row + s.c0);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s.has(k)) row[s.c0 + k] = uint16_t(p.w[k / 2] >> (k % 2 * 16));
+  }
+}
+
+// 8 parameters of a 16-bit type from column c0 on, where c0 + off is a multiple of 8:
+// taken out of the two aligned units around them; 1 without any.
+template <int D>
+__device__ __forceinline__ void span_params(const void* p, uint32_t off, const Span& s, float (&g)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = 1.0f;
+  if (!p || !s.any()) return;
+  const uint16_t* w = static_cast<const uint16_t*>(p);
+  const int u = s.c0 + int(off);
+  if (u >= 8 && u + 8 <= s.cols) {
+    const uint4 a = *reinterpret_cast<const uint4*>(w + u - 8), b = *reinterpret_cast<const uint4*>(w + u);
+    uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    // 8 - off elements on, in words by powers of two and then half a word.
+    const uint32_t by = 8 - off;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = by & 8 ? v[i + 4] : v[i];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = by & 4 ? v[i + 2] : v[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = by & 2 ? v[i + 1] : v[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Elem<D>::widen2(__funnelshift_r(v[i], v[i + 1], (by & 1) * 16), g[2 * i], g[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s.has(k)) g[k] = Elem<D>::widen(w[s.c0 + k]);
+  }
+}
+
+template <int D, int W, int T, int NV>
+__global__ void __launch_bounds__(T) rms_span_kernel(const __grid_constant__ RmsArgs<D> a) {
+  __shared__ float buf[4 * (T / 32)];
+  dependent_launch_prologue();
+  const size_t row = blockIdx.x, at = row * a.cols;
+  const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(a.slot[0] + at) & 15) / 2;
+  Span s[NV];
+  float f[NV][8], g[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    s[i] = {int((i * T + threadIdx.x) * 8) - int(off), int(a.cols)};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[i][k] = 0.0f;
+    if (!s[i].any()) continue;
+    Terms<D, W, 8> t;
+#pragma unroll
+    for (int w = 0; w < W; ++w) load_span<D>(t.p[w], a.slot[w] + at, s[i]);
+    if (a.residual) load_span<D>(t.r, a.residual + at, s[i]);
+    t.sum(a, f[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) span_params<D>(a.weight, off, s[i], g[i]);
+  const RowSums sums = row_statistics<D, T, 1, NV, 8>(a, f, g, buf, [&] {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (s[i].any()) store_span<D>(a.h + at, f[i], s[i]);
+  });
+  normalise_row<D, NV, 8>(f, g, sums.rstd);
+  if (a.y) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (s[i].any()) store_span<D>(a.y + at, f[i], s[i]);
+  }
+  if (a.q) {
+    float inverse;
+    const float scale = row_scale(largest<T, 1, NV, 8>(sums, f, buf), inverse);
+    scale_row<D, NV, 8>(f, inverse);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (s[i].has(k)) a.q[row * a.ldq + s[i].c0 + k] = uint8_t(round_e4m3x2(f[i][k], 0.0f));
+    if (threadIdx.x == 0) a.scale[row] = scale;
+  }
+  if (threadIdx.x == 0 && a.rstd) a.rstd[row] = sums.rstd;
 }
 
 // Any row length: one block per row, h computed anew in each pass and stored,
@@ -440,6 +582,10 @@ cudaError_t run_ring(const RmsArgs<D>& a, bool* done, cudaStream_t st) {
 // from 305 rows on (8191: 2,432 rows 42 against 56 us, 152: 3.9 against 3.6), else
 // 1024 (4 ranks 1.7 times as long with 512); up to 16384 columns 1024 up to 304 rows
 // (152 rows of 12001: 5.3 against 10.3 us), above, two passes over the row are as fast.
+// By units that lie alike, time by that of elements, above 5120 columns: one rank .7
+// to 1.0, two .6 to .9, four to eight .55 to .85 (608 rows of 16001, four ranks: 70.7
+// against 37.9 us; 2,432 of 8181: 117 against 68); up to 5120, whose elements fewer
+// threads have in flight together, .75 to 2.
 template <int D, int W>
 cudaError_t run_w(const RmsArgs<D>& a, bool vec, cudaStream_t st) {
   const uint64_t n = a.cols;
@@ -472,6 +618,12 @@ cudaError_t run_w(const RmsArgs<D>& a, bool vec, cudaStream_t st) {
       return run<D, W, 512, 1, 4, 8>(a, st);
     }
   } else {
+    if constexpr (D != ARX_F32)
+      if (a.alike && n > 5120) {  // (a row may begin 7 elements into its first unit)
+        const dim3 grid(unsigned(a.rows));
+        if (n + 7 <= 8192) return launch_op(rms_span_kernel<D, W, 512, 2>, grid, 512, 0, st, a);
+        if (n + 7 <= 16384) return launch_op(rms_span_kernel<D, W, 1024, 2>, grid, 1024, 0, st, a);
+      }
     if (n <= 256) return run<D, W, 32, 4, 8, 1>(a, st);
     if (n <= 512 && a.rows > 8 * kSms) return run<D, W, 64, 1, 8, 1>(a, st);
     if (n <= 1024) return run<D, W, 128, 1, 8, 1>(a, st);

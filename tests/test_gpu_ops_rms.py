@@ -101,6 +101,23 @@ def test_forward_strides(arx, cols, pads):
     forward(arx, 4, cols, F32, wdtype=F32, pads=pads, lead=1)
 
 
+@pytest.mark.parametrize("cols", [6001, 12001])
+def test_16_bit_rows_that_leave_the_range(arx, cols):
+    # As above, in bf16 and by units that lie alike: zeros, tiny numbers, NaN, and an infinity.
+    x, w = make((5, cols), BF, 1), make((cols,), BF, 2, 0.2, 1.0)
+    x[0], x[1] = 0.0, x[1] * 2.0 ** -100
+    y, q, s = Out(x.shape, BF), OutQ(*x.shape), Out((5,), F32)
+    arx.arx_rms_norm(x, y.t, weight=w, q=q.t, scale=s.t)
+    check([f64(x)], f64(w), 1e-6, None, y, q, s)
+    assert float(s.t[0]) == 1.0 and not bool(q.t[0].float().any())
+    x[2, cols - 1], x[3, 0] = float("nan"), float("inf")
+    arx.arx_rms_norm(x, y.t, weight=w, q=q.t, scale=s.t)
+    for row in (2, 3):
+        assert bool(torch.isnan(s.t[row])) and bool(torch.isnan(q.t[row].float()).all())
+    assert bool(torch.isnan(y.t[2]).all()) and bool(torch.isnan(y.t[3, 0])) and not bool(y.t[3, 1:].any())
+    assert bool(torch.isfinite(y.t[4]).all()) and bool(torch.isfinite(s.t[4]))
+
+
 @pytest.mark.parametrize("rows,cols", [(609, 4096), (2433, 1024), (5000, 264), (1300, 8192), (1000, 4099), (700, 5000),
                                        (3000, 2048), (9000, 256), (700, 16384), (2500, 4096), (2440, 5000), (2440, 8192),
                                        (700, 8191), (100, 12001), (400, 12288), (2000, 500)])
@@ -164,7 +181,17 @@ def test_h_without_a_residual_is_x(arx):
     assert torch.equal(h, x) and torch.equal(y, want)
 
 
-@pytest.mark.parametrize("cols", [1000, 4096, 4099, 20001])
+@pytest.mark.parametrize("lead", range(8))
+@pytest.mark.parametrize("cols", [6000, 8177, 8185, 9001])
+def test_units_that_lie_alike(arx, cols, lead):
+    # Contiguous matrices that begin `lead` elements after 16 bytes, with weights on 16 bytes, whole
+    # units or not; and one that begins elsewhere.
+    forward(arx, 3, cols, BF, wdtype=BF, lead=lead)
+    forward(arx, 4, cols, torch.float16, wdtype=torch.float16, lead=lead, res=False, form="y")
+    forward(arx, 2, cols, BF, wdtype=BF, lead=lead, pads=(0, 1, 0, 0, 0))
+
+
+@pytest.mark.parametrize("cols", [1000, 4096, 4099, 6001, 12001, 20001])
 def test_in_place(arx, cols):
     x, r, w = make((7, cols), BF, 1), make((7, cols), BF, 2), make((cols,), BF, 3, 0.2, 1)
     want_h, want_y = torch.empty_like(x), torch.empty_like(x)
@@ -223,7 +250,7 @@ def test_reduce_is_the_reduce_and_then_the_norm(arx):
     assert torch.equal(bits(q[0]), bits(q[1]))
 
 
-@pytest.mark.parametrize("cols", [1000, 4096, 4099, 20001])
+@pytest.mark.parametrize("cols", [1000, 4096, 4099, 6001, 12001, 20001])
 def test_reduce_in_place(arx, cols):
     slots, r, w = [make((5, cols), BF, k) for k in range(3)], make((5, cols), BF, 9), make((cols,), BF, 8, 0.2, 1)
     want = torch.empty_like(r), torch.empty_like(r)
