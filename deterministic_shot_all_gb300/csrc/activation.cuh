@@ -165,4 +165,54 @@ __device__ __forceinline__ void multiply_activation_grad(float (&f)[N], const fl
   }
 }
 
+// f[i] *= act'(z[i]), h[i] *= act(z[i]), with what the two have in common worked out
+// once.
+template <int N>  // even
+__device__ __forceinline__ void multiply_activation_both(float (&f)[N], float (&h)[N], const float (&z)[N], int act) {
+  switch (act) {
+    case ARX_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        f[i] = z[i] > 0.0f ? f[i] : 0.0f;
+        h[i] *= z[i] < 0.0f ? 0.0f : z[i];
+      }
+      break;
+    case ARX_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const Pair a = pair(min_nan(fabsf(z[i]), 30.0f), min_nan(fabsf(z[i + 1]), 30.0f));
+        Pair e, tail;
+        normal_tail(a, e, tail);
+        float s0, s1, v0, v1;
+        halves(fma2(tail, pair(-1.0f), fma2(a * pair(kInvSqrt2Pi), e, pair(0.5f))), s0, s1);
+        halves(fma2(a * pair(-1.0f), tail, pair(max_nan(z[i], 0.0f), max_nan(z[i + 1], 0.0f))), v0, v1);
+        f[i] *= 0.5f + copysignf(s0, z[i]);
+        f[i + 1] *= 0.5f + copysignf(s1, z[i + 1]);
+        h[i] *= v0, h[i + 1] *= v1;
+      }
+      break;
+    case ARX_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        constexpr float k = -2.0f * kLog2E * kSqrt2OverPi;
+        const float s = logistic2(z[i] * fmaf(k * kGeluCubic, z[i] * z[i], k)), w = s * (1.0f - s);
+        f[i] *= s + (w == 0.0f ? 0.0f : z[i] * w * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * kGeluCubic * z[i] * z[i]));
+        h[i] *= max_nan(z[i], -FLT_MAX) * s;
+      }
+      break;
+    case ARX_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float s = logistic(z[i]), w = s * (1.0f - s);
+        f[i] *= s + (w == 0.0f ? 0.0f : z[i] * w);
+        h[i] *= max_nan(z[i], -FLT_MAX) * s;
+      }
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < N; ++i) h[i] *= z[i];
+      break;
+  }
+}
+
 }  // namespace arx
