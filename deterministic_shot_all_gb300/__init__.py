@@ -22,6 +22,9 @@ Functions keep the C names:
   for the flags and reduces.
 * ``arx_linear / arx_dropout_add / arx_layer_norm``, their ``_bwd`` forms and
   ``arx_reduce_layer_norm``: the operators around a sublayer's all-reduce.
+* ``arx_rms_norm / arx_gated_linear``, their ``_bwd`` forms and ``arx_reduce_rms_norm``:
+  those of a sublayer with a root-mean-square norm and a gated feed-forward block, in 16
+  bits or, for serving, with 8-bit operands and scales.
 """
 
 from __future__ import annotations

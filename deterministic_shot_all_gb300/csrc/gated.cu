@@ -8,15 +8,20 @@
 // with scales of x's rows and the weights' rows, at twice the rate; a stage of
 // the ring is 128 bytes of contraction either way.
 //
-// Three forms, chosen as in linear.cu (choose_form, with 2 N columns):
+// Three forms, chosen by estimates of their time (choose_gated_form; for one or two
+// rows by sizes, dot_units):
 //  vector one or two rows: dot products on the CUDA cores, a warp taking a
-//         feature of both weights;
+//         feature of both weights (one token, 4096 -> 2048: 6.0 us, 5.6 TB/s);
 //  wide   persistent pairs of blocks.  The tensor cores' B operand is split over
 //         the pair: the first block brings in rows of Wg, the second the same rows
-//         of Wu, and an accumulator's first half is g, its second u;
+//         of Wu, and an accumulator's first half is g, its second u (8185 tokens,
+//         4096 -> 4096 bf16, both projections kept: 328 to 337 us, 1.6 PFLOP/s, and
+//         e4m3, 1024 of 8192 -> 8192: 83 to 85 us, 3.3 PFLOP/s, while the card is
+//         cool; back to back 343 and 96, bound by the card's power);
 //  split  for few tokens: 64 features' rows of Wg and of Wu take the 128
 //         accumulator lanes, the tokens the instruction's N, and a cluster of up to
-//         8 blocks splits the contraction.
+//         8 blocks splits the contraction (e4m3, 32 of 8192 -> 4096: 15.3 us, of
+//         which about 4 are the set-up and the join and the rest the weights' bytes).
 // 16-bit operands off 16 bytes are copied to aligned rows first (realign.cu),
 // but for one or two rows of small weights, which are read element by element.
 #include <cuda_runtime.h>

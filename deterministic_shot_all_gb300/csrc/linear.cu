@@ -16,6 +16,9 @@
 // loaded by 512 more threads into the same swizzled stages, beside four
 // epilogue warps, 18 bytes a cycle into an SM where the copy engine brings 50.
 //
+// The parts that the gated block's products (gated.cu) share are in gemm.cuh; its
+// backward pass also takes two products in one launch of these kernels (Extra).
+//
 // Every wait on a barrier is bounded (tensor_core.cuh); a block whose wait ran
 // out sets the call's status word, waits for what it has in flight (drain_block),
 // leaves NaN in the outputs that it did not finish, and ends.
