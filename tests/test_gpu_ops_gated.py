@@ -431,3 +431,39 @@ def test_a_wait_that_runs_out_ends_with_a_status(arx, form):
         arx.arx_gated_linear(x, wg, wu, out, act=arx.ARX_ACT_RELU, status=status, **scale)
         torch.cuda.synchronize()
         assert int(status) == 0 and bool((out == value).all())
+
+
+# M, N, K and the gradients asked for: dx as one sum over both projections, and both weights'
+# gradients in one launch, in the split form and over pairs.
+BACKWARD_FORMS = {"dx_split": (64, 1 << 20, 128, "x"), "dx_pairs": (2000, 1 << 17, 2000, "x"),
+                  "dw_split": (1 << 20, 64, 64, "gu"), "dw_pairs": (1 << 18, 1500, 2000, "gu")}
+
+
+@pytest.mark.parametrize("form", BACKWARD_FORMS)
+def test_a_gradients_wait_that_runs_out(arx, form):
+    M, N, K, what = BACKWARD_FORMS[form]
+    ones = lambda r, c: torch.ones(r, c, dtype=BF, device="cuda")  # noqa: E731
+    d, x, w = ones(M, N), ones(M, K), ones(N, K)
+    outs = {"dx": torch.full((M, K), 3.0, dtype=BF, device="cuda")} if what == "x" else \
+        {n: torch.full((N, K), 3.0, dtype=BF, device="cuda") for n in ("dw_gate", "dw_up")}
+    value = 2.0 * N if what == "x" else float(M)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(arx.arx_gated_linear_bwd_workspace_bytes(M, N), dtype=torch.uint8, device="cuda")
+    call = lambda **kw: arx.arx_gated_linear_bwd(d, x, w, w, d, d, act=arx.ARX_ACT_NONE, workspace=ws, status=status,  # noqa: E731
+                                                 **outs, **kw)
+    call(wait_us=100)
+    torch.cuda.synchronize()
+    assert int(status) & 0xFF == arx.ARX_ETIMEOUT
+    some = False
+    for o in outs.values():
+        nan = torch.isnan(o)
+        some |= bool(nan.any())
+        assert bool((o[~nan] == value).all())
+    assert some
+    for _ in range(2):
+        status.zero_()
+        for o in outs.values():
+            o.zero_()
+        call()
+        torch.cuda.synchronize()
+        assert int(status) == 0 and all(bool((o == value).all()) for o in outs.values())
