@@ -640,31 +640,40 @@ GatedCopies copies_of(const arx_gated_linear_args& c) {
   return r;
 }
 
-// The split form's estimate is choose_form's.  The wide form's tiles are 64 to 128
+// The split form's estimate is choose_form's, with 20 cycles more for a token that a
+// block of 256 stores alone (both sums and the activation, and no second block on the
+// SM to work meanwhile; e4m3 [512, 1024] x [1024, 4096]: 20.2 us, the wide form 10.1)
+// and a part of it where a cluster shares them.  The wide form's tiles are 64 to 128
 // features (bn / 2) to an accumulator, so that the last round of tiles is full: of
 // e4m3 [1024, 8192] x [8192, 8192], two accumulators, 152 pairs of tiles in two
 // rounds of 76 take 91.7 us with 128 features, and 148 of 112 84.4 (one
 // accumulator, four rounds: 90.1, 89.0).  Measured, cycles of a stage: 600
 // for one accumulator of 256 columns, bound by the copies (55 bytes a cycle into
-// an SM), 580 for one of 224; 4.25 a column of two, bound by the products (4.2);
-// what is outside the stages of a round with two accumulators, whose epilogue no
-// products hide, 12500, and 2900 for each projection that is kept.
+// an SM, more while few pairs are at work and less for the shorter copies of narrow
+// tiles), 580 for one of 224; 4.25 a column of two, bound by the products (4.2).
+// What is outside the stages: with one accumulator 10500 (256 tokens of 64 -> 4096: 5.9
+// us) and, until the rings are full, up to 5500 when all pairs ask at once; 12500 for
+// a round with two, whose epilogue no products hide; and 2900 for each projection that
+// is kept.
 Form choose_gated_form(const arx_gated_linear_args& c, uint32_t steps) {
   GemmCall shape{};
   shape.rows = c.M, shape.cols = 2 * c.N, shape.k = c.K;
-  Form best = choose_form(shape, steps, true, true, false);
+  Form best = choose_form(shape, steps, true, true, false, 20);
   constexpr uint32_t pairs = 152 / 2;
   const double kept = 2900.0 * ((c.z_gate != nullptr) + (c.z_up != nullptr));
   best.cycles += kept;
   for (uint32_t bn = 256; bn >= 128; bn -= 32)
     for (uint32_t subs = 1; subs <= 2; ++subs) {
       const uint32_t tiles = ceil_div(c.M, 2 * kLanes) * ceil_div(c.N, subs * bn / 2), rest = tiles % pairs;
-      const double engine = (64 - 10.0 * (tiles < pairs ? tiles : pairs) / pairs) * (bn < 192 ? 0.86 : 1);
+      const double at_work = double(tiles < pairs ? tiles : pairs) / pairs;
+      const double engine = bn >= 224 ? 64 - 10 * at_work : bn >= 192 ? 54 : 46;
       const double copies = (kLanes + bn / 2) * 128.0 / engine, one = copies > 2.1 * bn ? copies : 2.1 * bn;
       double cycles;
       if (subs == 1) {
         const double tile = steps * one, epilogue = 4000 + kept;
-        cycles = ceil_div(tiles, pairs) * (tile > epilogue ? tile : epilogue) + 18000 + kept;
+        const double fill = steps < 6 ? steps / 6.0 : 1;
+        cycles = tile + (ceil_div(tiles, pairs) - 1) * (tile > epilogue ? tile : epilogue) + 10500 +
+                 5500 * at_work * fill + kept;
       } else {
         const double all = (kLanes + bn) * 128.0 / 46, two = all > 4.25 * bn ? all : 4.25 * bn;
         const bool halves = rest && 2 * rest <= pairs;

@@ -516,8 +516,10 @@ struct Form {
   double cycles;
 };
 
-// (allow_wide: false leaves the wide forms out.)
-inline Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, bool allow_wide = true) {
+// (allow_wide: false leaves the wide forms out; join_more: cycles more for a row of Q
+// that a split block joins and stores.)
+inline Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_copy, bool allow_wide = true,
+                        double join_more = 0) {
   constexpr uint32_t sms = 152;
   Form best{};
   const auto consider = [&](const Form& f) {
@@ -563,7 +565,7 @@ inline Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_c
       // cluster over.
       const uint32_t at_once = two ? (split == 8 ? 36 : split == 4 ? 72 : 2 * sms / split)
                                    : (split == 8 ? 14 : split == 4 ? 36 : sms / split);
-      const double join = (split == 8 ? 40 : split > 1 ? 30 : 25) * bn;
+      const double join = ((split == 8 ? 40 : split > 1 ? 30 : 25) + (two ? 0 : join_more / split)) * bn;
       const uint32_t rounds = ceil_div(tiles, at_once);
       const double on_sm = !two ? rounds : rounds > 1 ? 2 * rounds : ceil_div(uint64_t(tiles) * split, sms);
       const double engine = two && on_sm > 1 ? 66 : bn > 128 ? 55 : 41;
