@@ -36,7 +36,7 @@ SOURCES = ["reduce.cu", "step.cu", "abi.cu", "step_noalloc.cu", "external.cu", "
            "gated.cu", "gated_grad.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("arx_device.cuh", "arx_internal.h", "arx_rows.cuh", "norm.cuh",
                                            "activation.cuh", "tensor_core.cuh", "ops_launch.h", "spans.h",
-                                           "ops_check.h", "rms_norm.cuh", "gemm.cuh", "tiles.cuh", "pairs.cuh")] + [
+                                           "ops_check.h", "rms_norm.cuh", "gemm.cuh", "forms.h", "tiles.cuh", "pairs.cuh")] + [
     os.path.join(INCLUDE, "arx.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -680,7 +680,7 @@ Form choose_gated_form(const arx_gated_linear_args& c, uint32_t steps) {
         cycles = (tiles / pairs + (rest && !halves)) * (steps * two + 12500 + kept) +
                  (halves ? steps * one * 1.25 + 8000 + kept : 0) + 11000;
       }
-      if (cycles < best.cycles) best = {true, bn, 1, subs, cycles};
+      if (cycles < best.cycles) best = {true, bn, 1, subs, tiles, cycles};
     }
   return best;
 }

@@ -798,9 +798,7 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
   if (!cp_copy) bits |= reinterpret_cast<uintptr_t>(cp) | (cp_rows > 1 ? c.ldp * 2 : 0);
   if (!cq_copy) bits |= reinterpret_cast<uintptr_t>(cq) | (cq_rows > 1 ? c.ldq * 2 : 0);
   const uint32_t word = cp_copy && cq_copy ? 16 : bits % 8 == 0 ? 8 : 2;
-  GemmCall shape = c;
-  if (stack) shape.rows *= 2;
-  const Form form = choose_form(shape, a.steps, cp_copy, cq_copy);
+  const Form form = choose_form(c, a.steps, cp_copy, cq_copy);
   const bool wide = form.wide;
   a.bn = form.bn;
   a.split = form.split;
@@ -818,13 +816,10 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t st) {
     a.tmem_columns = a.bn < 32 ? 32 : a.bn;
   }
   const uint32_t lanes = wide ? 2 * kLanes : kLanes;
-  a.tiles_p = ceil_div(a.P, lanes);
-  a.tiles_q = ceil_div(a.Q, form.subs * a.bn);
-  if (stack) {
-    uint32_t& tiles = wide ? a.tiles_p : a.tiles_q;
-    a.tiles_first = tiles;
-    tiles *= 2;
-  }
+  const Tiles tiles = tiles_of(c, wide, a.bn, form.subs);
+  a.tiles_p = wide ? tiles.rows : tiles.cols;
+  a.tiles_q = wide ? tiles.cols : tiles.rows;
+  a.tiles_first = tiles.rows / 2;  // of two stacked products
   a.stage_bytes = kPBytes + form.subs * a.bq * 128;
   a.stages = (word != 16 ? kLoadedBudget : wide || a.bn > 128 ? kStageBudget : kSplitBudget) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
