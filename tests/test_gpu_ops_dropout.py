@@ -185,3 +185,15 @@ def test_offsets_past_32_bits(arx):
     got = torch.empty_like(x)
     arx.arx_dropout_add_bwd(far, got, 0.5, rng(1, 1))
     assert torch.equal(bits(got), bits(want))
+
+
+@pytest.mark.parametrize("rows", [1, 256, 8192, 32768, 32769, 65536, 81921, 116736])
+def test_bias_gradient_over_few_and_many_partial_sums(arx, rows):
+    # 1 to 456 partial rows, to either side of the 128 up to which they are added in a plain loop;
+    # whole numbers, whose sums stay below 2^24, so that every order gives the same.
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    d = torch.randint(-8, 9, (rows, 8), generator=g, device="cuda").float()
+    db = Out((8,), torch.float32)
+    arx.arx_dropout_add_bwd(d, None, 0.0, dbias=db.t, workspace=scratch(arx.arx_dropout_add_bwd_workspace_bytes(rows, 8)))
+    db.check_guards()
+    assert torch.equal(db.t.double(), d.double().sum(0))
