@@ -236,16 +236,18 @@ __device__ __forceinline__ void normalise_row(float (&f)[NV][V], const float (&g
     }
 }
 
-// The largest |v| of the row, v in `f` (columns past the end hold 0).
-template <int T, int RPC, int NV, int V>
-__device__ __forceinline__ float largest(const RowSums& r, const float (&f)[NV][V], float* buf) {
+// The largest |v| of the row, v in `f`; has(i, k): is f[i][k] a column of the row?  (Those
+// past its end hold 0 times rstd, which is NaN where rstd is infinite.)
+template <int T, int RPC, int NV, int V, typename Has>
+__device__ __forceinline__ float largest(const RowSums& r, const float (&f)[NV][V], float* buf, const Has& has) {
   if (!r.again) return r.most;
   uint32_t m = 0;
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int k = 0; k < V; ++k) m = max(m, magnitude(f[i][k]));
+    for (int k = 0; k < V; ++k)
+      if (has(i, k)) m = max(m, magnitude(f[i][k]));
   row_sum_max<T, RPC>(s, m, buf + 2 * (T / 32));
   return __uint_as_float(m);
 }
@@ -261,7 +263,7 @@ __device__ __forceinline__ void finish_row(const RmsArgs<D>& a, size_t row, uint
   if (a.q) {
     if (a.y) store_row<D, T, NV, V>(a.y + row * a.ldy, cols, f);
     float inverse;
-    scale = row_scale(largest<T, RPC, NV, V>(sums, f, buf), inverse);
+    scale = row_scale(largest<T, RPC, NV, V>(sums, f, buf, [&](int i, int) { return row_col<T, V>(i) < cols; }), inverse);
     scale_row<D, NV, V>(f, inverse);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(T) rms_span_kernel(const __grid_constant__ Rms
   }
   if (a.q) {
     float inverse;
-    const float scale = row_scale(largest<T, 1, NV, 8>(sums, f, buf), inverse);
+    const float scale = row_scale(largest<T, 1, NV, 8>(sums, f, buf, [&](int i, int k) { return s[i].has(k); }), inverse);
     scale_row<D, NV, 8>(f, inverse);
 #pragma unroll
     for (int i = 0; i < NV; ++i)

@@ -119,3 +119,23 @@ def test_reduce_begins_anywhere(arx, W, cols, leads):
 def test_reduce_of_many_rows_begins_anywhere(arx, W, rows, cols, leads):
     for form in ("y", "q"):
         reduce(arx, W, rows, cols, leads, form)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+@pytest.mark.parametrize("cols", [8, 200, 1000, 1024, 4096, 4099, 6001, 8192, 8200, 12001, 20001])
+def test_a_row_whose_squares_vanish_without_eps(arx, cols, dtype):
+    # Squares below 2^-149 add nothing: rstd is infinite, and so are y and the scale of a row
+    # without zeros (columns that no element stands for, past the row's end, do not count).
+    x = torch.full((3, cols), 1e-30, device="cuda").to(dtype)
+    x[1] *= -1
+    for form in ("both", "q"):
+        y, q, s, rstd = torch.empty_like(x), rms.OutQ(3, cols), Out((3,), F32), Out((3,), F32)
+        arx.arx_rms_norm(x, y if form == "both" else None, q=q.t, scale=s.t, rstd=rstd.t, eps=0.0)
+        assert bool((rstd.t == float("inf")).all()) and bool((s.t == float("inf")).all())
+        assert bool(torch.isnan(q.t.float()).all())
+        if form == "both":
+            assert bool((y[::2] == float("inf")).all()) and bool((y[1] == float("-inf")).all())
+    x[2, cols // 2] = 0.0  # 0 times infinity
+    q, s = rms.OutQ(3, cols), Out((3,), F32)
+    arx.arx_rms_norm(x, None, q=q.t, scale=s.t, eps=0.0)
+    assert bool(torch.isnan(s.t[2])) and bool((s.t[:2] == float("inf")).all())
