@@ -87,8 +87,8 @@ __device__ __forceinline__ float row_scale(float most, float& inverse) {
 }
 
 // The largest |v| = |h rstd weight| from the largest |h weight|, which is known
-// with the sum of squares, by the same barrier: within a rounding of it while
-// both are normal numbers.  Else (a row of zeros, of values whose squares leave
+// with the sum of squares, by the same barrier: two products in another order,
+// within 4 2^-24 of each other while both are normal numbers.  Else (a row of zeros, of values whose squares leave
 // the range, with infinities or NaN) `again` says that it has to be taken anew.
 __device__ __forceinline__ float row_most(uint32_t m, float rstd, bool& again) {
   const float p = __uint_as_float(m);

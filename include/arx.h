@@ -717,7 +717,10 @@ arx_status arx_reduce_layer_norm(const arx_reduce_layer_norm_args* a, void* stre
  * the norm taken of h before its rounding.  y is v; q is v in 8 bits (e4m3),
  * with a scale for each row:
  *   scale = max |v| / 448, or 1 where that is below 2^-126,  q = e4m3(v / scale),
- * rounded to nearest even and never above 448, the type's largest number.  A row
+ * rounded to nearest even and never above 448, the type's largest number.  (Worked
+ * out in fp32: max |v| may be taken as max |h * weight| * rstd, so that scale is
+ * within four roundings, 2^-22 of it, of this, and q is rounded from v times 1 / scale,
+ * so that within as much of the middle between two numbers it may be either.)  A row
  * with a NaN has a NaN scale and NaN in all of q.
  *   x         [rows, cols] of `dtype`
  *   residual  [rows, cols], or NULL for 0

@@ -398,3 +398,19 @@ def test_offsets_beyond_32_bits(arx):
     arx.arx_rms_norm_bwd(dy, x, rstd, dx.t)
     want, _ = plain.rms_norm_bwd(f64(dy), f64(x), f64(rstd))
     assert_close(dx, want, 100 * E * (np.abs(want) + np.abs(f64(x)) * np.abs(f64(dy)).mean()), "dx")
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 200), (700, 1000), (40, 4096), (5, 4099), (40, 8192), (3, 12288), (3, 20001)])
+def test_scale_and_q_are_the_definition_s_to_within_four_roundings(arx, rows, cols):
+    # Of v = x rstd weight in 64 bits, from the rstd that was returned: the scale is within 4 2^-24 of
+    # max |v| / 448, and q lies between the roundings of v / scale to either side (one 2^-24 more: the
+    # way to 8 bits leads through 32).
+    x, w = make((rows, cols), F32, rows), make((cols,), F32, 2, 0.2, 1.0)
+    q, s, rstd = torch.empty(rows, cols, dtype=Q8, device="cuda"), *(torch.empty(rows, device="cuda") for _ in range(2))
+    arx.arx_rms_norm(x, None, weight=w, q=q, scale=s, rstd=rstd)
+    v = x.double() * rstd.double()[:, None] * w.double()
+    most = v.abs().amax(1) / 448
+    assert bool(((s.double() - most).abs() <= 4 * E * most).all())
+    lo, hi = ((v / s.double()[:, None] * (1 + k * E)).clamp(-448, 448).float().to(Q8).float() for k in (-5, 5))
+    got = q.float()
+    assert bool((got >= torch.minimum(lo, hi)).all()) and bool((got <= torch.maximum(lo, hi)).all())
