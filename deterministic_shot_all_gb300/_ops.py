@@ -651,7 +651,8 @@ Enqueue out = act(x w_gate^T + bias_gate) * (x w_up^T + bias_up) on the tensor c
     w_up [N, K]; the fp32 scales [M], [N], [N] multiply the 8-bit sums.  8-bit operands are on
     rows of 16 bytes.  Biases of out's type or fp32.  ``z_gate`` and ``z_up`` receive the two
     projections for the backward pass.  ``copies`` as in ``arx_linear``, but operands whose rows
-    are off 16 bytes need them (False is an error there).
+    are off 16 bytes need them (False is an error there).  They are made at each call: weights
+    whose K is no multiple of 8 are best kept in a buffer with longer rows, ``buf[:, :K]``.
     """)
 arx_gated_linear_bwd, arx_gated_linear_bwd_plan = _function("arx_gated_linear_bwd", _gated_linear_bwd, """\
 Enqueue dg = dout * u * act'(g), du = dout * act(g) and from them the gradients of ``arx_gated_linear``.

@@ -909,7 +909,9 @@ arx_status arx_linear_bwd(const arx_linear_bwd_args* a, void* stream);
  *   copies  arx_gated_linear_copies_bytes(a) bytes on 16 bytes: 16-bit operands whose
  *           address or leading dimension is off 16 bytes are copied here first.  May be
  *           NULL where that is 0; 8-bit operands have to be on 16 bytes (their
- *           leading dimension a multiple of 16; K may be any)
+ *           leading dimension a multiple of 16; K may be any).  The copies are made anew
+ *           at each call, however few tokens it has: weights that are used again are
+ *           best stored with a leading dimension on 16 bytes, which needs none
  *   status, wait_us  as in arx_linear */
 typedef struct arx_gated_linear_args {
   const void* x;
@@ -938,7 +940,8 @@ arx_status arx_gated_linear(const arx_gated_linear_args* a, void* stream);
  *   dg = dout * u * act'(g),  du = dout * act(g),
  *   dx = dg w_gate + du w_up (one sum),  dw_gate = dg^T x,  dw_up = du^T x,
  *   dbias_gate = sum over rows of dg,  dbias_up = sum over rows of du.
- * dg and du are operands of the products and so rounded to `dtype`; the bias
+ * dg and du are operands of the products and so rounded to `dtype` (in ARX_F16 beyond
+ * 65504 to infinity, and to 0 up to 2^-25: dout has to be scaled to suit); the bias
  * gradients sum them unrounded.
  *   dout, z_gate, z_up  [M, N]; z_gate (g) and z_up (u) from the forward
  *   x, w_gate, w_up     as in the forward; x may be NULL without dw_gate and dw_up, the
