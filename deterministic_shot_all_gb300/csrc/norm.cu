@@ -441,7 +441,8 @@ cudaError_t fwd_any(const arx_layer_norm_args& a, bool vec, cudaStream_t st) {
 // Row chunks of the column-sum kernel for long rows.
 constexpr unsigned kColumnChunks = 64;
 // As many blocks as 152 SMs hold at once: a constant, so that the order of the
-// sums depends on the sizes alone.
+// sums depends on the call alone: sizes, type, alignment, and whether dresidual (an
+// array more in the ring) is there.
 template <int D, int T, int RPC, int NV, int V, int kRing>
 cudaError_t bwd_ring(const arx_layer_norm_bwd_args& a, unsigned* parts, uint32_t slot, size_t smem, cudaStream_t st) {
   size_t per_sm = kRingBytes / (smem + 2048);

@@ -237,7 +237,8 @@ constexpr size_t kRingBytes = 222 * 1024, kBlockRingBytes = 220 * 1024;
 constexpr unsigned kColumnChunks = 64;
 
 // As many blocks as 152 SMs hold at once: a constant, so that the order of the
-// sums depends on the sizes alone.
+// sums depends on the call alone: sizes, type, alignment, and whether dresidual (an
+// array more in the ring) is there.
 template <int D, int T, int RPC, int NV, int V, int kRing>
 cudaError_t ring(const arx_rms_norm_bwd_args& a, unsigned* parts, uint32_t slot, bool res_ring, cudaStream_t st) {
   size_t smem = size_t(kRing) * (res_ring ? 3 : 2) * slot * RPC;

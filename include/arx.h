@@ -554,8 +554,10 @@ arx_status arx_step_noalloc(const void* const* inputs, int W, void* out, size_t 
  *    once (nearest even) where it is stored, except where a call says so.
  *    Infinities and NaN follow the formulas.
  *  - The same call on the same values gives the same bits on every run: sums
- *    are taken in an order that depends on the sizes and the alignment of the
- *    arguments alone (no atomics).
+ *    are taken in an order that depends on the arguments' sizes, types and
+ *    alignment, and on which of the optional ones are given, alone (no atomics).
+ *    (So a norm's y may differ in single roundings with q asked for and without,
+ *    a weight's gradient with dresidual and without.)
  *  - An output may be exactly one of the inputs that a call names (same
  *    address, same leading dimension: each element is read before it is
  *    written); any other overlap of an output with an input, another output
