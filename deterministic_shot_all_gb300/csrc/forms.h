@@ -59,7 +59,7 @@ inline Form choose_form(const GemmCall& c, uint32_t steps, bool p_copy, bool q_c
   // tile 25 a row of Q, 30 to 40 through a cluster; of a wide tile all but the last
   // run under the next one's products, 2800 + 7 a row at the least.
   // Of stacked products, whose contraction is the tokens and whose outputs are the
-  // weights, most of a split block's time is the storing: 60 a row more.  Over 89
+  // weights, most of a split block's time is the storing: 60 a row more.  Over 88
   // sizes, 1 to 7,909 tokens, the forms chosen take 1.04 of the best ones' time in
   // the mean and 1.28 at most, without it 1.15 and 2.27.  Both gradients of
   // [2048, 1024] from 64 tokens: wide 8.2 us, split 14.1 and more; of [96, 2832] from

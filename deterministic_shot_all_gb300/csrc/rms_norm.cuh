@@ -6,7 +6,7 @@
 // stays in its threads' registers between the pass that sums its squares and
 // the pass that uses the sum; the largest |y|, which q's scale needs, is found
 // with the sum (see row_most).  [8192, 4096] bf16 with residual and 32-bit weights
-// 42.2 us, 6.3 TB/s; W = 4 [1024, 8192] 19.7 us, 6.0 TB/s; 32 rows of 4096 2.1 us.
+// 42.9 us, 6.3 TB/s; W = 4 [1024, 8192] 19.7 us, 6.0 TB/s; 32 rows of 4096 2.1 us.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -311,24 +311,19 @@ __global__ void __launch_bounds__(T* RPC) rms_kernel(const __grid_constant__ Rms
 // Many rows of whole aligned units: persistent, the weights in registers and the
 // rows coming in through a ring of kRing rows in shared memory, each thread
 // copying what it reads itself.
-template <int T, int RPC>
-constexpr int kRingBlocks = T * RPC > 512 ? 1 : 2;
-
-template <int D, int T, int RPC, int NV, int kRing>
-__global__ void __launch_bounds__(T* RPC, kRingBlocks<T, RPC>)
-    rms_ring_kernel(const __grid_constant__ RmsArgs<D> a, uint32_t slot) {
+template <int D, int T, int NV, int kRing>
+__global__ void __launch_bounds__(T, 1) rms_ring_kernel(const __grid_constant__ RmsArgs<D> a, uint32_t slot) {
   using S = typename Elem<D>::S;
   constexpr int V = 8;
-  __shared__ float buf[2][RPC][4 * (T / 32)];
-  extern __shared__ __align__(16) uint8_t smem[];  // [RPC][kRing][slots, residual][slot]
+  __shared__ float buf[2][4 * (T / 32)];
+  extern __shared__ __align__(16) uint8_t smem[];  // [kRing][slots, residual][slot]
   dependent_launch_prologue();
-  const uint32_t cols = uint32_t(a.cols), sub = threadIdx.x / T, W = a.W, arrays = W + (a.residual ? 1 : 0);
-  uint8_t* ring = smem + sub * kRing * arrays * slot;
-  const size_t step = size_t(gridDim.x) * RPC;
-  size_t row = size_t(blockIdx.x) * RPC + sub;
+  const uint32_t cols = uint32_t(a.cols), W = a.W, arrays = W + (a.residual ? 1 : 0);
+  const size_t step = gridDim.x;
+  size_t row = blockIdx.x;
   const auto start = [&](size_t r, uint32_t at) {  // one group, empty past the last row
     if (r < a.rows) {
-      uint8_t* dst = ring + at * arrays * slot;
+      uint8_t* dst = smem + at * arrays * slot;
       for (uint32_t w = 0; w < W; ++w) copy_matrix_row<D, T, NV, V>(dst + w * slot, a.slot[w], a.ldx, r, a.rows, cols);
       if (a.residual) copy_matrix_row<D, T, NV, V>(dst + W * slot, a.residual, a.ldresidual, r, a.rows, cols);
     }
@@ -342,7 +337,7 @@ __global__ void __launch_bounds__(T* RPC, kRingBlocks<T, RPC>)
   int parity = 0;
   for (; row < a.rows; row += step) {
     cp_async_wait<kRing - 2>();
-    const uint8_t* base = ring + at * arrays * slot;
+    const uint8_t* base = smem + at * arrays * slot;
     float f[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -365,7 +360,7 @@ __global__ void __launch_bounds__(T* RPC, kRingBlocks<T, RPC>)
     }
     // The slot of the row before, which this thread has read.
     start(row + (kRing - 1) * step, at == 0 ? kRing - 1 : at - 1);
-    finish_row<D, T, RPC, NV, V>(a, row, cols, f, g, buf[parity][sub]);
+    finish_row<D, T, 1, NV, V>(a, row, cols, f, g, buf[parity]);
     parity ^= 1;
     at = at + 1 == kRing ? 0 : at + 1;
   }
@@ -536,25 +531,21 @@ cudaError_t run(const RmsArgs<D>& a, cudaStream_t st) {
   return launch_op(rms_kernel<D, W, T, RPC, NV, V>, dim3(unsigned((a.rows + RPC - 1) / RPC)), T * RPC, 0, st, a);
 }
 
-// Shared memory of an SM that its blocks' rings may fill, and of one block.
-constexpr size_t kRingBytes = 222 * 1024, kBlockRingBytes = 220 * 1024;
+// Shared memory that a block's ring may fill; one block fits an SM.
+constexpr size_t kBlockRingBytes = 220 * 1024;
 constexpr unsigned kSms = 152;
 
 // Four rows in the ring, two where four are too large; *done is false where two
 // are as well.
-template <int D, int T, int RPC, int NV>
+template <int D, int T, int NV>
 cudaError_t run_ring(const RmsArgs<D>& a, bool* done, cudaStream_t st) {
-  const size_t row = size_t(row_slot(a.cols, sizeof(typename Elem<D>::S), 8)) * (a.W + (a.residual ? 1 : 0)) * RPC;
+  const size_t row = size_t(row_slot(a.cols, sizeof(typename Elem<D>::S), 8)) * (a.W + (a.residual ? 1 : 0));
   const auto with = [&](auto rows) {
     constexpr int kRing = decltype(rows)::value;
-    const size_t smem = kRing * row;
-    size_t per_sm = kRingBytes / (smem + 2048);
-    if (per_sm > kRingBlocks<T, RPC>) per_sm = kRingBlocks<T, RPC>;
-    const uint64_t need = (a.rows + RPC - 1) / RPC, most = per_sm * kSms;
-    constexpr auto kernel = rms_ring_kernel<D, T, RPC, NV, kRing>;
+    constexpr auto kernel = rms_ring_kernel<D, T, NV, kRing>;
     const cudaError_t e = allow_dynamic_smem<kernel>(kBlockRingBytes);
     if (e != cudaSuccess) return e;
-    return launch_op(kernel, dim3(unsigned(need < most ? need : most)), T * RPC, smem, st, a,
+    return launch_op(kernel, dim3(unsigned(a.rows < kSms ? a.rows : kSms)), T, kRing * row, st, a,
                      row_slot(a.cols, sizeof(typename Elem<D>::S), 8));
   };
   *done = true;
@@ -565,18 +556,20 @@ cudaError_t run_ring(const RmsArgs<D>& a, bool* done, cudaStream_t st) {
 }
 
 // One block to a row or the ring?  Measured, GPU time in microseconds (16-bit rows
-// with residual and y, 32-bit weights; one row to a block, then the ring):
+// with residual, h and y, 32-bit weights; one row to a block, then the ring):
 //   aligned        152 rows       608          2,432        8,192
-//   2048 columns   1.7  2.1     3.0  3.0     8.1  8.7    23.5  22.4
-//   4096           2.0  2.2     4.5  4.5    16.1 15.3    46.7  43.8
-//   5120           2.3  2.4     5.0  6.0    21.8 20.7
-//   8192           3.0  3.3     9.0 10.4    33.0 31.4
-//   12288          3.7  4.3    17.2 14.6    64.3 45.6
-// 32-bit rows of 4096 columns and more gain 9 to 13 % from 2,432 rows on; sums of 3
-// and 4 ranks above 4096 columns 5 to 11 %, at 4096 none (4 ranks, 1,024 rows of 8192:
-// 22.4 against 19.1); with q, whose largest |y|
-// takes issue slots, the ring costs 1 to 14 %.  Rows off 16 bytes, read element
-// by element, took 1.1 to 2 times as long through it.
+//   2048 columns   1.6  2.0     2.4  3.0     7.5  9.3    21.9  25.2
+//   4096           2.0  2.2     3.5  4.2    14.6 14.7    42.6  42.0
+//   5120           2.2  2.4     5.2  5.6    18.2 19.7    55.0  60.1
+//   8192           2.7  2.9     8.8  9.5    32.6 29.0     104    90
+//   12288          3.5  3.5    16.9 12.9    63.8 37.4     209   118
+// The ring by the one row's time: 2500 to 5120 columns, 1,216 rows and more, fp16
+// and 32 bits 1.0 to 1.25, bf16 .98 to 1.3; 5121 to 8192, 2,432 rows and more, 16 bits
+// .86 to .97 with a residual and .95 to 1.06 without, 32 bits 1.07 to 1.17 and .91 to
+// .95; sums of 3 and 4 ranks .86 to 1.0 from 1,216 rows on (4 ranks, 1,024 rows of 8192:
+// 22.4 against 19.1), at 4096 columns 1.0; with q, whose largest |y| takes issue slots,
+// 1.12 and more, but above 8192 columns .6 to .85 with it and without.  Rows off 16
+// bytes, read element by element, took 1.1 to 2 times as long through it.
 // The threads to a row: 640 up to 5120 columns (1024: 2,432 rows of 5120, 34.7 us
 // against 21.8); above, 512 with two units each (1024: 41.7 against 33.0 at 8192,
 // 152 rows alike), but 1024 for 32-bit rows (31.3 against 45.8 us).  A warp to rows
@@ -593,29 +586,23 @@ template <int D, int W>
 cudaError_t run_w(const RmsArgs<D>& a, bool vec, cudaStream_t st) {
   const uint64_t n = a.cols;
   if (vec) {
-    const bool ring = a.rows >= 16 * kSms && !a.q;
     bool done = false;
     cudaError_t e = cudaSuccess;
     if (n <= 256) return run<D, W, 32, 4, 1, 8>(a, st);
     if (n <= 512 && a.rows > 8 * kSms) return run<D, W, 32, 4, 2, 8>(a, st);
     if (n <= 1024) return run<D, W, 128, 1, 1, 8>(a, st);
     if (n <= 2048) return run<D, W, 256, 1, 1, 8>(a, st);
-    if (n <= 4096) {
-      if (ring && W <= 2) e = run_ring<D, 512, 1, 1>(a, &done, st);
-      return e != cudaSuccess || done ? e : run<D, W, 512, 1, 1, 8>(a, st);
-    }
-    if (n <= 5120) {
-      if (ring && W <= 4) e = run_ring<D, 640, 1, 1>(a, &done, st);
-      return e != cudaSuccess || done ? e : run<D, W, 640, 1, 1, 8>(a, st);
-    }
+    if (n <= 4096) return run<D, W, 512, 1, 1, 8>(a, st);
+    if (n <= 5120) return run<D, W, 640, 1, 1, 8>(a, st);
     if (n <= 8192) {
-      if ((W > 2 ? a.rows >= 5 * kSms && !a.q : ring) && W <= 4) e = run_ring<D, 1024, 1, 1>(a, &done, st);
+      const bool ring = !a.q && !(D == ARX_F32 && a.residual) && a.rows >= (W > 2 ? 5 : 16) * kSms;
+      if (ring && W <= 4) e = run_ring<D, 1024, 1>(a, &done, st);
       if (e != cudaSuccess || done) return e;
       if constexpr (D == ARX_F32) return run<D, W, 1024, 1, 1, 8>(a, st);
       return run<D, W, 512, 1, 2, 8>(a, st);
     }
     if (n <= 16384) {
-      if (a.rows > 2 * kSms && W <= 2) e = run_ring<D, 1024, 1, 2>(a, &done, st);
+      if (a.rows > 2 * kSms && W <= 2) e = run_ring<D, 1024, 2>(a, &done, st);
       if (e != cudaSuccess || done) return e;
       if constexpr (W > 2) return run<D, W, 1024, 1, 2, 8>(a, st);
       return run<D, W, 512, 1, 4, 8>(a, st);
